@@ -1,0 +1,207 @@
+// api_layer.cu -- C ABI of the operators around the matmuls (declared in
+// include/uw.h): routing, grouping of rows, low-rank adapters.  Checks of the
+// arguments; the kernels are in route.cu and lora.cu.
+#include <cmath>
+
+#include "kernels.h"
+
+namespace uw {
+namespace {
+
+inline bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+inline uw_status cuda_status(cudaError_t e) { return e == cudaSuccess ? UW_OK : UW_ERR_CUDA; }
+inline uint64_t up256(uint64_t x) { return (x + 255u) / 256u * 256u; }
+
+constexpr int64_t kMaxItems = (int64_t(1) << 31) - 1;
+
+uw_status check_router(const uw_router *r, int64_t t) {
+    if (!r || t < 0) return UW_ERR_INVALID_ARG;
+    if (r->experts < 1 || r->experts > UW_MAX_GROUPS || r->top_k < 1 || r->top_k > UW_MAX_TOP_K) return UW_ERR_INVALID_ARG;
+    if (r->n_groups < 1 || r->n_groups > 32 || r->experts % r->n_groups) return UW_ERR_INVALID_ARG;
+    if (r->top_groups < 1 || r->top_groups > r->n_groups) return UW_ERR_INVALID_ARG;
+    if (r->top_k > r->top_groups * (r->experts / r->n_groups)) return UW_ERR_INVALID_ARG;
+    if (r->score != UW_SCORE_SOFTMAX && r->score != UW_SCORE_SIGMOID) return UW_ERR_INVALID_ARG;
+    if (r->group_score != UW_GROUP_MAX && r->group_score != UW_GROUP_TOP2) return UW_ERR_INVALID_ARG;
+    if (r->logits_type != UW_TYPE_F32 && r->logits_type != UW_TYPE_BF16) return UW_ERR_INVALID_ARG;
+    if (!std::isfinite(r->scale)) return UW_ERR_INVALID_ARG;
+    if (t > kMaxItems / r->top_k) return UW_ERR_UNSUPPORTED_SHAPE;
+    return UW_OK;
+}
+
+uw_status check_groups(int64_t rows, int32_t per_row, int32_t groups) {
+    if (rows < 0 || per_row < 1 || per_row > 64 || groups < 1 || groups > UW_MAX_GROUPS) return UW_ERR_INVALID_ARG;
+    if (rows > kMaxItems / per_row) return UW_ERR_UNSUPPORTED_SHAPE;
+    return UW_OK;
+}
+
+uw_status check_adapters(const uw_adapters *a, int64_t t) {
+    if (!a || t < 0 || a->n <= 0 || a->k <= 0) return UW_ERR_INVALID_ARG;
+    if (a->n % 64 || a->k % 64 || a->n > kMaxItems || a->k > kMaxItems) return UW_ERR_UNSUPPORTED_SHAPE;
+    if (a->count < 1 || a->count > UW_MAX_GROUPS) return UW_ERR_INVALID_ARG;
+    if (a->max_rank < 8 || a->max_rank > 256 || a->max_rank % 8) return UW_ERR_INVALID_ARG;
+    if (t > kMaxItems) return UW_ERR_UNSUPPORTED_SHAPE;
+    const LoraGeometry g = lora_geometry(t, a->k, a->count, a->max_rank);
+    if (g.splits > 65535) return UW_ERR_UNSUPPORTED_SHAPE;   // K slices are a grid dimension
+    return UW_OK;
+}
+
+// uw_lora_add's own grouping: offsets, order and the sort's workspace, then V
+struct LoraWorkspace {
+    uint64_t order_off, sort_off, v_off, bytes;
+};
+LoraWorkspace lora_workspace(int64_t t, const uw_adapters *a) {
+    LoraWorkspace w;
+    w.order_off = up256(uint64_t(a->count + 1) * 4);
+    w.sort_off = w.order_off + up256(uint64_t(t) * 4);
+    w.v_off = w.sort_off + group_geometry(t, 1, a->count).bytes;
+    w.bytes = w.v_off + lora_geometry(t, a->k, a->count, a->max_rank).v_bytes;
+    return w;
+}
+
+}  // namespace
+}  // namespace uw
+
+using namespace uw;
+
+extern "C" uw_status uw_route_workspace_size(int64_t t, const uw_router *router, size_t *bytes) {
+    if (!bytes) return UW_ERR_INVALID_ARG;
+    const uw_status st = check_router(router, t);
+    if (st != UW_OK) return st;
+    *bytes = size_t(route_geometry(t, router->top_k, router->experts).bytes);
+    return UW_OK;
+}
+
+extern "C" uw_status uw_route_experts(const void *logits_dev, int64_t t, int64_t row_stride, const float *bias_dev,
+                                      const uw_router *router, int32_t *ids_dev, float *weights_dev,
+                                      int32_t *offsets_dev, int32_t *order_dev, int32_t *slot_dev, void *ws,
+                                      size_t ws_bytes, void *stream) {
+    const uw_status st = check_router(router, t);
+    if (st != UW_OK) return st;
+    if (!offsets_dev || (t > 0 && (!logits_dev || !ids_dev || !weights_dev || !order_dev || !slot_dev)))
+        return UW_ERR_INVALID_ARG;
+    if (row_stride < router->experts) return UW_ERR_INVALID_ARG;
+    if (!aligned(logits_dev, router->logits_type == UW_TYPE_BF16 ? 2 : 4) || !aligned(bias_dev, 4) ||
+        !aligned(ids_dev, 4) || !aligned(weights_dev, 4) || !aligned(offsets_dev, 4) || !aligned(order_dev, 4) ||
+        !aligned(slot_dev, 4))
+        return UW_ERR_INVALID_ARG;
+    const uint64_t need = route_geometry(t, router->top_k, router->experts).bytes;
+    if (need && (!ws || ws_bytes < need || !aligned(ws, 256))) return UW_ERR_WORKSPACE;
+    RouteLaunch p{};
+    p.logits = logits_dev;
+    p.t = t;
+    p.stride = row_stride;
+    p.bias = bias_dev;
+    p.router = router;
+    p.ids = ids_dev;
+    p.weights = weights_dev;
+    p.offsets = offsets_dev;
+    p.order = order_dev;
+    p.slot = slot_dev;
+    p.ws = ws;
+    return cuda_status(launch_route(p, static_cast<cudaStream_t>(stream)));
+}
+
+extern "C" uw_status uw_group_workspace_size(int64_t rows, int32_t per_row, int32_t groups, size_t *bytes) {
+    if (!bytes) return UW_ERR_INVALID_ARG;
+    const uw_status st = check_groups(rows, per_row, groups);
+    if (st != UW_OK) return st;
+    *bytes = size_t(group_geometry(rows, per_row, groups).bytes);
+    return UW_OK;
+}
+
+extern "C" uw_status uw_group_rows(const int32_t *ids_dev, int64_t rows, int32_t per_row, int32_t groups,
+                                   int32_t *offsets_dev, int32_t *order_dev, int32_t *slot_dev, void *ws,
+                                   size_t ws_bytes, void *stream) {
+    const uw_status st = check_groups(rows, per_row, groups);
+    if (st != UW_OK) return st;
+    if (!offsets_dev || (rows > 0 && (!ids_dev || !order_dev))) return UW_ERR_INVALID_ARG;
+    if (!aligned(ids_dev, 4) || !aligned(offsets_dev, 4) || !aligned(order_dev, 4) || !aligned(slot_dev, 4))
+        return UW_ERR_INVALID_ARG;
+    const uint64_t need = group_geometry(rows, per_row, groups).bytes;
+    if (need && (!ws || ws_bytes < need || !aligned(ws, 256))) return UW_ERR_WORKSPACE;
+    GroupLaunch p{};
+    p.ids = ids_dev;
+    p.rows = rows;
+    p.per_row = per_row;
+    p.groups = groups;
+    p.offsets = offsets_dev;
+    p.order = order_dev;
+    p.slot = slot_dev;
+    p.ws = ws;
+    return cuda_status(launch_group_rows(p, static_cast<cudaStream_t>(stream)));
+}
+
+extern "C" uw_status uw_lora_workspace_size(int64_t t, const uw_adapters *adapters, size_t *bytes) {
+    if (!bytes) return UW_ERR_INVALID_ARG;
+    const uw_status st = check_adapters(adapters, t);
+    if (st != UW_OK) return st;
+    *bytes = t ? size_t(lora_workspace(t, adapters).bytes) : 0;
+    return UW_OK;
+}
+
+extern "C" uw_status uw_lora_add(const uint16_t *x_dev, int64_t x_stride, int64_t t, const uw_adapters *adapters,
+                                 const int32_t *ids_dev, const int32_t *offsets_dev, const int32_t *order_dev,
+                                 const float *y_dev, int64_t y_stride, float *out_dev, int64_t out_stride, void *ws,
+                                 size_t ws_bytes, void *stream) {
+    const uw_status st = check_adapters(adapters, t);
+    if (st != UW_OK) return st;
+    const uw_adapters &d = *adapters;
+    if (x_stride < d.k || x_stride % 8 || y_stride < d.n || y_stride % 4 || out_stride < d.n || out_stride % 4)
+        return UW_ERR_INVALID_ARG;
+    if (t == 0) return UW_OK;
+    if (!x_dev || !y_dev || !out_dev || !d.a_dev || !d.b_dev) return UW_ERR_INVALID_ARG;
+    if (!ids_dev && (!offsets_dev || !order_dev)) return UW_ERR_INVALID_ARG;
+    if (!aligned(x_dev, 16) || !aligned(y_dev, 16) || !aligned(out_dev, 16) || !aligned(d.a_dev, 16) ||
+        !aligned(d.b_dev, 16) || !aligned(d.ranks_dev, 4) || !aligned(d.scales_dev, 4) || !aligned(ids_dev, 4) ||
+        !aligned(offsets_dev, 4) || !aligned(order_dev, 4))
+        return UW_ERR_INVALID_ARG;
+    if (out_dev == y_dev) {
+        if (out_stride != y_stride) return UW_ERR_INVALID_ARG;
+    } else {
+        const uintptr_t y0 = reinterpret_cast<uintptr_t>(y_dev), o0 = reinterpret_cast<uintptr_t>(out_dev);
+        const uintptr_t y1 = y0 + uintptr_t((t - 1) * y_stride + d.n) * 4, o1 = o0 + uintptr_t((t - 1) * out_stride + d.n) * 4;
+        // column ranges of one buffer (equal strides) may lie side by side
+        const bool apart = y1 <= o0 || o1 <= y0;
+        const uintptr_t gap = (o0 > y0 ? o0 - y0 : y0 - o0) / 4 % uintptr_t(y_stride);
+        const bool columns = y_stride == out_stride && gap >= uintptr_t(d.n) && gap + uintptr_t(d.n) <= uintptr_t(y_stride);
+        if (!apart && !columns) return UW_ERR_INVALID_ARG;
+    }
+    const LoraWorkspace w = lora_workspace(t, adapters);
+    if (!ws || ws_bytes < w.bytes || !aligned(ws, 256)) return UW_ERR_WORKSPACE;
+    uint8_t *base = static_cast<uint8_t *>(ws);
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (ids_dev) {
+        GroupLaunch g{};
+        g.ids = ids_dev;
+        g.rows = t;
+        g.per_row = 1;
+        g.groups = d.count;
+        g.offsets = reinterpret_cast<int32_t *>(base);
+        g.order = reinterpret_cast<int32_t *>(base + w.order_off);
+        g.ws = base + w.sort_off;
+        const cudaError_t err = launch_group_rows(g, s);
+        if (err != cudaSuccess) return UW_ERR_CUDA;
+        offsets_dev = g.offsets;
+        order_dev = g.order;
+    }
+    LoraLaunch p{};
+    p.x = x_dev;
+    p.x_stride = x_stride;
+    p.t = t;
+    p.k = d.k;
+    p.n = d.n;
+    p.a = d.a_dev;
+    p.b = d.b_dev;
+    p.groups = d.count;
+    p.max_rank = d.max_rank;
+    p.ranks = d.ranks_dev;
+    p.scales = d.scales_dev;
+    p.offsets = offsets_dev;
+    p.order = order_dev;
+    p.y = y_dev;
+    p.y_stride = y_stride;
+    p.out = out_dev;
+    p.out_stride = out_stride;
+    p.v = reinterpret_cast<float *>(base + w.v_off);
+    return cuda_status(launch_lora(p, s));
+}

@@ -205,6 +205,63 @@ uw_status matmul_bf16_ex(const uint16_t *x_dev, int64_t m, const uint16_t *w_dev
                          const uw_plan *plan, void *ws, size_t ws_bytes, uint32_t *dev_status, uint32_t *sk_counters,
                          cudaStream_t s);
 
+// Grouping of rows by an index (route.cu): `items` = rows * per_row ids in a
+// stable counting sort.  Calls of one block need no workspace.
+struct GroupGeometry {
+    int blocks = 1;
+    int64_t rows_per_block = 1;
+    uint64_t bytes = 0;        // per-block counts (0: one block)
+};
+GroupGeometry group_geometry(int64_t rows, int per_row, int groups);
+GroupGeometry route_geometry(int64_t t, int top_k, int experts);
+struct GroupLaunch {
+    const int32_t *ids;
+    int64_t rows;
+    int per_row, groups;
+    int32_t *offsets, *order, *slot;   // slot may be null
+    void *ws;
+};
+cudaError_t launch_group_rows(const GroupLaunch &p, cudaStream_t stream);
+
+// Routing of t tokens to experts (route.cu); counts in `ws`.
+struct RouteLaunch {
+    const void *logits;
+    int64_t t, stride;
+    const float *bias;
+    const uw_router *router;
+    int32_t *ids;
+    float *weights;
+    int32_t *offsets, *order, *slot;
+    void *ws;
+};
+cudaError_t launch_route(const RouteLaunch &p, cudaStream_t stream);
+
+// Low-rank adapters beside a projection (lora.cu): out = y + scale * B (A x)
+// per row of an adapter's group.  v: [splits][t][max_rank] floats.
+struct LoraGeometry {
+    int splits = 1;            // slices of K
+    int token_tiles = 1;       // 8-token tiles of the first product's tile: 1 or 4
+    int rank_tiles = 1;        // 16-rank tiles per CTA of the first product: 1 or 2
+    int64_t shrink_tiles = 0, expand_tiles = 0;   // most row tiles there can be
+    uint64_t v_bytes = 0;
+};
+LoraGeometry lora_geometry(int64_t t, int64_t k, int groups, int max_rank);
+struct LoraLaunch {
+    const uint16_t *x;
+    int64_t x_stride, t, k, n;
+    const uint16_t *a, *b;     // [groups][max_rank][k], [groups][n][max_rank]
+    int groups, max_rank;
+    const int32_t *ranks;      // may be null
+    const float *scales;       // may be null
+    const int32_t *offsets, *order;
+    const float *y;
+    int64_t y_stride;
+    float *out;
+    int64_t out_stride;
+    float *v;
+};
+cudaError_t launch_lora(const LoraLaunch &p, cudaStream_t stream);
+
 // Fixed-order sum of split-K partials: y[i] = sum_s partial[s][i], s ascending.
 cudaError_t launch_splitk_reduce(const float *partial, int split_k, int64_t count, float *y,
                                  cudaStream_t stream);

@@ -1,0 +1,456 @@
+// lora.cu -- low-rank adapters of many requests beside a shared projection:
+//   out[i] = y[i] + scale_a * B_a (A_a x[i]),   a = the adapter of row i,
+// with A_a [rank, k] and B_a [n, rank] in BF16, x in BF16 and y, out in FP32 (y
+// is what the projection's matmul wrote).  Rows without an adapter pass
+// through.
+//
+// Rows come grouped by adapter (offsets and order of a stable counting sort),
+// so a tile of rows reads one adapter's matrices.  Two launches: the inner
+// product over all of K must be complete before the outer one starts.
+//
+// First product, V = A x: warp-level MMA (m16n8k16) with the ranks as M and the
+// tokens as N.  Both operands are K-contiguous, so every lane loads 32
+// consecutive bytes of its rows straight into fragment order (the K slots of
+// the MMA are permuted alike for both) with no shared-memory staging.  K is
+// split over the CTA's eight warps and over `splits` CTAs; the pieces are
+// added in a fixed order in the second kernel.  The tensor core truncates when
+// it accumulates (measured: about 1.1e-9 per unit of K, relative, biased
+// towards zero), so no chain is longer than 512 of K.
+//
+// Second product, out = y + V B^T: tokens are M, output columns N.  V keeps its
+// 32 bits: it is split into three BF16 parts (8 + 8 + 8 bits of mantissa), whose
+// products with B are exact in the MMA.  A warp takes 16 rows x 32 columns; the
+// four MMA column tiles interleave so that a thread owns eight consecutive
+// columns and reads y and writes out in 16-byte pieces.
+//
+// Bound: for many rows, the bytes of y and out (8 t n); for one token per
+// request, the adapters' bytes, which the many small tiles keep in flight.
+// The second kernel is launched early: its tile search and its first loads of
+// B and y overlap the first kernel.
+#include <algorithm>
+
+#include "device_common.cuh"
+#include "kernels.h"
+
+namespace uw {
+namespace {
+
+using namespace dev;
+
+constexpr uint32_t kAll = 0xFFFFFFFFu;
+constexpr int kShrinkWarps = 8;
+constexpr int kExpandWarps = 4;
+constexpr int kTileM = 16;                // rows per tile of the second product
+
+struct LoraArgs {
+    const uint16_t *x;
+    int64_t x_stride, t, k, n;
+    const uint16_t *a, *b;
+    int groups, max_rank;
+    const int32_t *ranks;
+    const float *scales;
+    const int32_t *offsets, *order;
+    float *v;
+    int splits;
+    const float *y;
+    int64_t y_stride;
+    float *out;
+    int64_t out_stride;
+    int copy_rest;             // rows without an adapter are copied (out is not y)
+    int steps;                 // second product: 32-column steps per warp
+};
+
+struct Tile {
+    int group;                 // -1: there is no such tile
+    int pos;                   // first row, as a place in `order`
+    int rows;
+};
+
+// The tile-th tile of at most `size` rows, found by one warp from the groups'
+// offsets (clamped to [0, t], so that no offsets lead out of bounds).
+__device__ __forceinline__ Tile find_tile(const LoraArgs &a, int size, int64_t tile, bool rest) {
+    const int lane = threadIdx.x & 31;
+    const int t = int(a.t);
+    int64_t run = 0;
+    for (int g0 = 0; g0 <= a.groups; g0 += 32) {
+        const int g = g0 + lane;
+        int lo = 0, cnt = 0;
+        if (g <= a.groups) {
+            lo = min(max(__ldg(a.offsets + g), 0), t);
+            const int hi = g < a.groups ? min(max(__ldg(a.offsets + g + 1), 0), t) : (rest ? t : lo);
+            cnt = max(hi - lo, 0);
+        }
+        const int tiles = (cnt + size - 1) / size;
+        int incl = tiles;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int u = __shfl_up_sync(kAll, incl, d);
+            if (lane >= d) incl += u;
+        }
+        const int total = __shfl_sync(kAll, incl, 31);
+        if (tile < run + total) {
+            const int src = __ffs(__ballot_sync(kAll, run + incl > tile)) - 1;
+            Tile r;
+            const int skip = int(tile - run) - (__shfl_sync(kAll, incl, src) - __shfl_sync(kAll, tiles, src));
+            r.group = g0 + src;
+            r.pos = __shfl_sync(kAll, lo, src) + skip * size;
+            r.rows = min(size, __shfl_sync(kAll, cnt, src) - skip * size);
+            return r;
+        }
+        run += total;
+    }
+    return Tile{-1, 0, 0};
+}
+
+__device__ __forceinline__ int rank_of(const LoraArgs &a, int group) {
+    if (group >= a.groups) return 0;
+    return a.ranks ? min(max(__ldg(a.ranks + group), 0), a.max_rank) : a.max_rank;
+}
+
+__device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                          uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 "
+        "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// ---------------------------------------------------------------- V = A x
+
+// RT: 16-rank tiles, NT: 8-token tiles per CTA.  Grid: row tile, K slice, rank part.
+template <int RT, int NT>
+__global__ void __launch_bounds__(kShrinkWarps * 32) k_lora_shrink(const LoraArgs a) {
+    __shared__ Tile s_tile;
+    __shared__ float red[kShrinkWarps][RT * NT * 4][32];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+    pdl_trigger();
+    if (warp == 0) {
+        const Tile f = find_tile(a, 8 * NT, blockIdx.x, false);
+        if (lane == 0) s_tile = f;
+    }
+    __syncthreads();
+    const Tile tile = s_tile;
+    if (tile.group < 0) return;
+    const int rank = rank_of(a, tile.group), r0 = int(blockIdx.z) * RT * 16;
+    if (r0 >= rank) return;
+
+    const int64_t steps = a.k / 64;
+    const int64_t c0 = steps * blockIdx.y / a.splits, c1 = steps * (blockIdx.y + 1) / a.splits;
+    const int64_t k0 = c0 + (c1 - c0) * warp / kShrinkWarps, k1 = c0 + (c1 - c0) * (warp + 1) / kShrinkWarps;
+    // this lane's rows of A (rows past the adapter's storage repeat its last) and of x
+    const uint16_t *pa[RT][2];
+    const uint16_t *px[NT];
+#pragma unroll
+    for (int i = 0; i < RT; i++)
+#pragma unroll
+        for (int h = 0; h < 2; h++) {
+            const int r = min(r0 + 16 * i + 8 * h + g, a.max_rank - 1);
+            pa[i][h] = a.a + (int64_t(tile.group) * a.max_rank + r) * a.k + k0 * 64 + 16 * c;
+        }
+#pragma unroll
+    for (int i = 0; i < NT; i++) {
+        const int row = min(max(__ldg(a.order + tile.pos + min(8 * i + g, tile.rows - 1)), 0), int(a.t) - 1);
+        px[i] = a.x + row * a.x_stride + k0 * 64 + 16 * c;
+    }
+    float d[RT][NT][4];
+#pragma unroll
+    for (int i = 0; i < RT; i++)
+#pragma unroll
+        for (int j = 0; j < NT; j++)
+#pragma unroll
+            for (int q = 0; q < 4; q++) d[i][j][q] = 0.f;
+#pragma unroll 2
+    for (int64_t s = k0; s < k1; s++) {
+        uint4 wa[RT][2][2], xv[NT][2];
+#pragma unroll
+        for (int i = 0; i < RT; i++)
+#pragma unroll
+            for (int h = 0; h < 2; h++) {
+                const uint4 *p = reinterpret_cast<const uint4 *>(pa[i][h]);
+                wa[i][h][0] = __ldg(p);
+                wa[i][h][1] = __ldg(p + 1);
+                pa[i][h] += 64;
+            }
+#pragma unroll
+        for (int i = 0; i < NT; i++) {
+            const uint4 *p = reinterpret_cast<const uint4 *>(px[i]);
+            xv[i][0] = __ldg(p);
+            xv[i][1] = __ldg(p + 1);
+            px[i] += 64;
+        }
+#pragma unroll
+        for (int i = 0; i < RT; i++)
+#pragma unroll
+            for (int j = 0; j < NT; j++)
+#pragma unroll
+                for (int h = 0; h < 2; h++) {
+                    mma_16816(d[i][j], wa[i][0][h].x, wa[i][1][h].x, wa[i][0][h].y, wa[i][1][h].y, xv[j][h].x, xv[j][h].y);
+                    mma_16816(d[i][j], wa[i][0][h].z, wa[i][1][h].z, wa[i][0][h].w, wa[i][1][h].w, xv[j][h].z, xv[j][h].w);
+                }
+    }
+#pragma unroll
+    for (int i = 0; i < RT; i++)
+#pragma unroll
+        for (int j = 0; j < NT; j++)
+#pragma unroll
+            for (int q = 0; q < 4; q++) red[warp][(i * NT + j) * 4 + q][lane] = d[i][j][q];
+    __syncthreads();
+    for (int u = threadIdx.x; u < RT * NT * 128; u += kShrinkWarps * 32) {
+        const int l = u & 31, f = u >> 5, q = f & 3, j = (f >> 2) % NT, i = (f >> 2) / NT;
+        float sum = red[0][f][l];
+#pragma unroll
+        for (int w = 1; w < kShrinkWarps; w++) sum += red[w][f][l];
+        // element q of lane l: rank l / 4 (+ 8), token 2 (l % 4) (+ 1)
+        const int r = r0 + 16 * i + (l >> 2) + (q >= 2 ? 8 : 0);
+        const int tok = 8 * j + 2 * (l & 3) + (q & 1);
+        if (tok < tile.rows && r < a.max_rank)
+            a.v[(int64_t(blockIdx.y) * a.t + tile.pos + tok) * a.max_rank + r] = sum;
+    }
+}
+
+// ---------------------------------------------------------------- out = y + V B^T
+
+__device__ __forceinline__ uint32_t bf16_bits(float f) {   // round to nearest even; f is finite or inf
+    uint32_t o;
+    asm("{ .reg .b16 h; cvt.rn.bf16.f32 h, %1; cvt.u32.u16 %0, h; }" : "=r"(o) : "f"(f));
+    return o;
+}
+
+// v = p[0] + p[1] + p[2] up to 2^-24 of v, each a BF16
+__device__ __forceinline__ void split3(float v, uint32_t (&p)[3]) {
+    p[0] = bf16_bits(v);
+    const float h = __uint_as_float(p[0] << 16);
+    if (!(fabsf(h) <= 3.402823466e38f)) {     // inf or NaN: there is no remainder
+        p[1] = p[2] = 0u;
+        return;
+    }
+    p[1] = bf16_bits(v - h);
+    p[2] = bf16_bits((v - h) - __uint_as_float(p[1] << 16));
+}
+
+// C: 16-rank chunks whose B loads are in flight together.  Dynamic shared
+// memory: fragments of V, [chunk][part][lane] uint4.
+template <int C>
+__global__ void __launch_bounds__(kExpandWarps * 32) k_lora_expand(const LoraArgs a) {
+    extern __shared__ uint4 s_frag[];
+    __shared__ Tile s_tile;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+    if (warp == 0) {
+        const Tile f = find_tile(a, kTileM, blockIdx.x, a.copy_rest != 0);
+        if (lane == 0) s_tile = f;
+    }
+    __syncthreads();
+    const Tile tile = s_tile;
+    if (tile.group < 0) return;
+    const int rank = rank_of(a, tile.group);
+    if (rank == 0 && !a.copy_rest) return;
+    const int chunks = (rank + 15) / 16;
+
+    // this thread's two rows of y and out
+    int64_t row[2];
+    bool live[2];
+#pragma unroll
+    for (int h = 0; h < 2; h++) {
+        live[h] = g + 8 * h < tile.rows;
+        row[h] = live[h] ? __ldg(a.order + tile.pos + g + 8 * h) : 0;
+        live[h] = live[h] && row[h] >= 0 && row[h] < a.t;
+    }
+    const int64_t n0 = (int64_t(blockIdx.y) * kExpandWarps + warp) * a.steps * 32;
+    const int steps = int(max(int64_t(0), min(int64_t(a.steps), (a.n - n0) / 32)));
+    // column tile q, MMA column j is output column 8 (j / 2) + 2 q + j % 2 of the step's 32
+    const uint16_t *pb = a.b + (int64_t(min(tile.group, a.groups - 1)) * a.n + n0 + 8 * (g >> 1) + (g & 1)) * a.max_rank + 4 * c;
+    const float *py[2] = {a.y + row[0] * a.y_stride + n0 + 8 * c, a.y + row[1] * a.y_stride + n0 + 8 * c};
+    float *po[2] = {a.out + row[0] * a.out_stride + n0 + 8 * c, a.out + row[1] * a.out_stride + n0 + 8 * c};
+
+    // B of chunks [j0, j0 + C) for the step at column offset `n`; ranks past the
+    // adapter's are zeroed, whatever its storage holds there
+    auto load_b = [&](uint2 (&w)[C][4], int64_t n, int j0) {
+#pragma unroll
+        for (int j = 0; j < C; j++) {
+            const int r = 16 * (j0 + j) + 4 * c;
+#pragma unroll
+            for (int q = 0; q < 4; q++) {
+                w[j][q] = make_uint2(0u, 0u);
+                if (r < rank) {
+                    w[j][q] = __ldg(reinterpret_cast<const uint2 *>(pb + (n + 2 * q) * a.max_rank + 16 * (j0 + j)));
+                    if (r + 4 > rank) {
+                        const int left = rank - r;     // 1, 2 or 3 ranks
+                        if (left < 2) w[j][q].x &= 0xFFFFu;
+                        w[j][q].y = left < 3 ? 0u : w[j][q].y & 0xFFFFu;
+                    }
+                }
+            }
+        }
+    };
+    auto load_y = [&](float4 (&v)[2][2], int64_t n) {
+#pragma unroll
+        for (int h = 0; h < 2; h++) {
+            v[h][0] = v[h][1] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (live[h]) {
+                v[h][0] = *reinterpret_cast<const float4 *>(py[h] + n);
+                v[h][1] = *reinterpret_cast<const float4 *>(py[h] + n + 4);
+            }
+        }
+    };
+    uint2 w[C][4];
+    float4 yv[2][2];
+    if (steps > 0) {
+        load_b(w, 0, 0);
+        load_y(yv, 0);
+    }
+
+    pdl_wait();   // V is the previous kernel's; everything read so far is older
+    // fragments: lane (g, c) holds ranks 16 j + 4 c .. + 3 of rows g and g + 8
+    const float scale = a.scales && rank ? __ldg(a.scales + tile.group) : 1.f;
+    for (int u = threadIdx.x; u < chunks * 32; u += kExpandWarps * 32) {
+        const int j = u >> 5, l = u & 31, r = 16 * j + 4 * (l & 3);
+        uint32_t part[3][4];
+#pragma unroll
+        for (int h = 0; h < 2; h++) {
+            const int m = (l >> 2) + 8 * h;
+            float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (m < tile.rows && r < rank) {
+                const float *pv = a.v + int64_t(tile.pos + m) * a.max_rank + r;
+                s = __ldcg(reinterpret_cast<const float4 *>(pv));
+                for (int z = 1; z < a.splits; z++) {
+                    const float4 o = __ldcg(reinterpret_cast<const float4 *>(pv + int64_t(z) * a.t * a.max_rank));
+                    s.x += o.x;
+                    s.y += o.y;
+                    s.z += o.z;
+                    s.w += o.w;
+                }
+            }
+            const float v[4] = {s.x * scale, r + 1 < rank ? s.y * scale : 0.f, r + 2 < rank ? s.z * scale : 0.f,
+                                r + 3 < rank ? s.w * scale : 0.f};
+            uint32_t p[4][3];
+#pragma unroll
+            for (int i = 0; i < 4; i++) split3(v[i], p[i]);
+#pragma unroll
+            for (int z = 0; z < 3; z++) {
+                part[z][h] = p[0][z] | p[1][z] << 16;          // K slots 2 c, 2 c + 1
+                part[z][2 + h] = p[2][z] | p[3][z] << 16;      // K slots 2 c + 8, 2 c + 9
+            }
+        }
+#pragma unroll
+        for (int z = 0; z < 3; z++)
+            s_frag[(j * 3 + z) * 32 + l] = make_uint4(part[z][0], part[z][1], part[z][2], part[z][3]);
+    }
+    __syncthreads();
+
+    for (int s = 0; s < steps; s++) {
+        float d[4][4];
+#pragma unroll
+        for (int q = 0; q < 4; q++)
+#pragma unroll
+            for (int i = 0; i < 4; i++) d[q][i] = 0.f;
+        for (int j0 = 0; j0 < chunks; j0 += C) {
+            uint2 cur[C][4];
+#pragma unroll
+            for (int j = 0; j < C; j++)
+#pragma unroll
+                for (int q = 0; q < 4; q++) cur[j][q] = w[j][q];
+            if (j0 + C < chunks) load_b(w, int64_t(s) * 32, j0 + C);
+            else if (s + 1 < steps) load_b(w, int64_t(s + 1) * 32, 0);
+#pragma unroll
+            for (int j = 0; j < C; j++) {
+                if (j0 + j >= chunks) break;
+                // smallest part first
+#pragma unroll
+                for (int z = 2; z >= 0; z--) {
+                    const uint4 f = s_frag[((j0 + j) * 3 + z) * 32 + lane];
+#pragma unroll
+                    for (int q = 0; q < 4; q++) mma_16816(d[q], f.x, f.y, f.z, f.w, cur[j][q].x, cur[j][q].y);
+                }
+            }
+        }
+        float4 cy[2][2];
+#pragma unroll
+        for (int h = 0; h < 2; h++) cy[h][0] = yv[h][0], cy[h][1] = yv[h][1];
+        if (s + 1 < steps) load_y(yv, int64_t(s + 1) * 32);
+#pragma unroll
+        for (int h = 0; h < 2; h++) {
+            if (!live[h]) continue;
+            float *o = po[h] + int64_t(s) * 32;
+            // columns 8 c + 2 q + {0, 1} come from column tile q
+            *reinterpret_cast<float4 *>(o) = make_float4(cy[h][0].x + d[0][2 * h], cy[h][0].y + d[0][2 * h + 1],
+                                                         cy[h][0].z + d[1][2 * h], cy[h][0].w + d[1][2 * h + 1]);
+            *reinterpret_cast<float4 *>(o + 4) = make_float4(cy[h][1].x + d[2][2 * h], cy[h][1].y + d[2][2 * h + 1],
+                                                             cy[h][1].z + d[3][2 * h], cy[h][1].w + d[3][2 * h + 1]);
+        }
+    }
+}
+
+// most tiles of `size` rows that t rows in at most `groups` groups can make
+int64_t most_tiles(int64_t t, int64_t groups, int64_t size) {
+    return (t + (size - 1) * std::min(groups, t)) / size;
+}
+
+}  // namespace
+
+LoraGeometry lora_geometry(int64_t t, int64_t k, int groups, int max_rank) {
+    LoraGeometry g;
+    // tiles of 32 tokens reuse A's fragments four times where rows per adapter
+    // are many; single tokens would only repeat themselves in them
+    g.token_tiles = t >= 16 * int64_t(groups) && t >= 64 ? 4 : 1;
+    g.shrink_tiles = most_tiles(t, groups, 8 * g.token_tiles);
+    g.expand_tiles = most_tiles(t, groups + 1, kTileM);
+    const int rt = (max_rank + 15) / 16;
+    g.rank_tiles = g.token_tiles == 4 && rt > 1 ? 2 : 1;
+    const int64_t parts = (rt + g.rank_tiles - 1) / g.rank_tiles;
+    // no accumulation longer than 512 of K per warp; beyond that, slices until
+    // there are two CTAs per SM, none shorter than one 64-wide step per warp
+    const int64_t least = (k + 512 * kShrinkWarps - 1) / (512 * kShrinkWarps);
+    const int64_t most = std::max<int64_t>(least, std::min<int64_t>(16, k / (64 * kShrinkWarps)));
+    const int64_t want = 2 * 148 / std::max<int64_t>(1, g.shrink_tiles * parts);
+    g.splits = int(std::max<int64_t>(1, std::min(most, std::max(least, want))));
+    g.v_bytes = (uint64_t(g.splits) * uint64_t(t) * uint64_t(max_rank) * 4 + 255) / 256 * 256;
+    return g;
+}
+
+cudaError_t launch_lora(const LoraLaunch &p, cudaStream_t stream) {
+    const LoraGeometry geo = lora_geometry(p.t, p.k, p.groups, p.max_rank);
+    LoraArgs a{};
+    a.x = p.x;
+    a.x_stride = p.x_stride;
+    a.t = p.t;
+    a.k = p.k;
+    a.n = p.n;
+    a.a = p.a;
+    a.b = p.b;
+    a.groups = p.groups;
+    a.max_rank = p.max_rank;
+    a.ranks = p.ranks;
+    a.scales = p.scales;
+    a.offsets = p.offsets;
+    a.order = p.order;
+    a.v = p.v;
+    a.splits = geo.splits;
+    a.y = p.y;
+    a.y_stride = p.y_stride;
+    a.out = p.out;
+    a.out_stride = p.out_stride;
+    a.copy_rest = p.out != p.y;
+    const int rt = (p.max_rank + 15) / 16;
+    const dim3 grid1(unsigned(geo.shrink_tiles), unsigned(geo.splits), unsigned((rt + geo.rank_tiles - 1) / geo.rank_tiles));
+    const dim3 block1(kShrinkWarps * 32);
+    if (geo.token_tiles == 1) k_lora_shrink<1, 1><<<grid1, block1, 0, stream>>>(a);
+    else if (geo.rank_tiles == 1) k_lora_shrink<1, 4><<<grid1, block1, 0, stream>>>(a);
+    else k_lora_shrink<2, 4><<<grid1, block1, 0, stream>>>(a);
+    cudaError_t err = cudaGetLastError();
+    if (err != cudaSuccess) return err;
+    // enough steps per warp that the fragments of V are worth their set-up,
+    // few enough that all SMs have work
+    const int64_t total = geo.expand_tiles * (p.n / 32);
+    a.steps = int(std::max<int64_t>(1, std::min<int64_t>(16, total / (148 * 16))));
+    const int64_t per_cta = int64_t(kExpandWarps) * a.steps * 32;
+    const dim3 grid2(unsigned(geo.expand_tiles), unsigned((p.n + per_cta - 1) / per_cta));
+    const size_t smem = size_t(rt) * 3 * 32 * 16;
+    const dim3 block2(kExpandWarps * 32);
+    if (rt == 1) err = launch_pdl(true, k_lora_expand<1>, grid2, block2, smem, stream, a);
+    else if (rt == 2) err = launch_pdl(true, k_lora_expand<2>, grid2, block2, smem, stream, a);
+    else err = launch_pdl(true, k_lora_expand<4>, grid2, block2, smem, stream, a);
+    return err != cudaSuccess ? err : cudaGetLastError();
+}
+
+}  // namespace uw

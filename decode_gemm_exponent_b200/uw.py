@@ -33,6 +33,10 @@ NUM_SECTIONS = 8
 PIPE_DECODE_GEMM, PIPE_DECODE_EXP_FUSED, PIPE_TRANSCODE_FUSED, PIPE_DIRECT_PALETTE, PIPE_HUFFMAN_FUSED = 1, 2, 3, 4, 5
 KERNEL_FMA, KERNEL_TC, KERNEL_MMA, KERNEL_TC_SK, KERNEL_MMA_SK = 1, 2, 3, 4, 5
 DEBUG_NEVER_ARRIVE = 1
+MAX_GROUPS, MAX_TOP_K = 1024, 32
+TYPE_F32, TYPE_BF16 = 1, 2
+SCORES = {"softmax": 1, "sigmoid": 2}
+GROUP_SCORES = {"max": 1, "top2": 2}
 
 # every symbol include/uw.h declares
 EXPORTS = ("uw_status_str", "uw_version", "uw_encode", "uw_blob_data", "uw_blob_free",
@@ -41,7 +45,8 @@ EXPORTS = ("uw_status_str", "uw_version", "uw_encode", "uw_blob_data", "uw_blob_
            "uw_matmul_bf16", "uw_autotune_workspace_size", "uw_plan_autotune",
            "uw_fused_matmul_noalloc", "uw_stack_workspace_size", "uw_stack_run",
            "uw_sm_split_create", "uw_sm_split_get", "uw_sm_split_destroy", "uw_stack_tune_split",
-           "uw_fused_matmul_batched")
+           "uw_fused_matmul_batched", "uw_route_workspace_size", "uw_route_experts", "uw_group_workspace_size",
+           "uw_group_rows", "uw_lora_workspace_size", "uw_lora_add")
 
 
 class UwError(RuntimeError):
@@ -96,6 +101,18 @@ class BatchItem(ctypes.Structure):
                 ("y_dev", ctypes.c_void_p)]
 
 
+class Router(ctypes.Structure):
+    _fields_ = [("experts", ctypes.c_int32), ("top_k", ctypes.c_int32), ("n_groups", ctypes.c_int32),
+                ("top_groups", ctypes.c_int32), ("score", ctypes.c_int32), ("group_score", ctypes.c_int32),
+                ("renormalize", ctypes.c_int32), ("logits_type", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
+class Adapters(ctypes.Structure):
+    _fields_ = [("n", ctypes.c_int64), ("k", ctypes.c_int64), ("count", ctypes.c_int32), ("max_rank", ctypes.c_int32),
+                ("a_dev", ctypes.c_void_p), ("b_dev", ctypes.c_void_p), ("ranks_dev", ctypes.c_void_p),
+                ("scales_dev", ctypes.c_void_p)]
+
+
 def make_plan(pipeline=PIPE_DIRECT_PALETTE, kernel=KERNEL_TC, bn=16, split_k=1, stages=0,
               debug_flags=0, timeout_ns=0) -> Plan:
     return Plan(pipeline, kernel, bn, split_k, stages, debug_flags, timeout_ns)
@@ -135,6 +152,12 @@ def lib() -> ctypes.CDLL:
         "uw_fused_matmul_batched": (ctypes.c_int, [ctypes.POINTER(BatchItem), ctypes.c_int, ctypes.POINTER(Plan), P]),
         "uw_stack_workspace_size": (ctypes.c_int, [ctypes.POINTER(StackStep), ctypes.c_int, ctypes.POINTER(SZ)]),
         "uw_stack_run": (ctypes.c_int, [ctypes.POINTER(StackStep), ctypes.c_int, P, SZ, P, P]),
+        "uw_route_workspace_size": (ctypes.c_int, [I64, ctypes.POINTER(Router), ctypes.POINTER(SZ)]),
+        "uw_route_experts": (ctypes.c_int, [P, I64, I64, P, ctypes.POINTER(Router), P, P, P, P, P, P, SZ, P]),
+        "uw_group_workspace_size": (ctypes.c_int, [I64, I32, I32, ctypes.POINTER(SZ)]),
+        "uw_group_rows": (ctypes.c_int, [P, I64, I32, I32, P, P, P, P, SZ, P]),
+        "uw_lora_workspace_size": (ctypes.c_int, [I64, ctypes.POINTER(Adapters), ctypes.POINTER(SZ)]),
+        "uw_lora_add": (ctypes.c_int, [P, I64, I64, ctypes.POINTER(Adapters), P, P, P, P, I64, P, I64, P, SZ, P]),
         "uw_sm_split_create": (ctypes.c_int, [ctypes.c_int, ctypes.c_int, ctypes.POINTER(P)]),
         "uw_sm_split_get": (ctypes.c_int, [P, ctypes.POINTER(P), ctypes.POINTER(P), ctypes.POINTER(ctypes.c_int),
                                            ctypes.POINTER(ctypes.c_int)]),
@@ -441,6 +464,180 @@ def autotune(mats: Sequence[Matrix], ms: Sequence[int], reps: int = 5, stream=No
                                  reps, plans, js, cap, _stream_handle(stream)), "uw_plan_autotune")
     out = [[plans[i * len(ms) + j] for j in range(len(ms))] for i in range(len(mats))]
     return out, js.value.decode()
+
+
+# ----------------------------------------------------------------------------- around the matmuls
+
+def _enter(t, stream):
+    """Context in which a call on `t`'s device runs: that device and `stream`
+    (default: the device's current stream) are current inside, so that what is
+    allocated there belongs to the stream that uses it."""
+    import contextlib
+    import torch
+    if t.device.type != "cuda":
+        raise ValueError("tensors must be on a CUDA device, got %s" % t.device)
+    if stream is not None and stream.device != t.device:
+        raise ValueError("stream of %s for tensors of %s" % (stream.device, t.device))
+    current = torch.cuda.current_stream(t.device)
+    if t.device.index == torch.cuda.current_device() and (stream is None or stream == current):
+        return contextlib.nullcontext()
+    return torch.cuda.stream(current if stream is None else stream)
+
+
+def _need(t, name, shape, dtypes, like, rows=False):
+    """Check a tensor argument: shape, type, device, and contiguity (rows=True:
+    only of each row)."""
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError("%s: shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
+    if t.dtype not in dtypes:
+        raise ValueError("%s: type %s, expected %s" % (name, t.dtype, " or ".join(str(d) for d in dtypes)))
+    if t.device != like.device:
+        raise ValueError("%s: on %s, expected %s" % (name, t.device, like.device))
+    if not t.is_contiguous() and not (rows and t.dim() == 2 and t.stride(1) == 1):
+        raise ValueError("%s: not contiguous" % name)
+
+
+def _bits():
+    import torch
+    return (torch.bfloat16, torch.int16)
+
+
+class Grouping:
+    """Items grouped by an id (uw_group_rows): offsets int32[groups + 1],
+    order int32[items], slot int32 in the ids' shape (or None)."""
+
+    def __init__(self, offsets, order, slot=None):
+        self.offsets, self.order, self.slot = offsets, order, slot
+        self.ws = None
+
+
+class Routing(Grouping):
+    """Tokens routed to experts (uw_route_experts): ids and weights
+    [t, top_k], and the grouping of the t * top_k slots by expert."""
+
+    def __init__(self, ids, weights, offsets, order, slot):
+        super().__init__(offsets, order, slot)
+        self.ids, self.weights = ids, weights
+
+
+def route_experts(logits, top_k: int, *, score: str = "softmax", bias=None, n_groups: int = 1, top_groups: int = 1,
+                  group_score: str = "max", renormalize: bool = True, scale: float = 1.0, out: Optional[Routing] = None,
+                  stream=None) -> Routing:
+    """uw_route_experts: logits [t, experts] (float32 or bfloat16; rows may be
+    strided) -> Routing.  `out`: a Routing of the same sizes to write into
+    (its workspace is kept with it)."""
+    import torch
+    if logits.dim() != 2 or logits.dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError("logits: a [t, experts] tensor of float32 or bfloat16")
+    if score not in SCORES or group_score not in GROUP_SCORES:
+        raise ValueError("unknown score %r or group score %r" % (score, group_score))
+    t, e = logits.shape
+    if t > 1 and (logits.stride(1) != 1 and e > 1 or logits.stride(0) < e):
+        raise ValueError("logits: rows must be contiguous and must not overlap")
+    if t == 1 and e > 1 and logits.stride(1) != 1:
+        raise ValueError("logits: rows must be contiguous and must not overlap")
+    if bias is not None:
+        _need(bias, "bias", (e,), (torch.float32,), logits)
+    r = Router(e, top_k, n_groups, top_groups, SCORES[score], GROUP_SCORES[group_score], int(renormalize),
+               TYPE_BF16 if logits.dtype == torch.bfloat16 else TYPE_F32, scale)
+    size = ctypes.c_size_t()
+    check(lib().uw_route_workspace_size(t, ctypes.byref(r), ctypes.byref(size)), "uw_route_workspace_size")
+    with _enter(logits, stream):
+        if out is None:
+            i32 = dict(dtype=torch.int32, device=logits.device)
+            out = Routing(torch.empty(t, top_k, **i32), torch.empty(t, top_k, dtype=torch.float32, device=logits.device),
+                          torch.empty(e + 1, **i32), torch.empty(t * top_k, **i32), torch.empty(t, top_k, **i32))
+        else:
+            for f, shape in (("ids", (t, top_k)), ("offsets", (e + 1,)), ("order", (t * top_k,)), ("slot", (t, top_k))):
+                _need(getattr(out, f), "out." + f, shape, (torch.int32,), logits)
+            _need(out.weights, "out.weights", (t, top_k), (torch.float32,), logits)
+        if size.value and (out.ws is None or out.ws.numel() < size.value or out.ws.device != logits.device):
+            out.ws = torch.empty(size.value, dtype=torch.uint8, device=logits.device)
+        check(lib().uw_route_experts(logits.data_ptr(), t, logits.stride(0) if t > 1 else e,
+                                     None if bias is None else bias.data_ptr(), ctypes.byref(r), out.ids.data_ptr(),
+                                     out.weights.data_ptr(), out.offsets.data_ptr(), out.order.data_ptr(),
+                                     out.slot.data_ptr(), out.ws.data_ptr() if size.value else None, size.value,
+                                     _stream_handle()), "uw_route_experts")
+    return out
+
+
+def group_rows(ids, groups: int, out: Optional[Grouping] = None, stream=None) -> Grouping:
+    """uw_group_rows: int32 ids [rows] or [rows, per_row] -> Grouping of their
+    items by id; ids outside [0, groups) belong to no group."""
+    import torch
+    if ids.dim() not in (1, 2) or ids.dtype != torch.int32 or not ids.is_contiguous():
+        raise ValueError("ids: a contiguous int32 tensor [rows] or [rows, per_row]")
+    rows, per_row = ids.shape[0], ids.shape[1] if ids.dim() == 2 else 1
+    size = ctypes.c_size_t()
+    check(lib().uw_group_workspace_size(rows, per_row, groups, ctypes.byref(size)), "uw_group_workspace_size")
+    with _enter(ids, stream):
+        if out is None:
+            i32 = dict(dtype=torch.int32, device=ids.device)
+            out = Grouping(torch.empty(groups + 1, **i32), torch.empty(ids.numel(), **i32), torch.empty(ids.shape, **i32))
+        else:
+            _need(out.offsets, "out.offsets", (groups + 1,), (torch.int32,), ids)
+            _need(out.order, "out.order", (ids.numel(),), (torch.int32,), ids)
+            if out.slot is not None:
+                _need(out.slot, "out.slot", ids.shape, (torch.int32,), ids)
+        if size.value and (out.ws is None or out.ws.numel() < size.value or out.ws.device != ids.device):
+            out.ws = torch.empty(size.value, dtype=torch.uint8, device=ids.device)
+        check(lib().uw_group_rows(ids.data_ptr(), rows, per_row, groups, out.offsets.data_ptr(), out.order.data_ptr(),
+                                  None if out.slot is None else out.slot.data_ptr(),
+                                  out.ws.data_ptr() if size.value else None, size.value, _stream_handle()), "uw_group_rows")
+    return out
+
+
+def lora_workspace_size(t: int, k: int, n: int, adapters: int, max_rank: int) -> int:
+    d = Adapters(n, k, adapters, max_rank)
+    size = ctypes.c_size_t()
+    check(lib().uw_lora_workspace_size(t, ctypes.byref(d), ctypes.byref(size)), "uw_lora_workspace_size")
+    return int(size.value)
+
+
+def lora_add(x, a, b, ids, y, *, ranks=None, scales=None, groups: Optional[Grouping] = None, out=None, ws=None,
+             stream=None):
+    """uw_lora_add: y [t, n] (float32) plus each row's adapter on x [t, k]
+    (bfloat16, or its bits as int16).  a [adapters, max_rank, k] and
+    b [adapters, n, max_rank] hold the adapters in slots; ids int32 [t] names
+    each row's slot (outside: none), or `groups` holds the rows' grouping
+    (group_rows(ids, adapters), then ids may be None).  out: where the result
+    goes (y itself for an update in place)."""
+    import torch
+    if x.dim() != 2 or a.dim() != 3 or b.dim() != 3 or y.dim() != 2:
+        raise ValueError("x [t, k], a [adapters, max_rank, k], b [adapters, n, max_rank], y [t, n]")
+    t, k = x.shape
+    count, rank = a.shape[0], a.shape[1]
+    n = b.shape[1]
+    _need(x, "x", (t, k), _bits(), x, rows=True)
+    _need(a, "a", (count, rank, k), _bits(), x)
+    _need(b, "b", (count, n, rank), _bits(), x)
+    _need(y, "y", (t, n), (torch.float32,), x, rows=True)
+    if ranks is not None:
+        _need(ranks, "ranks", (count,), (torch.int32,), x)
+    if scales is not None:
+        _need(scales, "scales", (count,), (torch.float32,), x)
+    if groups is None:
+        _need(ids, "ids", (t,), (torch.int32,), x)
+    else:
+        _need(groups.offsets, "groups.offsets", (count + 1,), (torch.int32,), x)
+        _need(groups.order, "groups.order", (t,), (torch.int32,), x)
+    d = Adapters(n, k, count, rank, a.data_ptr(), b.data_ptr(), None if ranks is None else ranks.data_ptr(),
+                 None if scales is None else scales.data_ptr())
+    with _enter(x, stream):
+        if out is None:
+            out = torch.empty(t, n, dtype=torch.float32, device=x.device)
+        else:
+            _need(out, "out", (t, n), (torch.float32,), x, rows=True)
+        if ws is None:
+            size = ctypes.c_size_t()
+            check(lib().uw_lora_workspace_size(t, ctypes.byref(d), ctypes.byref(size)), "uw_lora_workspace_size")
+            ws = torch.empty(max(size.value, 1), dtype=torch.uint8, device=x.device)
+        row = (lambda v: v.stride(0) if t > 1 else v.shape[1])
+        check(lib().uw_lora_add(x.data_ptr(), row(x), t, ctypes.byref(d), None if groups is not None else ids.data_ptr(),
+                                None if groups is None else groups.offsets.data_ptr(),
+                                None if groups is None else groups.order.data_ptr(), y.data_ptr(), row(y),
+                                out.data_ptr(), row(out), ws.data_ptr(), ws.numel(), _stream_handle()), "uw_lora_add")
+    return out
 
 
 PIPELINE_NAMES = {PIPE_DECODE_GEMM: "decode_gemm", PIPE_DECODE_EXP_FUSED: "decode_exp_fused",

@@ -474,6 +474,99 @@ uw_status uw_stack_tune_split(const uw_stack_step *steps, int n_steps, void *ws,
                               int device, const int *cand, int n_cand, int reps, int *best,
                               float *us_out, void *stream);
 
+/* ------------------------------------------------------------------------ */
+/* Routing to experts, and rows grouped by an index (the step in front of a   */
+/* mixture-of-experts layer, which the Unweight page §十一 names as the next  */
+/* target).                                                                   */
+
+#define UW_MAX_GROUPS 1024    /* experts, adapters: most of them in one call   */
+#define UW_MAX_TOP_K 32       /* experts per token                             */
+
+enum { UW_TYPE_F32 = 1, UW_TYPE_BF16 = 2 };
+enum { UW_SCORE_SOFTMAX = 1, UW_SCORE_SIGMOID = 2 };
+enum { UW_GROUP_MAX = 1, UW_GROUP_TOP2 = 2 };
+
+/* How a token's experts are chosen. */
+typedef struct uw_router {
+    int32_t experts;       /* 1..UW_MAX_GROUPS                                      */
+    int32_t top_k;         /* 1..UW_MAX_TOP_K, <= top_groups * experts / n_groups   */
+    int32_t n_groups;      /* equal runs of experts, 1..32, a divisor of experts    */
+    int32_t top_groups;    /* runs that stay in the choice, 1..n_groups             */
+    int32_t score;         /* UW_SCORE_*                                            */
+    int32_t group_score;   /* UW_GROUP_*: a run's value is its largest choice, or
+                              the sum of its two largest scores plus bias          */
+    int32_t renormalize;   /* non-zero: the chosen scores are divided by their sum
+                              plus 1e-20                                            */
+    int32_t logits_type;   /* UW_TYPE_F32 or UW_TYPE_BF16                           */
+    float scale;           /* factor of every weight                                */
+} uw_router;
+
+/* Route t tokens (t >= 0).  logits_dev: [t, experts] of router->logits_type, rows
+ * row_stride elements apart (>= experts).  bias_dev: float[experts] or NULL; it is
+ * added to the scores for the choice only (selection and run values), never to the
+ * weights.  Choices are compared exactly: the logits themselves without a bias,
+ * scores in 64 bits with one; ties go to the lowest index.  An expert whose logit
+ * is -inf or NaN, or whose bias is, is never chosen; a slot for which no expert is
+ * left gets id -1 and weight 0 (a token whose logits are all -inf routes nowhere).
+ * Outputs:
+ *   ids_dev      int32[t, top_k], largest choice first
+ *   weights_dev  float[t, top_k], scale * score (renormalized or not)
+ *   offsets_dev, order_dev, slot_dev   as uw_group_rows gives for these ids
+ * All pointers 4-byte aligned.  ws: >= uw_route_workspace_size bytes (0 for small
+ * calls), 256-byte aligned; its contents do not matter.  Results do not vary from
+ * run to run.  t * top_k must be below 2^31.                                       */
+uw_status uw_route_workspace_size(int64_t t, const uw_router *router, size_t *bytes);
+uw_status uw_route_experts(const void *logits_dev, int64_t t, int64_t row_stride, const float *bias_dev,
+                           const uw_router *router, int32_t *ids_dev, float *weights_dev, int32_t *offsets_dev,
+                           int32_t *order_dev, int32_t *slot_dev, void *ws, size_t ws_bytes, void *stream);
+
+/* Group the rows * per_row items of ids_dev (rows >= 0, 1 <= per_row <= 64) by their
+ * id; ids outside [0, groups) belong to no group.  groups: 1..UW_MAX_GROUPS.
+ *   offsets_dev  int32[groups + 1]: items of group g stand at places offsets[g] ..
+ *                offsets[g + 1] of the order; offsets[groups] items have a group
+ *   order_dev    int32[rows * per_row]: the items' indices by group, in index order
+ *                inside a group; the items of no group stand last
+ *   slot_dev     int32[rows * per_row]: each item's place in the order, -1 for items
+ *                of no group (may be NULL)
+ * An id may occur several times in a row.  ws as for uw_route_experts.             */
+uw_status uw_group_workspace_size(int64_t rows, int32_t per_row, int32_t groups, size_t *bytes);
+uw_status uw_group_rows(const int32_t *ids_dev, int64_t rows, int32_t per_row, int32_t groups, int32_t *offsets_dev,
+                        int32_t *order_dev, int32_t *slot_dev, void *ws, size_t ws_bytes, void *stream);
+
+/* ------------------------------------------------------------------------ */
+/* Low-rank adapters of many requests beside a shared projection.             */
+
+/* The adapters of one projection, in slots of equal size. */
+typedef struct uw_adapters {
+    int64_t n, k;             /* the projection's sizes, multiples of 64              */
+    int32_t count;            /* 1..UW_MAX_GROUPS slots                               */
+    int32_t max_rank;         /* ranks per slot, a multiple of 8, 8..256              */
+    const uint16_t *a_dev;    /* BF16 [count, max_rank, k], 16-byte aligned           */
+    const uint16_t *b_dev;    /* BF16 [count, n, max_rank], 16-byte aligned           */
+    const int32_t *ranks_dev; /* int32[count], each clamped to [0, max_rank]; NULL:
+                                 max_rank for all.  What a slot holds beyond its rank
+                                 is never part of a result, NaN included.             */
+    const float *scales_dev;  /* float[count]; NULL: 1                                */
+} uw_adapters;
+
+/* out[i] = y[i] + scale_a * B_a (A_a x[i]) for every row i < t whose adapter
+ * a = ids[i] is in [0, count); out[i] = y[i] for the others.  x_dev: BF16 [t, k];
+ * y_dev, out_dev: float [t, n]; out_dev may be y_dev (then with the same stride:
+ * the update is in place and rows without an adapter are not touched) but may not
+ * overlap it otherwise.  Strides are elements between rows: x_stride >= k and a
+ * multiple of 8, y_stride and out_stride >= n and multiples of 4; x, y and out are
+ * 16-byte aligned.
+ * The rows' adapters are given either by ids_dev (int32[t]; the call groups them
+ * itself) or, with ids_dev NULL, by offsets_dev and order_dev as uw_group_rows wrote
+ * them for per_row = 1 and groups = count, so that the projections of a step share
+ * one grouping.  The inner product is summed and kept in 32 bits.
+ * ws: >= uw_lora_workspace_size bytes, 256-byte aligned; its contents do not matter.
+ * t >= 0; t = 0 launches nothing.                                                  */
+uw_status uw_lora_workspace_size(int64_t t, const uw_adapters *adapters, size_t *bytes);
+uw_status uw_lora_add(const uint16_t *x_dev, int64_t x_stride, int64_t t, const uw_adapters *adapters,
+                      const int32_t *ids_dev, const int32_t *offsets_dev, const int32_t *order_dev, const float *y_dev,
+                      int64_t y_stride, float *out_dev, int64_t out_stride, void *ws, size_t ws_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif
