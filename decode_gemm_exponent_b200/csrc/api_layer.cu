@@ -1,6 +1,6 @@
 // api_layer.cu -- C ABI of the operators around the matmuls (declared in
-// include/uw.h): routing, grouping of rows, low-rank adapters.  Checks of the
-// arguments; the kernels are in route.cu and lora.cu.
+// include/uw.h): routing, grouping of rows, expert products, low-rank adapters.
+// Checks of the arguments; the kernels are in route.cu, expert.cu and lora.cu.
 #include <cmath>
 
 #include "kernels.h"
@@ -43,6 +43,77 @@ uw_status check_adapters(const uw_adapters *a, int64_t t) {
     const LoraGeometry g = lora_geometry(t, a->k, a->count, a->max_rank);
     if (g.splits > 65535) return UW_ERR_UNSUPPORTED_SHAPE;   // K slices are a grid dimension
     return UW_OK;
+}
+
+uw_status check_set(const uw_expert_set *s) {
+    if (!s || s->n <= 0 || s->k <= 0) return UW_ERR_INVALID_ARG;
+    if (s->n % 64 || s->k % 64 || s->n > kMaxItems || s->k > kMaxItems) return UW_ERR_UNSUPPORTED_SHAPE;
+    if (s->experts < 1 || s->experts > UW_MAX_GROUPS) return UW_ERR_INVALID_ARG;
+    if ((s->w_dev != nullptr) == (s->table_dev != nullptr)) return UW_ERR_INVALID_ARG;
+    if (!aligned(s->w_dev, 16) || !aligned(s->table_dev, 16)) return UW_ERR_INVALID_ARG;
+    if (s->w_dev && (s->stride < s->n * s->k || s->stride % 8)) return UW_ERR_INVALID_ARG;
+    return UW_OK;
+}
+
+uw_status check_expert_call(const uw_expert_rows *r, const uw_expert_set *a, const uw_expert_set *b, const void *out,
+                            int64_t out_stride, int out_unit, const uw_plan *p) {
+    uw_status st = check_set(a);
+    if (st != UW_OK) return st;
+    if (b) {
+        st = check_set(b);
+        if (st != UW_OK) return st;
+        if (b->n != a->n || b->k != a->k || b->experts != a->experts || !a->w_dev != !b->w_dev) return UW_ERR_INVALID_ARG;
+    }
+    if (!r || !p || r->places < 0 || r->per_row < 1) return UW_ERR_INVALID_ARG;
+    if (r->places > kMaxItems || r->x_rows > kMaxItems) return UW_ERR_UNSUPPORTED_SHAPE;
+    if (p->pipeline != UW_PIPE_DIRECT_PALETTE || p->split_k != 1 || p->timeout_ns < 0) return UW_ERR_INVALID_ARG;
+    if (p->kernel == UW_KERNEL_MMA) {
+        if (p->bn < 1 || p->bn > 8 || p->stages < 0 || p->stages > 2 || (p->stages == 2 && a->k % 128))
+            return UW_ERR_INVALID_ARG;
+        // the raw-group bitmaps of a tile of rows are staged in 48 KB
+        if (a->table_dev && a->k > 131072) return UW_ERR_UNSUPPORTED_SHAPE;
+    } else if (p->kernel == UW_KERNEL_TC) {
+        if (!a->w_dev || (p->bn != 128 && p->bn != 256) || p->stages != 0) return UW_ERR_INVALID_ARG;
+        if (a->stride >= int64_t(1) << 39 || (b && b->stride >= int64_t(1) << 39)) return UW_ERR_UNSUPPORTED_SHAPE;
+    } else {
+        return UW_ERR_INVALID_ARG;
+    }
+    if (out_stride < a->n || out_stride % out_unit) return UW_ERR_INVALID_ARG;
+    if (r->places == 0) return UW_OK;
+    if (!r->x_dev || r->x_rows < 1 || !r->offsets_dev || !out) return UW_ERR_INVALID_ARG;
+    if (!r->order_dev && r->x_rows < r->places) return UW_ERR_INVALID_ARG;
+    if (r->x_stride < a->k || r->x_stride % 8) return UW_ERR_INVALID_ARG;
+    if (p->kernel == UW_KERNEL_TC && r->x_stride >= int64_t(1) << 39) return UW_ERR_UNSUPPORTED_SHAPE;
+    if (!aligned(r->x_dev, 16) || !aligned(out, 16) || !aligned(r->offsets_dev, 4) || !aligned(r->order_dev, 4))
+        return UW_ERR_INVALID_ARG;
+    return UW_OK;
+}
+
+ExpertLaunch expert_launch(const uw_expert_rows *r, const uw_expert_set *a, const uw_expert_set *b, void *out,
+                           int64_t out_stride, const uw_plan *p, uint32_t *status) {
+    ExpertLaunch l{};
+    l.a = ExpertSet{a->w_dev, a->stride, a->table_dev};
+    if (b) l.b = ExpertSet{b->w_dev, b->stride, b->table_dev};
+    l.gated = b != nullptr;
+    l.experts = a->experts;
+    l.n = a->n;
+    l.k = a->k;
+    l.x = r->x_dev;
+    l.x_rows = r->x_rows;
+    l.x_stride = r->x_stride;
+    l.places = r->places;
+    l.per_row = r->per_row;
+    l.offsets = r->offsets_dev;
+    l.order = r->order_dev;
+    l.y = out;
+    l.y_stride = out_stride;
+    l.kernel = p->kernel;
+    l.slices = p->bn;
+    l.width = p->stages;
+    l.bn = p->bn;
+    l.timeout_ns = p->timeout_ns > 0 ? uint64_t(p->timeout_ns) : 2000000000ull;
+    l.status = status;
+    return l;
 }
 
 // uw_lora_add's own grouping: offsets, order and the sort's workspace, then V
@@ -204,4 +275,71 @@ extern "C" uw_status uw_lora_add(const uint16_t *x_dev, int64_t x_stride, int64_
     p.out_stride = out_stride;
     p.v = reinterpret_cast<float *>(base + w.v_off);
     return cuda_status(launch_lora(p, s));
+}
+
+extern "C" uw_status uw_expert_table(const uw_dmat *const *mats, int32_t experts, void *table, size_t table_bytes) {
+    if (!mats || !table || experts < 1 || experts > UW_MAX_GROUPS) return UW_ERR_INVALID_ARG;
+    if (table_bytes < size_t(experts) * UW_EXPERT_ENTRY_BYTES) return UW_ERR_WORKSPACE;
+    for (int32_t e = 0; e < experts; e++) {
+        const uw_dmat *w = mats[e];
+        if (!w || !w->sm || !w->flagbits || !w->rawbase || !w->pal || !aligned(w->pal, 16)) return UW_ERR_INVALID_ARG;
+        if (w->n != mats[0]->n || w->k != mats[0]->k) return UW_ERR_INVALID_ARG;
+        if (w->n <= 0 || w->k <= 0 || w->n % 64 || w->k % 64) return UW_ERR_UNSUPPORTED_SHAPE;
+    }
+    for (int32_t e = 0; e < experts; e++)
+        expert_fill_entry(static_cast<uint8_t *>(table) + size_t(e) * UW_EXPERT_ENTRY_BYTES, *mats[e]);
+    return UW_OK;
+}
+
+extern "C" uw_status uw_expert_plan_default(const uw_expert_set *w, int64_t places, uw_plan *plan) {
+    if (!plan || places < 0) return UW_ERR_INVALID_ARG;
+    const uw_status st = check_set(w);
+    if (st != UW_OK) return st;
+    *plan = uw_plan{};
+    plan->pipeline = UW_PIPE_DIRECT_PALETTE;
+    plan->split_k = 1;
+    if (!w->w_dev || places <= int64_t(16) * w->experts) {
+        plan->kernel = UW_KERNEL_MMA;
+        plan->bn = w->k > 4096 ? 8 : 4;
+    } else {
+        plan->kernel = UW_KERNEL_TC;
+        plan->bn = 256;
+    }
+    return UW_OK;
+}
+
+extern "C" uw_status uw_expert_matmul(const uw_expert_rows *rows, const uw_expert_set *w, float *y_dev, int64_t y_stride,
+                                      const uw_plan *plan, uint32_t *dev_status, void *stream) {
+    const uw_status st = check_expert_call(rows, w, nullptr, y_dev, y_stride, 4, plan);
+    if (st != UW_OK || rows->places == 0) return st;
+    return cuda_status(launch_expert(expert_launch(rows, w, nullptr, y_dev, y_stride, plan, dev_status),
+                                     static_cast<cudaStream_t>(stream)));
+}
+
+extern "C" uw_status uw_expert_gate_up(const uw_expert_rows *rows, const uw_expert_set *gate, const uw_expert_set *up,
+                                       uint16_t *h_dev, int64_t h_stride, const uw_plan *plan, uint32_t *dev_status,
+                                       void *stream) {
+    if (!up) return UW_ERR_INVALID_ARG;
+    const uw_status st = check_expert_call(rows, gate, up, h_dev, h_stride, 8, plan);
+    if (st != UW_OK || rows->places == 0) return st;
+    return cuda_status(launch_expert(expert_launch(rows, gate, up, h_dev, h_stride, plan, dev_status),
+                                     static_cast<cudaStream_t>(stream)));
+}
+
+extern "C" uw_status uw_expert_combine(const float *y_dev, int64_t y_stride, const int32_t *slot_dev,
+                                       const float *weights_dev, int64_t t, int32_t top_k, int64_t n,
+                                       const float *base_dev, int64_t base_stride, float *out_dev, int64_t out_stride,
+                                       void *stream) {
+    if (t < 0 || top_k < 1 || n <= 0) return UW_ERR_INVALID_ARG;
+    if (n % 4 || t > kMaxItems / top_k || n > (int64_t(1) << 25)) return UW_ERR_UNSUPPORTED_SHAPE;
+    if (y_stride < n || y_stride % 4 || out_stride < n || out_stride % 4) return UW_ERR_INVALID_ARG;
+    if (base_dev && (base_stride < n || base_stride % 4)) return UW_ERR_INVALID_ARG;
+    if (t == 0) return UW_OK;
+    if (!y_dev || !slot_dev || !weights_dev || !out_dev) return UW_ERR_INVALID_ARG;
+    if (!aligned(y_dev, 16) || !aligned(out_dev, 16) || !aligned(base_dev, 16) || !aligned(slot_dev, 4) ||
+        !aligned(weights_dev, 4))
+        return UW_ERR_INVALID_ARG;
+    if (base_dev == out_dev && base_stride != out_stride) return UW_ERR_INVALID_ARG;
+    CombineLaunch p{y_dev, y_stride, slot_dev, weights_dev, t, n, top_k, base_dev, base_stride, out_dev, out_stride};
+    return cuda_status(launch_expert_combine(p, static_cast<cudaStream_t>(stream)));
 }

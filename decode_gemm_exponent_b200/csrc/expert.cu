@@ -1,0 +1,752 @@
+// expert.cu -- products of routed rows with their experts' weights, the token
+// counts read on the device (a router's offsets), so that a step needs no copy
+// back to the host between the router and the experts:
+//   matmul    y[j] = W_e x[src(j)]                        (FP32)
+//   gate_up   h[j] = silu(G_e x[src(j)]) * (U_e x[src(j)])  (BF16)
+//   combine   out[t] = base[t] + sum_s weight[t, s] y[slot[t, s]]
+// for the places j of expert e, offsets[e] <= j < offsets[e + 1]; src(j) is
+// order[j] / per_row (the token of the place) or j.
+//
+// Few rows per expert (k_expert_mma): the job is one pass over the routed
+// experts' weights, whatever form they have.  A CTA owns 16 rows of W of one
+// expert that has rows (for gate_up: 8 rows of G and the same 8 of U, so that
+// a lane's accumulators hold a gate and its up value side by side), its warps
+// split K, and every lane loads its weights straight into MMA fragment order,
+// as the dense warp-MMA kernel does; compressed weights are rebuilt in
+// registers.  Rows beyond 16 take further passes over the tile, from L2.
+//
+// Many rows per expert (k_expert_tc): persistent tcgen05 kernel, plain BF16
+// weights.  Tokens are the MMA's M (128 rows of one expert), weights its N, so
+// that a token's outputs lie in one TMEM lane: its gate and up values meet in
+// one thread.  Rows of x are gathered by TMA (four row indices per copy), so no
+// sorted copy of x is written.  Two TMEM accumulators: the epilogue of a tile
+// overlaps the next tile's products.  The tensor core truncates as it
+// accumulates (about 1.1e-9 per unit of K, relative, measured), so FP32 outputs
+// are summed in registers over chunks of 512 of K; BF16 outputs need no chunks.
+#include <algorithm>
+#include <atomic>
+#include <cstring>
+
+#include <cuda_bf16.h>
+
+#include "device_common.cuh"
+#include "kernels.h"
+#include "mma_tile.cuh"
+#include "uw_format.h"
+
+namespace uw {
+namespace {
+
+using namespace dev;
+
+constexpr uint32_t kAll = 0xFFFFFFFFu;
+
+// One matrix, or where the experts' matrices are.
+struct Planes {
+    const uint16_t *w;         // plain BF16 [n, k]
+    const uint8_t *sm;         // compressed: the planes of a palette-form matrix
+    const uint32_t *pal;
+    const uint32_t *flagbits;
+    const uint32_t *rawbase;
+    const uint8_t *rawexp;
+    Palette16 palette;
+};
+static_assert(sizeof(Planes) == 64, "the table entry size in the header");
+
+struct SetArgs {
+    const uint16_t *w;         // plain: expert e at w + e * stride
+    int64_t stride;
+    const Planes *table;       // compressed: one entry per expert
+};
+
+struct MmaExpertArgs {
+    SetArgs a, b;              // b: the up matrices (gate_up only)
+    const uint16_t *x;
+    int64_t x_rows, x_stride;
+    int64_t n, k;
+    int experts;
+    int64_t places;            // rows * per_row
+    int per_row;
+    const int32_t *offsets, *order;
+    void *y;
+    int64_t y_stride;
+    int flag_words;            // compressed: bitmap words staged per half tile (8 rows)
+};
+
+__device__ __forceinline__ float silu(float g) { return g * __fdividef(1.f, 1.f + __expf(-g)); }
+
+struct Span {
+    int expert, pos, rows;
+};
+
+// The which-th expert that has rows (every warp for itself).
+__device__ __forceinline__ Span find_active(const int32_t *offsets, int experts, int64_t places, int which) {
+    const int lane = threadIdx.x & 31;
+    const int most = int(places);
+    int run = 0;
+    for (int e0 = 0; e0 < experts; e0 += 32) {
+        int lo = 0, cnt = 0;
+        if (e0 + lane < experts) {
+            lo = min(max(__ldg(offsets + e0 + lane), 0), most);
+            cnt = max(min(max(__ldg(offsets + e0 + lane + 1), 0), most) - lo, 0);
+        }
+        const uint32_t has = __ballot_sync(kAll, cnt > 0);
+        const int total = __popc(has);
+        if (which < run + total) {
+            const bool mine = (has >> lane & 1u) && __popc(has & ((1u << lane) - 1u)) == which - run;
+            const int src = __ffs(__ballot_sync(kAll, mine)) - 1;
+            return Span{e0 + src, __shfl_sync(kAll, lo, src), __shfl_sync(kAll, cnt, src)};
+        }
+        run += total;
+    }
+    return Span{-1, 0, 0};
+}
+
+// the row of x for place p
+__device__ __forceinline__ int64_t source_row(const int32_t *order, int per_row, int64_t x_rows, int p) {
+    const int64_t r = order ? int64_t(__ldg(order + p)) / per_row : int64_t(p);
+    return min(max(r, int64_t(0)), x_rows - 1);
+}
+
+// One half tile's matrix (8 rows from `row`) as a warp reads it.
+template <bool PAL>
+struct HalfTile {
+    Planes p;
+    const uint32_t *flags, *base;      // staged bitmap words and prefix counts
+    int64_t wbase, row;
+    int nwords;
+};
+
+template <bool PAL>
+__device__ __forceinline__ HalfTile<PAL> half_tile(const SetArgs &s, int expert, int64_t row, int64_t k, uint32_t *flags,
+                                                   uint32_t *base) {
+    HalfTile<PAL> h;
+    h.row = row;
+    h.flags = flags;
+    h.base = base;
+    h.wbase = 0;
+    h.nwords = 0;
+    if constexpr (PAL) {
+        h.p = s.table[expert];
+        const int64_t gpr = k / kGroup;
+        h.wbase = (row * gpr) >> 5;
+        h.nwords = int((((row + 8) * gpr - 1) >> 5) - h.wbase + 1);
+        for (int i = threadIdx.x; i < h.nwords; i += blockDim.x) {
+            flags[i] = __ldg(h.p.flagbits + h.wbase + i);
+            base[i] = __ldg(h.p.rawbase + h.wbase + i);
+        }
+    } else {
+        h.p.w = s.w + int64_t(expert) * s.stride;
+    }
+    return h;
+}
+
+// 16 rows of W times up to 8 * NT tokens at places [pos, pos + m)
+template <bool PAL, bool GATED, int NT, int Q>
+__device__ __forceinline__ void expert_pass(const MmaExpertArgs &a, const HalfTile<PAL> &ta, const HalfTile<PAL> &tb, int pos,
+                                            int m, float *red) {
+    constexpr int kCh = kGroup * Q, kWl = 16 * Q, kStages = Q == 1 ? 3 : 2, kWin = 64 / Q;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, slices = blockDim.x >> 5;
+    const int g = lane >> 2, c = lane & 3;
+    const int64_t gpr = a.k / kGroup, cpr = a.k / kCh;
+    const int64_t ch0 = cpr * warp / slices;
+    const int nch = int(cpr * (warp + 1) / slices - ch0);
+    const int64_t ea = (ta.row + g) * a.k + ch0 * kCh + c * kWl, eb = (tb.row + g) * a.k + ch0 * kCh + c * kWl;
+    const int coff = (c * kWl) / kGroup, goff = (c * kWl) % kGroup;
+    const int64_t ga = (ta.row + g) * gpr + ch0 * Q, gb = (tb.row + g) * gpr + ch0 * Q;
+    const int64_t xo = ch0 * kCh + c * kWl;
+    const uint16_t *x0 = a.x + source_row(a.order, a.per_row, a.x_rows, pos + min(g, m - 1)) * a.x_stride + xo;
+    const uint16_t *x1 = NT == 2 ? a.x + source_row(a.order, a.per_row, a.x_rows, pos + min(g + 8, m - 1)) * a.x_stride + xo : x0;
+    uint64_t rawa = 0, rawb = 0;
+    if (PAL) {
+        rawa = raw_window(ta.flags, ta.nwords, ta.wbase, ga);
+        rawb = raw_window(tb.flags, tb.nwords, tb.wbase, gb);
+    }
+    float d0[NT][4], d1[NT][4];
+#pragma unroll
+    for (int t = 0; t < NT; t++)
+#pragma unroll
+        for (int q = 0; q < 4; q++) d0[t][q] = d1[t][q] = 0.f;
+    Half<Q> ha[kStages], hb[kStages];
+    bool fa[kStages], fb[kStages];
+    auto issue = [&](int i, int s) {
+        const int bit = ((i * Q) & 63) + coff;
+        fa[s] = PAL && ((rawa >> bit) & 1u);
+        fb[s] = PAL && ((rawb >> bit) & 1u);
+        const int64_t oa = ea + int64_t(i) * kCh, ob = eb + int64_t(i) * kCh;
+        ha[s] = load_half<PAL, Q>(ta.p.rawexp, ta.p.sm + oa, ta.p.pal + oa / 8, ta.p.w + oa, fa[s], ga + i * Q + coff, goff,
+                                  ta.flags, ta.base, ta.wbase);
+        hb[s] = load_half<PAL, Q>(tb.p.rawexp, tb.p.sm + ob, tb.p.pal + ob / 8, tb.p.w + ob, fb[s], gb + i * Q + coff, goff,
+                                  tb.flags, tb.base, tb.wbase);
+        prefetch_l1(x0 + int64_t(i) * kCh);
+        if (NT == 2) prefetch_l1(x1 + int64_t(i) * kCh);
+    };
+    auto mma_tile = [&](int t, const uint32_t (&wA)[8 * Q], const uint32_t (&wB)[8 * Q], const uint16_t *xrow) {
+        uint32_t xw[8 * Q];
+#pragma unroll
+        for (int i = 0; i < 2 * Q; i++) {
+            const uint4 v = __ldg(reinterpret_cast<const uint4 *>(xrow) + i);
+            xw[4 * i] = v.x;
+            xw[4 * i + 1] = v.y;
+            xw[4 * i + 2] = v.z;
+            xw[4 * i + 3] = v.w;
+        }
+#pragma unroll
+        for (int j = 0; j < 4 * Q; j++)
+            mma_16816((j & 1) ? d1[t] : d0[t], wA[2 * j], wB[2 * j], wA[2 * j + 1], wB[2 * j + 1], xw[2 * j], xw[2 * j + 1]);
+    };
+    auto consume = [&](int i, int s) {
+        uint32_t wA[8 * Q], wB[8 * Q];
+        rebuild<PAL, Q>(ha[s], fa[s], ta.p.palette, wA);
+        rebuild<PAL, Q>(hb[s], fb[s], tb.p.palette, wB);
+        mma_tile(0, wA, wB, x0 + int64_t(i) * kCh);
+        if (NT == 2) mma_tile(NT - 1, wA, wB, x1 + int64_t(i) * kCh);
+    };
+#pragma unroll
+    for (int s = 0; s < kStages; s++)
+        if (s < nch) issue(s, s);
+    int i0 = 0;
+    for (; i0 + kStages <= nch; i0 += kStages) {
+#pragma unroll
+        for (int s = 0; s < kStages; s++) {
+            consume(i0 + s, s);
+            const int nx = i0 + s + kStages;
+            if (nx < nch) {
+                if (PAL && nx % kWin == 0) {
+                    rawa = raw_window(ta.flags, ta.nwords, ta.wbase, ga + nx * Q);
+                    rawb = raw_window(tb.flags, tb.nwords, tb.wbase, gb + nx * Q);
+                }
+                issue(nx, s);
+            }
+        }
+    }
+#pragma unroll
+    for (int s = 0; s < kStages; s++)
+        if (i0 + s < nch) consume(i0 + s, s);
+
+    float v[NT][4];
+#pragma unroll
+    for (int t = 0; t < NT; t++)
+#pragma unroll
+        for (int q = 0; q < 4; q++) v[t][q] = d0[t][q] + d1[t][q];
+    if (slices > 1) {
+#pragma unroll
+        for (int t = 0; t < NT; t++)
+#pragma unroll
+            for (int q = 0; q < 4; q++) red[(warp * 32 + lane) * 4 * NT + t * 4 + q] = v[t][q];
+        __syncthreads();
+        if (warp == 0) {
+#pragma unroll
+            for (int t = 0; t < NT; t++)
+#pragma unroll
+                for (int q = 0; q < 4; q++) {
+                    float acc = red[lane * 4 * NT + t * 4 + q];
+                    for (int w = 1; w < slices; w++) acc += red[(w * 32 + lane) * 4 * NT + t * 4 + q];
+                    v[t][q] = acc;
+                }
+        }
+        __syncthreads();   // the next pass writes `red` again
+    }
+    if (warp) return;
+    // v[t][0..1]: row g of the first half, tokens 8 t + 2 c, + 1; v[t][2..3]: of the second
+#pragma unroll
+    for (int t = 0; t < NT; t++)
+#pragma unroll
+        for (int u = 0; u < 2; u++) {
+            const int tok = 8 * t + 2 * c + u;
+            if (tok >= m) continue;
+            const int64_t at = int64_t(pos + tok) * a.y_stride;
+            if constexpr (GATED) {
+                static_cast<uint16_t *>(a.y)[at + ta.row + g] =
+                    __bfloat16_as_ushort(__float2bfloat16_rn(silu(v[t][u]) * v[t][2 + u]));
+            } else {
+                static_cast<float *>(a.y)[at + ta.row + g] = v[t][u];
+                static_cast<float *>(a.y)[at + tb.row + g] = v[t][2 + u];
+            }
+        }
+}
+
+template <bool PAL, bool GATED, int Q>
+__global__ void __launch_bounds__(256) k_expert_mma(const MmaExpertArgs a) {
+    extern __shared__ __align__(16) uint32_t smem_expert[];
+    const Span s = find_active(a.offsets, a.experts, a.places, int(blockIdx.y));
+    if (s.expert < 0) return;
+    uint32_t *f = smem_expert;
+    const int64_t row = int64_t(blockIdx.x) * (GATED ? 8 : 16);
+    const HalfTile<PAL> ta = half_tile<PAL>(a.a, s.expert, row, a.k, f, f + a.flag_words);
+    const HalfTile<PAL> tb = half_tile<PAL>(GATED ? a.b : a.a, s.expert, GATED ? row : row + 8, a.k, f + 2 * a.flag_words,
+                                            f + 3 * a.flag_words);
+    if (PAL) __syncthreads();
+    float *red = reinterpret_cast<float *>(f + 4 * a.flag_words);
+    for (int c0 = 0; c0 < s.rows; c0 += 16) {
+        const int m = min(16, s.rows - c0);
+        if (m > 8) expert_pass<PAL, GATED, 2, Q>(a, ta, tb, s.pos + c0, m, red);
+        else expert_pass<PAL, GATED, 1, Q>(a, ta, tb, s.pos + c0, m, red);
+    }
+}
+
+// ---------------------------------------------------------------- tcgen05
+
+constexpr int kBM = 128, kBK = 64;
+constexpr int kTcThreads = 384;       // W producer, MMA, X producer, spare, eight epilogue warps
+constexpr int kXTile = kBM * kBK * 2;
+constexpr int kSumSteps = 8;          // K-steps per FP32 chunk
+
+struct TcExpertArgs {
+    int experts, per_row, ksteps, stages;
+    int64_t places, x_rows, n;
+    const int32_t *offsets, *order;
+    void *y;
+    int64_t y_stride;
+    uint64_t timeout_ns;
+    uint32_t *status;
+};
+
+// 3-D tiled copy global -> shared (x innermost)
+__device__ __forceinline__ void tma_load_3d(void *dst, const CUtensorMap *map, int32_t x, int32_t y, int32_t z, uint64_t *bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
+            smem_addr(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_addr(bar))
+        : "memory");
+}
+
+// four rows of a 2-D tensor, one after the other in shared memory
+__device__ __forceinline__ void tma_gather4(void *dst, const CUtensorMap *map, int32_t x, const int32_t (&row)[4], uint64_t *bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5, "
+        "%6}], [%7];" ::"r"(smem_addr(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(row[0]), "r"(row[1]), "r"(row[2]), "r"(row[3]), "r"(smem_addr(bar))
+        : "memory");
+}
+
+// BN: weight rows per tile (gate_up: half of them of G, half of U)
+template <int BN, bool GATED>
+__global__ void __launch_bounds__(kTcThreads, 1)
+    k_expert_tc(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmA,
+                const __grid_constant__ CUtensorMap tmB, const TcExpertArgs a) {
+    constexpr int kW = BN * kBK * 2, kStage = kXTile + kW;
+    constexpr int kCols = GATED ? BN / 2 : BN;       // output columns per tile
+    extern __shared__ uint8_t smem_dyn[];
+    uint8_t *ring = smem_dyn + ((1024u - (smem_addr(smem_dyn) & 1023u)) & 1023u);
+    const int S = a.stages;
+    uint64_t *xfull = reinterpret_cast<uint64_t *>(ring + size_t(S) * kStage);
+    uint64_t *wfull = xfull + S, *empty = wfull + S, *accf = empty + S, *acce = accf + 2;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(acce + 2);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+    int32_t *first = reinterpret_cast<int32_t *>(tmem_slot + 2);     // [experts + 1] row tiles before each expert
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint64_t T = a.timeout_ns;
+    const int most = int(a.places);
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < S; s++) {
+            mbar_init(&xfull[s], 1);
+            mbar_init(&wfull[s], 1);
+            mbar_init(&empty[s], 1);
+        }
+        for (int b = 0; b < 2; b++) {
+            mbar_init(&accf[b], 1);
+            mbar_init(&acce[b], 8);
+        }
+        *abort_flag = 0;
+        fence_mbar_init();
+        prefetch_tensormap(&tmX);
+        prefetch_tensormap(&tmA);
+        if (GATED) prefetch_tensormap(&tmB);
+    }
+    if (warp == 1) {
+        tmem_alloc(tmem_slot, 2 * BN);
+        tmem_relinquish();
+    }
+    if (warp == 2) {
+        int run = 0;
+        for (int e0 = 0; e0 < a.experts; e0 += 32) {
+            int tiles = 0;
+            if (e0 + lane < a.experts) {
+                const int lo = min(max(__ldg(a.offsets + e0 + lane), 0), most);
+                const int hi = min(max(__ldg(a.offsets + e0 + lane + 1), 0), most);
+                tiles = (max(hi - lo, 0) + kBM - 1) / kBM;
+            }
+            int incl = tiles;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const int u = __shfl_up_sync(kAll, incl, d);
+                if (lane >= d) incl += u;
+            }
+            if (e0 + lane < a.experts) first[e0 + lane] = run + incl - tiles;
+            run += __shfl_sync(kAll, incl, 31);
+        }
+        if (lane == 0) first[a.experts] = run;
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    const int ntn = int((a.n + kCols - 1) / kCols);
+    const int64_t tiles = int64_t(first[a.experts]) * ntn;
+
+    // row tile mt -> expert (the last one with first[e] <= mt that has tiles), rows
+    auto locate = [&](int mt) {
+        int lo = 0, hi = a.experts;          // first[lo] <= mt < first[hi]
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (first[mid] <= mt) lo = mid;
+            else hi = mid;
+        }
+        const int p0 = min(max(__ldg(a.offsets + lo), 0), most), p1 = min(max(__ldg(a.offsets + lo + 1), 0), most);
+        const int skip = (mt - first[lo]) * kBM;
+        return Span{lo, p0 + skip, min(kBM, p1 - p0 - skip)};
+    };
+
+    if (warp == 0) {
+        // ------------------------------------------------ weights
+        if (lane == 0) {
+            int64_t it = 0;
+            bool ok = true;
+            for (int64_t tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x) {
+                const Span t = locate(int(tile / ntn));
+                const int n0 = int(tile % ntn) * kCols;
+                for (int ks = 0; ks < a.ksteps; ks++, it++) {
+                    const int s = int(it % S);
+                    if (it >= S) ok = mbar_wait_or_abort(&empty[s], (uint32_t(it / S) & 1u) ^ 1u, T, abort_flag);
+                    if (!ok || *abort_flag) {
+                        ok = false;
+                        break;
+                    }
+                    uint8_t *st = ring + size_t(s) * kStage + kXTile;
+                    mbar_arrive_expect_tx(&wfull[s], uint32_t(kW));
+                    if (GATED) {
+                        tma_load_3d(st, &tmA, ks * kBK, n0, t.expert, &wfull[s]);
+                        tma_load_3d(st + kW / 2, &tmB, ks * kBK, n0, t.expert, &wfull[s]);
+                    } else {
+                        tma_load_3d(st, &tmA, ks * kBK, n0, t.expert, &wfull[s]);
+                    }
+                }
+            }
+            if (!ok) {
+                if (!*abort_flag) flag_error(a.status, UW_DEVERR_TIMEOUT);
+                *abort_flag = 1;
+            }
+            for (int64_t i = max(int64_t(0), it - S); i < it; i++) mbar_wait(&wfull[i % S], uint32_t(i / S) & 1u, T);
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        // ------------------------------------------------ MMA
+        if (lane == 0) {
+            constexpr uint32_t idesc = idesc_bf16_f32(kBM, BN);
+            const int chunk = GATED ? a.ksteps : kSumSteps;
+            int64_t it = 0;
+            uint32_t acc = 0;
+            bool ok = true;
+            for (int64_t tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x) {
+                for (int k0 = 0; k0 < a.ksteps && ok; k0 += chunk, acc++) {
+                    const uint32_t b = acc & 1u;
+                    if (acc >= 2) ok = mbar_wait_or_abort(&acce[b], ((acc >> 1) & 1u) ^ 1u, T, abort_flag);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const int k1 = min(a.ksteps, k0 + chunk);
+                    for (int ks = k0; ks < k1; ks++, it++) {
+                        const int s = int(it % S);
+                        ok = mbar_wait_or_abort(&xfull[s], uint32_t(it / S) & 1u, T, abort_flag) &&
+                             mbar_wait_or_abort(&wfull[s], uint32_t(it / S) & 1u, T, abort_flag);
+                        if (!ok) break;
+                        tc_fence_after();
+                        const uint32_t sx = smem_addr(ring + size_t(s) * kStage), sw = sx + kXTile;
+#pragma unroll
+                        for (int kk = 0; kk < kBK / 16; kk++)
+                            tc_mma_bf16(tmem + b * BN, smem_desc_k128(sx + 32 * kk), smem_desc_k128(sw + 32 * kk), idesc,
+                                        (ks != k0 || kk) ? 1u : 0u);
+                        tc_commit(&empty[s]);
+                    }
+                    if (ok) tc_commit(&accf[b]);
+                }
+            }
+            if (!ok) {
+                if (!*abort_flag) flag_error(a.status, UW_DEVERR_TIMEOUT);
+                *abort_flag = 1;
+                // what was issued must end before TMEM is freed and shared memory goes away
+                tc_commit(&accf[acc & 1u]);
+                mbar_wait(&accf[acc & 1u], (acc >> 1) & 1u, T);
+            }
+        }
+        __syncwarp();
+    } else if (warp == 2) {
+        // ------------------------------------------------ rows of x, four per lane
+        int64_t it = 0;
+        bool ok = true;
+        for (int64_t tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x) {
+            const Span t = locate(int(tile / ntn));
+            int32_t row[4];
+#pragma unroll
+            for (int i = 0; i < 4; i++)
+                row[i] = int32_t(source_row(a.order, a.per_row, a.x_rows, t.pos + min(4 * lane + i, t.rows - 1)));
+            const uint32_t bytes = uint32_t((t.rows + 3) / 4) * 4u * kBK * 2u;
+            for (int ks = 0; ks < a.ksteps; ks++, it++) {
+                const int s = int(it % S);
+                if (it >= S) ok = mbar_wait_or_abort(&empty[s], (uint32_t(it / S) & 1u) ^ 1u, T, abort_flag);
+                ok = __all_sync(kAll, ok && !*abort_flag);
+                if (!ok) break;
+                if (lane == 0) mbar_arrive_expect_tx(&xfull[s], bytes);
+                __syncwarp();
+                if (4 * lane < t.rows)
+                    tma_gather4(ring + size_t(s) * kStage + 4 * lane * kBK * 2, &tmX, ks * kBK, row, &xfull[s]);
+            }
+        }
+        if (!ok && lane == 0) {
+            if (!*abort_flag) flag_error(a.status, UW_DEVERR_TIMEOUT);
+            *abort_flag = 1;
+        }
+        if (lane == 0)
+            for (int64_t i = max(int64_t(0), it - S); i < it; i++) mbar_wait(&xfull[i % S], uint32_t(i / S) & 1u, T);
+        __syncwarp();
+    } else if (warp >= 4) {
+        // ------------------------------------------------ epilogue: lane = token
+        const int q = warp & 3, half = (warp - 4) >> 2;
+        const uint32_t lane_base = tmem + (uint32_t(q * 32) << 16);
+        uint32_t acc = 0;
+        bool ok = true;
+        for (int64_t tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x) {
+            const Span t = locate(int(tile / ntn));
+            const int64_t n0 = (tile % ntn) * kCols;
+            const int tok = q * 32 + lane;
+            if constexpr (GATED) {
+                constexpr int kMine = kCols / 2;
+                const uint32_t b = acc & 1u;
+                ok = mbar_wait_or_abort(&accf[b], (acc >> 1) & 1u, T, abort_flag) && !*abort_flag;
+                ok = __all_sync(kAll, ok);
+                if (!ok) break;
+                tc_fence_after();
+                uint16_t *out = static_cast<uint16_t *>(a.y) + int64_t(t.pos + tok) * a.y_stride + n0;
+#pragma unroll 1
+                for (int c = half * kMine; c < (half + 1) * kMine; c += 16) {
+                    uint32_t gv[16], uv[16];
+                    tmem_ld16(lane_base + b * BN + c, gv);
+                    tmem_ld16(lane_base + b * BN + kCols + c, uv);
+                    tmem_ld_wait();
+                    if (tok < t.rows && n0 + c < a.n) {
+                        uint32_t o[8];
+#pragma unroll
+                        for (int i = 0; i < 8; i++) {
+                            const float h0 = silu(__uint_as_float(gv[2 * i])) * __uint_as_float(uv[2 * i]);
+                            const float h1 = silu(__uint_as_float(gv[2 * i + 1])) * __uint_as_float(uv[2 * i + 1]);
+                            const __nv_bfloat162 p = __floats2bfloat162_rn(h0, h1);
+                            o[i] = *reinterpret_cast<const uint32_t *>(&p);
+                        }
+                        *reinterpret_cast<uint4 *>(out + c) = make_uint4(o[0], o[1], o[2], o[3]);
+                        *reinterpret_cast<uint4 *>(out + c + 8) = make_uint4(o[4], o[5], o[6], o[7]);
+                    }
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&acce[b]);
+                acc++;
+            } else {
+                constexpr int kMine = BN / 2;
+                float sum[kMine];
+#pragma unroll
+                for (int i = 0; i < kMine; i++) sum[i] = 0.f;
+                for (int k0 = 0; k0 < a.ksteps; k0 += kSumSteps, acc++) {
+                    const uint32_t b = acc & 1u;
+                    ok = mbar_wait_or_abort(&accf[b], (acc >> 1) & 1u, T, abort_flag) && !*abort_flag;
+                    ok = __all_sync(kAll, ok);
+                    if (!ok) break;
+                    tc_fence_after();
+#pragma unroll
+                    for (int c = 0; c < kMine; c += 16) {
+                        uint32_t v[16];
+                        tmem_ld16(lane_base + b * BN + half * kMine + c, v);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int i = 0; i < 16; i++) sum[c + i] += __uint_as_float(v[i]);
+                    }
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&acce[b]);
+                }
+                if (!ok) break;
+                float *out = static_cast<float *>(a.y) + int64_t(t.pos + tok) * a.y_stride + n0 + half * kMine;
+                if (tok < t.rows) {
+#pragma unroll
+                    for (int c = 0; c < kMine; c += 4)
+                        if (n0 + half * kMine + c < a.n)
+                            *reinterpret_cast<float4 *>(out + c) = make_float4(sum[c], sum[c + 1], sum[c + 2], sum[c + 3]);
+                }
+            }
+        }
+        if (!ok && lane == 0) {
+            if (!*abort_flag) flag_error(a.status, UW_DEVERR_TIMEOUT);
+            *abort_flag = 1;
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 2 * BN);
+    }
+}
+
+// ---------------------------------------------------------------- join
+
+struct CombineArgs {
+    const float *y;
+    int64_t y_stride;
+    const int32_t *slot;
+    const float *weights;
+    int64_t t, places, n;
+    int top_k;
+    const float *base;
+    int64_t base_stride;
+    float *out;
+    int64_t out_stride;
+};
+
+// One token's columns in 16-byte pieces; the slots in order, so that the sum
+// does not vary.  The bytes of y bound it.
+__global__ void __launch_bounds__(256) k_expert_combine(const CombineArgs a) {
+    const int64_t t = blockIdx.x;
+    const int64_t c = (int64_t(blockIdx.y) * blockDim.x + threadIdx.x) * 4;
+    if (c >= a.n) return;
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (a.base) s = *reinterpret_cast<const float4 *>(a.base + t * a.base_stride + c);
+#pragma unroll 8
+    for (int i = 0; i < a.top_k; i++) {
+        const int32_t p = __ldg(a.slot + t * a.top_k + i);
+        if (p < 0 || p >= a.places) continue;
+        const float w = __ldg(a.weights + t * a.top_k + i);
+        const float4 v = __ldcs(reinterpret_cast<const float4 *>(a.y + int64_t(p) * a.y_stride + c));
+        s.x = fmaf(w, v.x, s.x);
+        s.y = fmaf(w, v.y, s.y);
+        s.z = fmaf(w, v.z, s.z);
+        s.w = fmaf(w, v.w, s.w);
+    }
+    *reinterpret_cast<float4 *>(a.out + t * a.out_stride + c) = s;
+}
+
+// ---------------------------------------------------------------- host side
+
+bool make_map(CUtensorMap *map, const void *base, int rank, const cuuint64_t *dims, const cuuint64_t *strides,
+              const cuuint32_t *box) {
+    EncodeTiledFn fn = encode_tiled_fn();
+    if (!fn) return false;
+    const cuuint32_t estr[3] = {1, 1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, cuuint32_t(rank), const_cast<void *>(base), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// all experts' matrices as one [experts, n, k] tensor, boxes of `rows` x 64
+bool weight_map(CUtensorMap *map, const ExpertSet &s, int experts, int64_t n, int64_t k, int rows) {
+    const cuuint64_t dims[3] = {cuuint64_t(k), cuuint64_t(n), cuuint64_t(experts)};
+    const cuuint64_t strides[2] = {cuuint64_t(k) * 2, cuuint64_t(s.stride) * 2};
+    const cuuint32_t box[3] = {kBK, cuuint32_t(rows), 1};
+    return make_map(map, s.w, 3, dims, strides, box);
+}
+
+template <int BN, bool GATED>
+cudaError_t launch_tc(const ExpertLaunch &p, cudaStream_t stream) {
+    constexpr int kStage = kXTile + BN * kBK * 2;
+    constexpr int kMaxSmem = 232448;
+    const int tail = 1024 + 64 + (p.experts + 4) * 4;
+    const int stages = std::min(8, (kMaxSmem - tail) / (kStage + 24));
+    if (stages < 2) return cudaErrorInvalidValue;
+    const size_t smem = size_t(stages) * (kStage + 24) + tail;
+    CUtensorMap mx, ma, mb;
+    const cuuint64_t xd[2] = {cuuint64_t(p.k), cuuint64_t(p.x_rows)};
+    const cuuint64_t xs[1] = {cuuint64_t(p.x_stride) * 2};
+    const cuuint32_t xb[2] = {kBK, 1};               // a gather's box is one row
+    const int rows = GATED ? BN / 2 : BN;
+    if (!make_map(&mx, p.x, 2, xd, xs, xb) || !weight_map(&ma, p.a, p.experts, p.n, p.k, rows)) return cudaErrorInvalidValue;
+    mb = ma;
+    if (GATED && !weight_map(&mb, p.b, p.experts, p.n, p.k, rows)) return cudaErrorInvalidValue;
+    int dev = 0;
+    cudaError_t err = cudaGetDevice(&dev);
+    if (err != cudaSuccess) return err;
+    static std::atomic<uint64_t> ready{0};           // devices whose shared-memory limit is raised
+    if (dev >= 64 || !(ready.load(std::memory_order_acquire) >> dev & 1u)) {
+        err = cudaFuncSetAttribute(k_expert_tc<BN, GATED>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
+        if (err != cudaSuccess) return err;
+        if (dev < 64) ready.fetch_or(uint64_t(1) << dev, std::memory_order_release);
+    }
+    TcExpertArgs a{};
+    a.experts = p.experts;
+    a.per_row = p.per_row;
+    a.ksteps = int(p.k / kBK);
+    a.stages = stages;
+    a.places = p.places;
+    a.x_rows = p.x_rows;
+    a.n = p.n;
+    a.offsets = p.offsets;
+    a.order = p.order;
+    a.y = p.y;
+    a.y_stride = p.y_stride;
+    a.timeout_ns = p.timeout_ns;
+    a.status = p.status;
+    const int64_t row_tiles = (p.places + (kBM - 1) * std::min<int64_t>(p.experts, p.places)) / kBM;
+    const int64_t tiles = row_tiles * ((p.n + (GATED ? BN / 2 : BN) - 1) / (GATED ? BN / 2 : BN));
+    const unsigned grid = unsigned(std::min<int64_t>(sm_count(), tiles));
+    k_expert_tc<BN, GATED><<<grid, kTcThreads, smem, stream>>>(mx, ma, mb, a);
+    return cudaGetLastError();
+}
+
+template <bool PAL, bool GATED>
+cudaError_t launch_mma(const ExpertLaunch &p, cudaStream_t stream) {
+    MmaExpertArgs a{};
+    a.a = SetArgs{p.a.w, p.a.stride, static_cast<const Planes *>(p.a.table)};
+    a.b = SetArgs{p.b.w, p.b.stride, static_cast<const Planes *>(p.b.table)};
+    a.x = p.x;
+    a.x_rows = p.x_rows;
+    a.x_stride = p.x_stride;
+    a.n = p.n;
+    a.k = p.k;
+    a.experts = p.experts;
+    a.places = p.places;
+    a.per_row = p.per_row;
+    a.offsets = p.offsets;
+    a.order = p.order;
+    a.y = p.y;
+    a.y_stride = p.y_stride;
+    if (PAL) a.flag_words = int(((8 * (p.k / kGroup)) >> 5) + 2);
+    const int q = p.width == 1 ? 1 : p.width == 2 ? 2 : (p.k % 128 == 0 ? 2 : 1);
+    const size_t smem = size_t(4 * a.flag_words) * 4 + (p.slices > 1 ? size_t(p.slices) * 32 * 8 * 4 : 0);
+    if (smem > 48 * 1024) return cudaErrorInvalidValue;
+    const dim3 grid(unsigned(p.n / (GATED ? 8 : 16)), unsigned(std::min<int64_t>(p.experts, p.places)));
+    const dim3 block(unsigned(p.slices * 32));
+    if (q == 2) k_expert_mma<PAL, GATED, 2><<<grid, block, smem, stream>>>(a);
+    else k_expert_mma<PAL, GATED, 1><<<grid, block, smem, stream>>>(a);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+size_t expert_entry_bytes() { return sizeof(Planes); }
+
+void expert_fill_entry(void *entry, const uw_dmat &w) {
+    Planes p{};
+    p.sm = w.sm;
+    p.pal = reinterpret_cast<const uint32_t *>(w.pal);
+    p.flagbits = w.flagbits;
+    p.rawbase = w.rawbase;
+    p.rawexp = w.rawexp;
+    p.palette = make_palette16(w.palette);
+    memcpy(entry, &p, sizeof(p));
+}
+
+cudaError_t launch_expert(const ExpertLaunch &p, cudaStream_t stream) {
+    if (p.kernel == UW_KERNEL_MMA) {
+        if (p.a.table) return p.gated ? launch_mma<true, true>(p, stream) : launch_mma<true, false>(p, stream);
+        return p.gated ? launch_mma<false, true>(p, stream) : launch_mma<false, false>(p, stream);
+    }
+    if (p.bn == 128) return p.gated ? launch_tc<128, true>(p, stream) : launch_tc<128, false>(p, stream);
+    return p.gated ? launch_tc<256, true>(p, stream) : launch_tc<256, false>(p, stream);
+}
+
+cudaError_t launch_expert_combine(const CombineLaunch &p, cudaStream_t stream) {
+    CombineArgs a{p.y, p.y_stride, p.slot, p.weights, p.t, p.t * p.top_k, p.n, p.top_k, p.base, p.base_stride, p.out, p.out_stride};
+    const dim3 grid(unsigned(p.t), unsigned((p.n / 4 + 255) / 256));
+    k_expert_combine<<<grid, 256, 0, stream>>>(a);
+    return cudaGetLastError();
+}
+
+}  // namespace uw

@@ -262,6 +262,47 @@ struct LoraLaunch {
 };
 cudaError_t launch_lora(const LoraLaunch &p, cudaStream_t stream);
 
+// Routed rows times their experts' weights (expert.cu).
+struct ExpertSet {
+    const uint16_t *w;         // plain BF16, expert e at w + e * stride
+    int64_t stride;
+    const void *table;         // compressed: entries of expert_entry_bytes(), on the device
+};
+struct ExpertLaunch {
+    ExpertSet a, b;            // gated: gate and up matrices
+    bool gated;
+    int experts;
+    int64_t n, k;
+    const uint16_t *x;
+    int64_t x_rows, x_stride;
+    int64_t places;            // routed slots
+    int per_row;
+    const int32_t *offsets, *order;   // order may be null: row j of x is place j's
+    void *y;                   // float, gated: BF16
+    int64_t y_stride;
+    int kernel;                // UW_KERNEL_MMA or UW_KERNEL_TC
+    int slices, width;         // MMA
+    int bn;                    // TC
+    uint64_t timeout_ns;
+    uint32_t *status;
+};
+size_t expert_entry_bytes();
+void expert_fill_entry(void *entry, const uw_dmat &w);
+cudaError_t launch_expert(const ExpertLaunch &p, cudaStream_t stream);
+struct CombineLaunch {
+    const float *y;
+    int64_t y_stride;
+    const int32_t *slot;
+    const float *weights;
+    int64_t t, n;
+    int top_k;
+    const float *base;
+    int64_t base_stride;
+    float *out;
+    int64_t out_stride;
+};
+cudaError_t launch_expert_combine(const CombineLaunch &p, cudaStream_t stream);
+
 // Fixed-order sum of split-K partials: y[i] = sum_s partial[s][i], s ascending.
 cudaError_t launch_splitk_reduce(const float *partial, int split_k, int64_t count, float *y,
                                  cudaStream_t stream);

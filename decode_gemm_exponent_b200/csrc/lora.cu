@@ -31,6 +31,7 @@
 
 #include "device_common.cuh"
 #include "kernels.h"
+#include "mma_tile.cuh"
 
 namespace uw {
 namespace {
@@ -105,15 +106,6 @@ __device__ __forceinline__ Tile find_tile(const LoraArgs &a, int size, int64_t t
 __device__ __forceinline__ int rank_of(const LoraArgs &a, int group) {
     if (group >= a.groups) return 0;
     return a.ranks ? min(max(__ldg(a.ranks + group), 0), a.max_rank) : a.max_rank;
-}
-
-__device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                          uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 "
-        "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
 // ---------------------------------------------------------------- V = A x

@@ -34,6 +34,7 @@ PIPE_DECODE_GEMM, PIPE_DECODE_EXP_FUSED, PIPE_TRANSCODE_FUSED, PIPE_DIRECT_PALET
 KERNEL_FMA, KERNEL_TC, KERNEL_MMA, KERNEL_TC_SK, KERNEL_MMA_SK = 1, 2, 3, 4, 5
 DEBUG_NEVER_ARRIVE = 1
 MAX_GROUPS, MAX_TOP_K = 1024, 32
+EXPERT_ENTRY_BYTES = 64
 TYPE_F32, TYPE_BF16 = 1, 2
 SCORES = {"softmax": 1, "sigmoid": 2}
 GROUP_SCORES = {"max": 1, "top2": 2}
@@ -46,7 +47,8 @@ EXPORTS = ("uw_status_str", "uw_version", "uw_encode", "uw_blob_data", "uw_blob_
            "uw_fused_matmul_noalloc", "uw_stack_workspace_size", "uw_stack_run",
            "uw_sm_split_create", "uw_sm_split_get", "uw_sm_split_destroy", "uw_stack_tune_split",
            "uw_fused_matmul_batched", "uw_route_workspace_size", "uw_route_experts", "uw_group_workspace_size",
-           "uw_group_rows", "uw_lora_workspace_size", "uw_lora_add")
+           "uw_group_rows", "uw_lora_workspace_size", "uw_lora_add", "uw_expert_table", "uw_expert_plan_default",
+           "uw_expert_matmul", "uw_expert_gate_up", "uw_expert_combine")
 
 
 class UwError(RuntimeError):
@@ -107,6 +109,17 @@ class Router(ctypes.Structure):
                 ("renormalize", ctypes.c_int32), ("logits_type", ctypes.c_int32), ("scale", ctypes.c_float)]
 
 
+class ExpertSetArgs(ctypes.Structure):
+    _fields_ = [("n", ctypes.c_int64), ("k", ctypes.c_int64), ("experts", ctypes.c_int32), ("w_dev", ctypes.c_void_p),
+                ("stride", ctypes.c_int64), ("table_dev", ctypes.c_void_p)]
+
+
+class ExpertRows(ctypes.Structure):
+    _fields_ = [("places", ctypes.c_int64), ("per_row", ctypes.c_int32), ("offsets_dev", ctypes.c_void_p),
+                ("order_dev", ctypes.c_void_p), ("x_dev", ctypes.c_void_p), ("x_rows", ctypes.c_int64),
+                ("x_stride", ctypes.c_int64)]
+
+
 class Adapters(ctypes.Structure):
     _fields_ = [("n", ctypes.c_int64), ("k", ctypes.c_int64), ("count", ctypes.c_int32), ("max_rank", ctypes.c_int32),
                 ("a_dev", ctypes.c_void_p), ("b_dev", ctypes.c_void_p), ("ranks_dev", ctypes.c_void_p),
@@ -158,6 +171,13 @@ def lib() -> ctypes.CDLL:
         "uw_group_rows": (ctypes.c_int, [P, I64, I32, I32, P, P, P, P, SZ, P]),
         "uw_lora_workspace_size": (ctypes.c_int, [I64, ctypes.POINTER(Adapters), ctypes.POINTER(SZ)]),
         "uw_lora_add": (ctypes.c_int, [P, I64, I64, ctypes.POINTER(Adapters), P, P, P, P, I64, P, I64, P, SZ, P]),
+        "uw_expert_table": (ctypes.c_int, [ctypes.POINTER(ctypes.POINTER(DMat)), I32, P, SZ]),
+        "uw_expert_plan_default": (ctypes.c_int, [ctypes.POINTER(ExpertSetArgs), I64, ctypes.POINTER(Plan)]),
+        "uw_expert_matmul": (ctypes.c_int, [ctypes.POINTER(ExpertRows), ctypes.POINTER(ExpertSetArgs), P, I64,
+                                            ctypes.POINTER(Plan), P, P]),
+        "uw_expert_gate_up": (ctypes.c_int, [ctypes.POINTER(ExpertRows), ctypes.POINTER(ExpertSetArgs),
+                                             ctypes.POINTER(ExpertSetArgs), P, I64, ctypes.POINTER(Plan), P, P]),
+        "uw_expert_combine": (ctypes.c_int, [P, I64, P, P, I64, I32, I64, P, I64, P, I64, P]),
         "uw_sm_split_create": (ctypes.c_int, [ctypes.c_int, ctypes.c_int, ctypes.POINTER(P)]),
         "uw_sm_split_get": (ctypes.c_int, [P, ctypes.POINTER(P), ctypes.POINTER(P), ctypes.POINTER(ctypes.c_int),
                                            ctypes.POINTER(ctypes.c_int)]),
@@ -584,6 +604,137 @@ def group_rows(ids, groups: int, out: Optional[Grouping] = None, stream=None) ->
         check(lib().uw_group_rows(ids.data_ptr(), rows, per_row, groups, out.offsets.data_ptr(), out.order.data_ptr(),
                                   None if out.slot is None else out.slot.data_ptr(),
                                   out.ws.data_ptr() if size.value else None, size.value, _stream_handle()), "uw_group_rows")
+    return out
+
+
+class ExpertSet:
+    """The palette-form matrices of one projection of all experts as one
+    compressed set (uw_expert_table).  Keeps the matrices alive."""
+
+    def __init__(self, mats: Sequence[Matrix]):
+        import torch
+        self.mats = list(mats)
+        arr = (ctypes.POINTER(DMat) * len(mats))(*[ctypes.pointer(m.dmat) for m in mats])
+        host = np.zeros(max(1, len(mats)) * EXPERT_ENTRY_BYTES, np.uint8)
+        check(lib().uw_expert_table(arr, len(mats), host.ctypes.data, host.size), "uw_expert_table")
+        device = mats[0].dev.device
+        if any(m.dev.device != device for m in mats):
+            raise ValueError("the experts' matrices are on different devices")
+        self.table = torch.from_numpy(host).to(device)
+        self.experts, self.n, self.k, self.device = len(mats), mats[0].n, mats[0].k, device
+
+
+def _expert_set(w, name, like) -> ExpertSetArgs:
+    if isinstance(w, ExpertSet):
+        if w.device != like.device:
+            raise ValueError("%s: on %s, expected %s" % (name, w.device, like.device))
+        return ExpertSetArgs(w.n, w.k, w.experts, None, 0, w.table.data_ptr())
+    if w.dim() != 3 or w.dtype not in _bits():
+        raise ValueError("%s: an ExpertSet or BF16 [experts, n, k]" % name)
+    e, n, k = w.shape
+    if w.device != like.device:
+        raise ValueError("%s: on %s, expected %s" % (name, w.device, like.device))
+    if w.stride(2) != 1 or w.stride(1) != k or (e > 1 and w.stride(0) < n * k):
+        raise ValueError("%s: each expert's matrix must be contiguous" % name)
+    return ExpertSetArgs(n, k, e, w.data_ptr(), w.stride(0) if e > 1 else n * k, None)
+
+
+def _expert_rows(x, grouping: Grouping, set_: ExpertSetArgs, gather: bool) -> ExpertRows:
+    import torch
+    places = grouping.order.numel()
+    if x.dim() != 2:
+        raise ValueError("x: [rows, k]")
+    _need(x, "x", (x.shape[0], set_.k), _bits(), x, rows=True)
+    _need(grouping.offsets, "offsets", (set_.experts + 1,), (torch.int32,), x)
+    _need(grouping.order, "order", (places,), (torch.int32,), x)
+    rows = x.shape[0]
+    if gather:
+        if (rows == 0) != (places == 0) or (rows and places % rows):
+            raise ValueError("x: %d rows do not share %d routed slots evenly" % (rows, places))
+        per_row = places // rows if rows else 1
+    else:
+        if rows != places:
+            raise ValueError("x: %d rows in expert order, expected %d" % (rows, places))
+        per_row = 1
+    return ExpertRows(places, per_row, grouping.offsets.data_ptr(), grouping.order.data_ptr() if gather else None,
+                      x.data_ptr(), rows, x.stride(0) if rows > 1 else set_.k)
+
+
+def expert_plan_default(w, places: int) -> Plan:
+    """uw_expert_plan_default for an ExpertSet or a BF16 [experts, n, k] tensor."""
+    p = Plan()
+    a = _expert_set(w, "w", w)
+    check(lib().uw_expert_plan_default(ctypes.byref(a), places, ctypes.byref(p)), "uw_expert_plan_default")
+    return p
+
+
+def expert_matmul(x, w, routing: Grouping, *, gather: bool = False, plan: Optional[Plan] = None, out=None, status=None,
+                  stream=None):
+    """uw_expert_matmul: float32 [places, n] in expert order.  w: an ExpertSet or
+    BF16 [experts, n, k].  x: rows in expert order, or with gather=True one row
+    per token (the routed slots of a token share its row)."""
+    import torch
+    a = _expert_set(w, "w", x)
+    r = _expert_rows(x, routing, a, gather)
+    with _enter(x, stream):
+        if out is None:
+            out = torch.empty(r.places, a.n, dtype=torch.float32, device=x.device)
+        else:
+            _need(out, "out", (r.places, a.n), (torch.float32,), x, rows=True)
+        if plan is None:
+            plan = Plan()
+            check(lib().uw_expert_plan_default(ctypes.byref(a), r.places, ctypes.byref(plan)), "uw_expert_plan_default")
+        check(lib().uw_expert_matmul(ctypes.byref(r), ctypes.byref(a), out.data_ptr(),
+                                     out.stride(0) if r.places > 1 else a.n, ctypes.byref(plan), _ptr(status),
+                                     _stream_handle()), "uw_expert_matmul")
+    return out
+
+
+def expert_gate_up(x, gate, up, routing: Grouping, *, gather: bool = True, plan: Optional[Plan] = None, out=None,
+                   status=None, stream=None):
+    """uw_expert_gate_up: bfloat16 [places, n] in expert order, the routed
+    experts' silu(gate x) * (up x); gate and up as expert_matmul's w."""
+    import torch
+    a, b = _expert_set(gate, "gate", x), _expert_set(up, "up", x)
+    if (a.n, a.k, a.experts) != (b.n, b.k, b.experts):
+        raise ValueError("gate and up have different sizes")
+    r = _expert_rows(x, routing, a, gather)
+    with _enter(x, stream):
+        if out is None:
+            out = torch.empty(r.places, a.n, dtype=torch.bfloat16, device=x.device)
+        else:
+            _need(out, "out", (r.places, a.n), _bits(), x, rows=True)
+        if plan is None:
+            plan = Plan()
+            check(lib().uw_expert_plan_default(ctypes.byref(a), r.places, ctypes.byref(plan)), "uw_expert_plan_default")
+        check(lib().uw_expert_gate_up(ctypes.byref(r), ctypes.byref(a), ctypes.byref(b), out.data_ptr(),
+                                      out.stride(0) if r.places > 1 else a.n, ctypes.byref(plan), _ptr(status),
+                                      _stream_handle()), "uw_expert_gate_up")
+    return out
+
+
+def expert_combine(y, routing: Routing, *, base=None, out=None, stream=None):
+    """uw_expert_combine: float32 [t, n], each token's weighted sum of its
+    slots' rows of y (float32 [places, n] in expert order), plus base."""
+    import torch
+    t, top_k = routing.slot.shape
+    if y.dim() != 2:
+        raise ValueError("y: [places, n]")
+    n = y.shape[1]
+    _need(y, "y", (t * top_k, n), (torch.float32,), y, rows=True)
+    _need(routing.slot, "slot", (t, top_k), (torch.int32,), y)
+    _need(routing.weights, "weights", (t, top_k), (torch.float32,), y)
+    if base is not None:
+        _need(base, "base", (t, n), (torch.float32,), y, rows=True)
+    row = (lambda v: v.stride(0) if v.shape[0] > 1 else n)
+    with _enter(y, stream):
+        if out is None:
+            out = torch.empty(t, n, dtype=torch.float32, device=y.device)
+        else:
+            _need(out, "out", (t, n), (torch.float32,), y, rows=True)
+        check(lib().uw_expert_combine(y.data_ptr(), row(y), routing.slot.data_ptr(), routing.weights.data_ptr(), t, top_k, n,
+                                      _ptr(base), 0 if base is None else row(base), out.data_ptr(), row(out),
+                                      _stream_handle()), "uw_expert_combine")
     return out
 
 

@@ -534,6 +534,72 @@ uw_status uw_group_rows(const int32_t *ids_dev, int64_t rows, int32_t per_row, i
                         int32_t *order_dev, int32_t *slot_dev, void *ws, size_t ws_bytes, void *stream);
 
 /* ------------------------------------------------------------------------ */
+/* Products of routed rows with their experts' weights.  The token counts are  */
+/* the router's offsets on the device: nothing is copied to the host between.  */
+
+/* One projection of all experts, either plain BF16 or compressed. */
+typedef struct uw_expert_set {
+    int64_t n, k;             /* of every expert's matrix, multiples of 64            */
+    int32_t experts;          /* 1..UW_MAX_GROUPS                                     */
+    const uint16_t *w_dev;    /* BF16: expert e's [n, k] at w_dev + e * stride,
+                                 16-byte aligned; NULL for a compressed set           */
+    int64_t stride;           /* elements between experts, >= n * k, a multiple of 8  */
+    const void *table_dev;    /* compressed: device copy of what uw_expert_table
+                                 filled, 16-byte aligned; NULL for a plain set        */
+} uw_expert_set;
+
+#define UW_EXPERT_ENTRY_BYTES 64
+
+/* Fill table[experts * UW_EXPERT_ENTRY_BYTES] (host memory) for a compressed set:
+ * entry e describes mats[e], a bound matrix in palette form (UW_EMIT_PALETTE), all
+ * of the same n and k.  The caller copies the table to the device once and keeps
+ * the matrices' device blobs.                                                      */
+uw_status uw_expert_table(const uw_dmat *const *mats, int32_t experts, void *table, size_t table_bytes);
+
+/* Plan of the calls below: UW_KERNEL_MMA (any set; bn warps 1..8 split K, stages as
+ * in uw_plan), made for few rows per expert, and UW_KERNEL_TC (plain sets; bn = 128
+ * or 256 weight rows per tile), for many.  pipeline is UW_PIPE_DIRECT_PALETTE (not
+ * used by plain sets), split_k 1, stages 0 for TC.  The default decides by the rows
+ * per expert.  places: routed slots, t * top_k.                                    */
+uw_status uw_expert_plan_default(const uw_expert_set *w, int64_t places, uw_plan *plan);
+
+/* The routed rows: place j of the order (offsets and order as uw_route_experts or
+ * uw_group_rows wrote them) belongs to the expert e with offsets[e] <= j <
+ * offsets[e + 1].  Its row of x is order[j] / per_row, or j where order_dev is NULL
+ * (x is in expert order already).  Outputs are in expert order, one row per place;
+ * rows of places that belong to no expert are left as they were.
+ * x_dev: BF16 [x_rows, k], rows x_stride apart (>= k, a multiple of 8), 16-byte
+ * aligned.  dev_status: device uint32 for kernel error bits, may be NULL.
+ * places >= 0; 0 launches nothing.  Argument errors as in uw_fused_matmul.          */
+typedef struct uw_expert_rows {
+    int64_t places;           /* t * top_k, < 2^31                                    */
+    int32_t per_row;          /* top_k                                                */
+    const int32_t *offsets_dev, *order_dev;
+    const uint16_t *x_dev;
+    int64_t x_rows, x_stride;
+} uw_expert_rows;
+
+/* y[j] = W_e x: float [places, n], rows y_stride apart (>= n, a multiple of 4),
+ * 16-byte aligned.  A compressed set's result is bit-identical to the plain set's
+ * with the same plan.  Sums are kept in 32 bits.                                   */
+uw_status uw_expert_matmul(const uw_expert_rows *rows, const uw_expert_set *w, float *y_dev, int64_t y_stride,
+                           const uw_plan *plan, uint32_t *dev_status, void *stream);
+
+/* h[j] = silu(G_e x) * (U_e x) with silu(g) = g / (1 + exp(-g)), rounded once to
+ * BF16: [places, n], rows h_stride apart (>= n, a multiple of 8), 16-byte aligned.
+ * gate and up: sets of the same sizes and form.                                    */
+uw_status uw_expert_gate_up(const uw_expert_rows *rows, const uw_expert_set *gate, const uw_expert_set *up, uint16_t *h_dev,
+                            int64_t h_stride, const uw_plan *plan, uint32_t *dev_status, void *stream);
+
+/* out[i] = (base[i] +) sum over s < top_k of weights[i, s] * y[slot[i, s]], in that
+ * order; slots of -1 add nothing.  y: float [t * top_k, n] in expert order; base_dev
+ * (float [t, n], may be NULL, may be out_dev) is for a shared expert's output or a
+ * residual.  n a multiple of 4, strides >= n and multiples of 4, 16-byte aligned.   */
+uw_status uw_expert_combine(const float *y_dev, int64_t y_stride, const int32_t *slot_dev, const float *weights_dev,
+                            int64_t t, int32_t top_k, int64_t n, const float *base_dev, int64_t base_stride,
+                            float *out_dev, int64_t out_stride, void *stream);
+
+/* ------------------------------------------------------------------------ */
 /* Low-rank adapters of many requests beside a shared projection.             */
 
 /* The adapters of one projection, in slots of equal size. */

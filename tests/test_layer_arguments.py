@@ -92,3 +92,88 @@ def test_lora(uw):
     for kw in (dict(ws=None), dict(ws=FAKE + 16), dict(nbytes=size.value - 1)):
         assert run(**kw) == uw.ERR_WORKSPACE, kw
     assert run(t=0, x=None, ids=None, y=None, out=None, ws=None, nbytes=0) == uw.UW_OK    # nothing to launch
+
+
+def test_expert_calls(uw):
+    L = uw.lib()
+
+    def rows(places=16, per_row=2, off=FAKE, order=FAKE, x=FAKE, x_rows=8, xs=128):
+        return uw.ExpertRows(places, per_row, off, order, x, x_rows, xs)
+
+    def wset(n=64, k=128, e=4, w=FAKE, stride=64 * 128, table=None):
+        return uw.ExpertSetArgs(n, k, e, w, stride, table)
+
+    ok = uw.make_plan(uw.PIPE_DIRECT_PALETTE, uw.KERNEL_MMA, 4)
+
+    def run(r=None, w=None, y=FAKE, ys=64, plan=ok):
+        r, w = r or rows(), w or wset()
+        return L.uw_expert_matmul(ctypes.byref(r), ctypes.byref(w), y, ys, ctypes.byref(plan), None, None)
+
+    assert run(rows(places=0, off=None, order=None, x=None, x_rows=0)) == uw.UW_OK
+    for r in (rows(places=-1), rows(per_row=0), rows(off=None), rows(x=None), rows(x_rows=0), rows(order=None), rows(xs=120),
+              rows(xs=132), rows(x=FAKE + 8), rows(off=FAKE + 2)):
+        assert run(r) == uw.ERR_INVALID_ARG
+    assert run(rows(places=1 << 31)) == uw.ERR_UNSUPPORTED_SHAPE
+    for w, status in ((wset(n=0), 1), (wset(n=96), 2), (wset(k=100), 2), (wset(e=0), 1), (wset(e=1025), 1), (wset(w=None), 1),
+                      (wset(table=FAKE), 1), (wset(w=FAKE + 8), 1), (wset(stride=64 * 127), 1), (wset(stride=64 * 128 + 4), 1),
+                      (wset(w=None, table=FAKE + 8), 1)):
+        assert run(w=w) == status
+    assert run(y=None) == uw.ERR_INVALID_ARG and run(y=FAKE + 8) == uw.ERR_INVALID_ARG
+    assert run(ys=60) == uw.ERR_INVALID_ARG and run(ys=66) == uw.ERR_INVALID_ARG
+    for plan in (uw.make_plan(4, uw.KERNEL_MMA, 0), uw.make_plan(4, uw.KERNEL_MMA, 9), uw.make_plan(4, uw.KERNEL_MMA, 4, 2),
+                 uw.make_plan(4, uw.KERNEL_MMA, 4, 1, 3), uw.make_plan(4, uw.KERNEL_TC, 64), uw.make_plan(4, uw.KERNEL_TC, 256, 1, 4),
+                 uw.make_plan(4, uw.KERNEL_TC_SK, 16), uw.make_plan(1, uw.KERNEL_MMA, 4), uw.make_plan(4, uw.KERNEL_MMA, 4, timeout_ns=-1)):
+        assert run(plan=plan) == uw.ERR_INVALID_ARG
+    assert run(w=wset(k=192, stride=64 * 192), r=rows(xs=192), plan=uw.make_plan(4, uw.KERNEL_MMA, 4, 1, 2)) == uw.ERR_INVALID_ARG
+    tc = uw.make_plan(4, uw.KERNEL_TC, 256)
+    assert run(w=wset(w=None, table=FAKE), plan=tc) == uw.ERR_INVALID_ARG
+
+    def gate_up(a, b, hs=64):
+        r = rows()
+        return L.uw_expert_gate_up(ctypes.byref(r), ctypes.byref(a), ctypes.byref(b) if b else None, FAKE, hs, ctypes.byref(ok),
+                                   None, None)
+    for b in (None, wset(n=128, stride=1 << 20), wset(k=64), wset(e=5), wset(w=None, table=FAKE)):
+        assert gate_up(wset(), b) == uw.ERR_INVALID_ARG
+    assert gate_up(wset(), wset(), 68) == uw.ERR_INVALID_ARG
+
+    p = uw.Plan()
+    for w, places, kernel in ((wset(), 8, uw.KERNEL_MMA), (wset(), 100000, uw.KERNEL_TC),
+                              (wset(w=None, table=FAKE), 100000, uw.KERNEL_MMA)):
+        assert L.uw_expert_plan_default(ctypes.byref(w), places, ctypes.byref(p)) == 0 and p.kernel == kernel
+    assert L.uw_expert_plan_default(ctypes.byref(wset()), -1, ctypes.byref(p)) == uw.ERR_INVALID_ARG
+    assert L.uw_expert_plan_default(ctypes.byref(wset()), 1, None) == uw.ERR_INVALID_ARG
+
+
+def test_expert_table(uw):
+    import numpy as np
+    from decode_gemm_exponent_b200 import synth
+    L = uw.lib()
+    dms = []
+    for n, flags in ((64, 0), (64, 0), (128, 0), (64, uw.EMIT_HUFFMAN)):
+        host = np.frombuffer(uw.encode(synth.weights_bf16(n, 128, 0.02, 0.002, 1.0, seed=n), flags), np.uint8)
+        dm = uw.DMat()
+        uw.check(L.uw_matrix_bind(host.ctypes.data, host.size, FAKE, FAKE, 0, ctypes.byref(dm)), "uw_matrix_bind")
+        dms.append(dm)
+    arr = lambda *i: (ctypes.POINTER(uw.DMat) * len(i))(*[ctypes.pointer(dms[j]) for j in i])
+    table = np.zeros(4 * uw.EXPERT_ENTRY_BYTES, np.uint8)
+    run = lambda a, n, size=table.size: L.uw_expert_table(a, n, table.ctypes.data, size)
+    assert run(arr(0, 1), 2) == uw.UW_OK and table.any()
+    assert run(arr(0, 1), 2, 127) == uw.ERR_WORKSPACE
+    assert run(arr(0, 2), 2) == uw.ERR_INVALID_ARG           # another size
+    assert run(arr(0, 3), 2) == uw.ERR_INVALID_ARG           # no palette plane
+    assert run(arr(0), 0) == uw.ERR_INVALID_ARG
+    assert run(None, 1) == uw.ERR_INVALID_ARG
+
+
+def test_expert_combine(uw):
+    L = uw.lib()
+
+    def run(y=FAKE, ys=64, slot=FAKE, w=FAKE, t=8, k=2, n=64, base=None, bs=0, out=FAKE, os_=64):
+        return L.uw_expert_combine(y, ys, slot, w, t, k, n, base, bs, out, os_, None)
+    assert run(t=0, y=None, slot=None, w=None, out=None) == uw.UW_OK
+    for kw in (dict(t=-1), dict(k=0), dict(n=0), dict(ys=60), dict(ys=66), dict(os_=60), dict(y=None), dict(slot=None),
+               dict(w=None), dict(out=None), dict(y=FAKE + 4), dict(out=FAKE + 8), dict(base=FAKE, bs=60),
+               dict(base=FAKE + 4, bs=64), dict(base=FAKE, bs=68), dict(slot=FAKE + 2)):
+        assert run(**kw) == uw.ERR_INVALID_ARG, kw
+    assert run(n=66, ys=68, os_=68) == uw.ERR_UNSUPPORTED_SHAPE
+    assert run(t=1 << 31) == uw.ERR_UNSUPPORTED_SHAPE
