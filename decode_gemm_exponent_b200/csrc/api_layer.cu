@@ -55,8 +55,29 @@ uw_status check_set(const uw_expert_set *s) {
     return UW_OK;
 }
 
+uw_status check_expert_plan(const uw_expert_plan *p, const uw_expert_set *w) {
+    if (!p || p->timeout_ns < 0) return UW_ERR_INVALID_ARG;
+    if (p->kernel == UW_KERNEL_MMA) {
+        if (p->bn < 1 || p->bn > 8 || p->width < 0 || p->width > 2 || (p->width == 2 && w->k % 128) || p->rows || p->sort)
+            return UW_ERR_INVALID_ARG;
+        // the raw-group bitmaps of a tile of rows are staged in 48 KB
+        if (w->table_dev && w->k > 131072) return UW_ERR_UNSUPPORTED_SHAPE;
+    } else if (p->kernel == UW_KERNEL_TC) {
+        if (!w->w_dev || (p->bn != 128 && p->bn != 256) || p->width) return UW_ERR_INVALID_ARG;
+        if (p->rows != 32 && p->rows != 64 && p->rows != 128) return UW_ERR_INVALID_ARG;
+        if (w->stride >= int64_t(1) << 39) return UW_ERR_UNSUPPORTED_SHAPE;   // a tensor map's largest stride
+    } else {
+        return UW_ERR_INVALID_ARG;
+    }
+    return UW_OK;
+}
+
+uint64_t expert_workspace(const uw_expert_rows *r, const uw_expert_set *w, const uw_expert_plan *p) {
+    return p->sort && r->order_dev ? up256(uint64_t(r->places) * uint64_t(w->k) * 2) : 0;
+}
+
 uw_status check_expert_call(const uw_expert_rows *r, const uw_expert_set *a, const uw_expert_set *b, const void *out,
-                            int64_t out_stride, int out_unit, const uw_plan *p) {
+                            int64_t out_stride, int out_unit, const uw_expert_plan *p, const void *ws, size_t ws_bytes) {
     uw_status st = check_set(a);
     if (st != UW_OK) return st;
     if (b) {
@@ -64,20 +85,11 @@ uw_status check_expert_call(const uw_expert_rows *r, const uw_expert_set *a, con
         if (st != UW_OK) return st;
         if (b->n != a->n || b->k != a->k || b->experts != a->experts || !a->w_dev != !b->w_dev) return UW_ERR_INVALID_ARG;
     }
-    if (!r || !p || r->places < 0 || r->per_row < 1) return UW_ERR_INVALID_ARG;
+    st = check_expert_plan(p, a);
+    if (st == UW_OK && b) st = check_expert_plan(p, b);
+    if (st != UW_OK) return st;
+    if (!r || r->places < 0 || r->per_row < 1) return UW_ERR_INVALID_ARG;
     if (r->places > kMaxItems || r->x_rows > kMaxItems) return UW_ERR_UNSUPPORTED_SHAPE;
-    if (p->pipeline != UW_PIPE_DIRECT_PALETTE || p->split_k != 1 || p->timeout_ns < 0) return UW_ERR_INVALID_ARG;
-    if (p->kernel == UW_KERNEL_MMA) {
-        if (p->bn < 1 || p->bn > 8 || p->stages < 0 || p->stages > 2 || (p->stages == 2 && a->k % 128))
-            return UW_ERR_INVALID_ARG;
-        // the raw-group bitmaps of a tile of rows are staged in 48 KB
-        if (a->table_dev && a->k > 131072) return UW_ERR_UNSUPPORTED_SHAPE;
-    } else if (p->kernel == UW_KERNEL_TC) {
-        if (!a->w_dev || (p->bn != 128 && p->bn != 256) || p->stages != 0) return UW_ERR_INVALID_ARG;
-        if (a->stride >= int64_t(1) << 39 || (b && b->stride >= int64_t(1) << 39)) return UW_ERR_UNSUPPORTED_SHAPE;
-    } else {
-        return UW_ERR_INVALID_ARG;
-    }
     if (out_stride < a->n || out_stride % out_unit) return UW_ERR_INVALID_ARG;
     if (r->places == 0) return UW_OK;
     if (!r->x_dev || r->x_rows < 1 || !r->offsets_dev || !out) return UW_ERR_INVALID_ARG;
@@ -86,11 +98,13 @@ uw_status check_expert_call(const uw_expert_rows *r, const uw_expert_set *a, con
     if (p->kernel == UW_KERNEL_TC && r->x_stride >= int64_t(1) << 39) return UW_ERR_UNSUPPORTED_SHAPE;
     if (!aligned(r->x_dev, 16) || !aligned(out, 16) || !aligned(r->offsets_dev, 4) || !aligned(r->order_dev, 4))
         return UW_ERR_INVALID_ARG;
+    const uint64_t need = expert_workspace(r, a, p);
+    if (need && (!ws || ws_bytes < need || !aligned(ws, 256))) return UW_ERR_WORKSPACE;
     return UW_OK;
 }
 
 ExpertLaunch expert_launch(const uw_expert_rows *r, const uw_expert_set *a, const uw_expert_set *b, void *out,
-                           int64_t out_stride, const uw_plan *p, uint32_t *status) {
+                           int64_t out_stride, const uw_expert_plan *p, void *ws, uint32_t *status) {
     ExpertLaunch l{};
     l.a = ExpertSet{a->w_dev, a->stride, a->table_dev};
     if (b) l.b = ExpertSet{b->w_dev, b->stride, b->table_dev};
@@ -109,8 +123,10 @@ ExpertLaunch expert_launch(const uw_expert_rows *r, const uw_expert_set *a, cons
     l.y_stride = out_stride;
     l.kernel = p->kernel;
     l.slices = p->bn;
-    l.width = p->stages;
+    l.width = p->width;
     l.bn = p->bn;
+    l.bm = p->rows;
+    l.sorted = expert_workspace(r, a, p) ? static_cast<uint16_t *>(ws) : nullptr;
     l.timeout_ns = p->timeout_ns > 0 ? uint64_t(p->timeout_ns) : 2000000000ull;
     l.status = status;
     return l;
@@ -291,38 +307,41 @@ extern "C" uw_status uw_expert_table(const uw_dmat *const *mats, int32_t experts
     return UW_OK;
 }
 
-extern "C" uw_status uw_expert_plan_default(const uw_expert_set *w, int64_t places, uw_plan *plan) {
+extern "C" uw_status uw_expert_plan_default(const uw_expert_set *w, int64_t places, uw_expert_plan *plan) {
     if (!plan || places < 0) return UW_ERR_INVALID_ARG;
     const uw_status st = check_set(w);
     if (st != UW_OK) return st;
-    *plan = uw_plan{};
-    plan->pipeline = UW_PIPE_DIRECT_PALETTE;
-    plan->split_k = 1;
-    if (!w->w_dev || places <= int64_t(16) * w->experts) {
-        plan->kernel = UW_KERNEL_MMA;
-        plan->bn = w->k > 4096 ? 8 : 4;
-    } else {
-        plan->kernel = UW_KERNEL_TC;
-        plan->bn = 256;
-    }
+    *plan = expert_plan(w->w_dev != nullptr, w->experts, w->n, w->k, places);
+    return UW_OK;
+}
+
+extern "C" uw_status uw_expert_workspace_size(const uw_expert_rows *rows, const uw_expert_set *w,
+                                              const uw_expert_plan *plan, size_t *bytes) {
+    if (!bytes || !rows || rows->places < 0) return UW_ERR_INVALID_ARG;
+    uw_status st = check_set(w);
+    if (st == UW_OK) st = check_expert_plan(plan, w);
+    if (st != UW_OK) return st;
+    if (rows->places > kMaxItems) return UW_ERR_UNSUPPORTED_SHAPE;
+    *bytes = size_t(expert_workspace(rows, w, plan));
     return UW_OK;
 }
 
 extern "C" uw_status uw_expert_matmul(const uw_expert_rows *rows, const uw_expert_set *w, float *y_dev, int64_t y_stride,
-                                      const uw_plan *plan, uint32_t *dev_status, void *stream) {
-    const uw_status st = check_expert_call(rows, w, nullptr, y_dev, y_stride, 4, plan);
+                                      const uw_expert_plan *plan, void *ws, size_t ws_bytes, uint32_t *dev_status,
+                                      void *stream) {
+    const uw_status st = check_expert_call(rows, w, nullptr, y_dev, y_stride, 4, plan, ws, ws_bytes);
     if (st != UW_OK || rows->places == 0) return st;
-    return cuda_status(launch_expert(expert_launch(rows, w, nullptr, y_dev, y_stride, plan, dev_status),
+    return cuda_status(launch_expert(expert_launch(rows, w, nullptr, y_dev, y_stride, plan, ws, dev_status),
                                      static_cast<cudaStream_t>(stream)));
 }
 
 extern "C" uw_status uw_expert_gate_up(const uw_expert_rows *rows, const uw_expert_set *gate, const uw_expert_set *up,
-                                       uint16_t *h_dev, int64_t h_stride, const uw_plan *plan, uint32_t *dev_status,
-                                       void *stream) {
+                                       uint16_t *h_dev, int64_t h_stride, const uw_expert_plan *plan, void *ws,
+                                       size_t ws_bytes, uint32_t *dev_status, void *stream) {
     if (!up) return UW_ERR_INVALID_ARG;
-    const uw_status st = check_expert_call(rows, gate, up, h_dev, h_stride, 8, plan);
+    const uw_status st = check_expert_call(rows, gate, up, h_dev, h_stride, 8, plan, ws, ws_bytes);
     if (st != UW_OK || rows->places == 0) return st;
-    return cuda_status(launch_expert(expert_launch(rows, gate, up, h_dev, h_stride, plan, dev_status),
+    return cuda_status(launch_expert(expert_launch(rows, gate, up, h_dev, h_stride, plan, ws, dev_status),
                                      static_cast<cudaStream_t>(stream)));
 }
 

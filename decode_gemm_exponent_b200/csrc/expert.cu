@@ -18,8 +18,7 @@
 // Many rows per expert (k_expert_tc): persistent tcgen05 kernel, plain BF16
 // weights.  Tokens are the MMA's M (128 rows of one expert), weights its N, so
 // that a token's outputs lie in one TMEM lane: its gate and up values meet in
-// one thread.  Rows of x are gathered by TMA (four row indices per copy), so no
-// sorted copy of x is written.  Two TMEM accumulators: the epilogue of a tile
+// one thread.  Two TMEM accumulators: the epilogue of a tile
 // overlaps the next tile's products.  The tensor core truncates as it
 // accumulates (about 1.1e-9 per unit of K, relative, measured), so FP32 outputs
 // are summed in registers over chunks of 512 of K; BF16 outputs need no chunks.
@@ -288,12 +287,14 @@ __global__ void __launch_bounds__(256) k_expert_mma(const MmaExpertArgs a) {
 // ---------------------------------------------------------------- tcgen05
 
 constexpr int kBM = 128, kBK = 64;
-constexpr int kTcThreads = 384;       // W producer, MMA, X producer, spare, eight epilogue warps
-constexpr int kXTile = kBM * kBK * 2;
+constexpr int kTcThreads = 384;       // W producer, MMA, two x producers, eight epilogue warps
+constexpr int kBox = 32;              // rows of x per tiled copy
 constexpr int kSumSteps = 8;          // K-steps per FP32 chunk
 
 struct TcExpertArgs {
     int experts, per_row, ksteps, stages;
+    int bm;                    // rows per tile: 32, 64 or 128
+    int boxes;                 // x is in expert order: tiled copies instead of gathers
     int64_t places, x_rows, n;
     const int32_t *offsets, *order;
     void *y;
@@ -325,12 +326,16 @@ template <int BN, bool GATED>
 __global__ void __launch_bounds__(kTcThreads, 1)
     k_expert_tc(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmA,
                 const __grid_constant__ CUtensorMap tmB, const TcExpertArgs a) {
-    constexpr int kW = BN * kBK * 2, kStage = kXTile + kW;
+    constexpr int kW = BN * kBK * 2;
     constexpr int kCols = GATED ? BN / 2 : BN;       // output columns per tile
     extern __shared__ uint8_t smem_dyn[];
     uint8_t *ring = smem_dyn + ((1024u - (smem_addr(smem_dyn) & 1023u)) & 1023u);
-    const int S = a.stages;
-    uint64_t *xfull = reinterpret_cast<uint64_t *>(ring + size_t(S) * kStage);
+    // x tiles of a.bm rows, then the weight tiles.  The MMA reads 128 rows from an
+    // x tile whatever a.bm is: what lies behind a smaller tile (other stages, at
+    // least one weight tile) reaches only accumulator rows that are not read.
+    const int S = a.stages, xtile = a.bm * kBK * 2;
+    uint8_t *wring = ring + size_t(S) * xtile;
+    uint64_t *xfull = reinterpret_cast<uint64_t *>(wring + size_t(S) * kW);
     uint64_t *wfull = xfull + S, *empty = wfull + S, *accf = empty + S, *acce = accf + 2;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(acce + 2);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
@@ -366,7 +371,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             if (e0 + lane < a.experts) {
                 const int lo = min(max(__ldg(a.offsets + e0 + lane), 0), most);
                 const int hi = min(max(__ldg(a.offsets + e0 + lane + 1), 0), most);
-                tiles = (max(hi - lo, 0) + kBM - 1) / kBM;
+                tiles = (max(hi - lo, 0) + a.bm - 1) / a.bm;
             }
             int incl = tiles;
 #pragma unroll
@@ -395,8 +400,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             else hi = mid;
         }
         const int p0 = min(max(__ldg(a.offsets + lo), 0), most), p1 = min(max(__ldg(a.offsets + lo + 1), 0), most);
-        const int skip = (mt - first[lo]) * kBM;
-        return Span{lo, p0 + skip, min(kBM, p1 - p0 - skip)};
+        const int skip = (mt - first[lo]) * a.bm;
+        return Span{lo, p0 + skip, min(a.bm, p1 - p0 - skip)};
     };
 
     if (warp == 0) {
@@ -414,7 +419,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         ok = false;
                         break;
                     }
-                    uint8_t *st = ring + size_t(s) * kStage + kXTile;
+                    uint8_t *st = wring + size_t(s) * kW;
                     mbar_arrive_expect_tx(&wfull[s], uint32_t(kW));
                     if (GATED) {
                         tma_load_3d(st, &tmA, ks * kBK, n0, t.expert, &wfull[s]);
@@ -452,7 +457,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                              mbar_wait_or_abort(&wfull[s], uint32_t(it / S) & 1u, T, abort_flag);
                         if (!ok) break;
                         tc_fence_after();
-                        const uint32_t sx = smem_addr(ring + size_t(s) * kStage), sw = sx + kXTile;
+                        const uint32_t sx = smem_addr(ring + size_t(s) * xtile), sw = smem_addr(wring + size_t(s) * kW);
 #pragma unroll
                         for (int kk = 0; kk < kBK / 16; kk++)
                             tc_mma_bf16(tmem + b * BN, smem_desc_k128(sx + 32 * kk), smem_desc_k128(sw + 32 * kk), idesc,
@@ -472,25 +477,36 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         }
         __syncwarp();
     } else if (warp == 2) {
-        // ------------------------------------------------ rows of x, four per lane
+        // ------------------------------------------------ rows of x
         int64_t it = 0;
         bool ok = true;
         for (int64_t tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x) {
             const Span t = locate(int(tile / ntn));
             int32_t row[4];
+            int copies, bytes;           // one copy per lane
+            if (a.boxes) {
+                copies = (t.rows + kBox - 1) / kBox;
+                bytes = kBox * kBK * 2;
+                row[0] = t.pos + lane * kBox;
+            } else {
+                copies = (t.rows + 3) / 4;
+                bytes = 4 * kBK * 2;
 #pragma unroll
-            for (int i = 0; i < 4; i++)
-                row[i] = int32_t(source_row(a.order, a.per_row, a.x_rows, t.pos + min(4 * lane + i, t.rows - 1)));
-            const uint32_t bytes = uint32_t((t.rows + 3) / 4) * 4u * kBK * 2u;
+                for (int i = 0; i < 4; i++)
+                    row[i] = int32_t(source_row(a.order, a.per_row, a.x_rows, t.pos + min(4 * lane + i, t.rows - 1)));
+            }
             for (int ks = 0; ks < a.ksteps; ks++, it++) {
                 const int s = int(it % S);
                 if (it >= S) ok = mbar_wait_or_abort(&empty[s], (uint32_t(it / S) & 1u) ^ 1u, T, abort_flag);
                 ok = __all_sync(kAll, ok && !*abort_flag);
                 if (!ok) break;
-                if (lane == 0) mbar_arrive_expect_tx(&xfull[s], bytes);
+                if (lane == 0) mbar_arrive_expect_tx(&xfull[s], uint32_t(copies * bytes));
                 __syncwarp();
-                if (4 * lane < t.rows)
-                    tma_gather4(ring + size_t(s) * kStage + 4 * lane * kBK * 2, &tmX, ks * kBK, row, &xfull[s]);
+                if (lane < copies) {
+                    uint8_t *dst = ring + size_t(s) * xtile + lane * bytes;
+                    if (a.boxes) tma_load_2d(dst, &tmX, ks * kBK, row[0], &xfull[s]);
+                    else tma_gather4(dst, &tmX, ks * kBK, row, &xfull[s]);
+                }
             }
         }
         if (!ok && lane == 0) {
@@ -646,16 +662,17 @@ bool weight_map(CUtensorMap *map, const ExpertSet &s, int experts, int64_t n, in
 
 template <int BN, bool GATED>
 cudaError_t launch_tc(const ExpertLaunch &p, cudaStream_t stream) {
-    constexpr int kStage = kXTile + BN * kBK * 2;
     constexpr int kMaxSmem = 232448;
+    const int bm = p.bm, stage = bm * kBK * 2 + BN * kBK * 2 + 24;      // tiles and three barriers
     const int tail = 1024 + 64 + (p.experts + 4) * 4;
-    const int stages = std::min(8, (kMaxSmem - tail) / (kStage + 24));
+    const int stages = std::min(12, (kMaxSmem - tail) / stage);
     if (stages < 2) return cudaErrorInvalidValue;
-    const size_t smem = size_t(stages) * (kStage + 24) + tail;
+    const size_t smem = size_t(stages) * stage + tail;
     CUtensorMap mx, ma, mb;
+    const bool boxes = p.order == nullptr;
     const cuuint64_t xd[2] = {cuuint64_t(p.k), cuuint64_t(p.x_rows)};
     const cuuint64_t xs[1] = {cuuint64_t(p.x_stride) * 2};
-    const cuuint32_t xb[2] = {kBK, 1};               // a gather's box is one row
+    const cuuint32_t xb[2] = {kBK, boxes ? cuuint32_t(kBox) : 1};       // a gather's box is one row
     const int rows = GATED ? BN / 2 : BN;
     if (!make_map(&mx, p.x, 2, xd, xs, xb) || !weight_map(&ma, p.a, p.experts, p.n, p.k, rows)) return cudaErrorInvalidValue;
     mb = ma;
@@ -674,6 +691,8 @@ cudaError_t launch_tc(const ExpertLaunch &p, cudaStream_t stream) {
     a.per_row = p.per_row;
     a.ksteps = int(p.k / kBK);
     a.stages = stages;
+    a.bm = bm;
+    a.boxes = boxes;
     a.places = p.places;
     a.x_rows = p.x_rows;
     a.n = p.n;
@@ -683,7 +702,7 @@ cudaError_t launch_tc(const ExpertLaunch &p, cudaStream_t stream) {
     a.y_stride = p.y_stride;
     a.timeout_ns = p.timeout_ns;
     a.status = p.status;
-    const int64_t row_tiles = (p.places + (kBM - 1) * std::min<int64_t>(p.experts, p.places)) / kBM;
+    const int64_t row_tiles = (p.places + (bm - 1) * std::min<int64_t>(p.experts, p.places)) / bm;
     const int64_t tiles = row_tiles * ((p.n + (GATED ? BN / 2 : BN) - 1) / (GATED ? BN / 2 : BN));
     const unsigned grid = unsigned(std::min<int64_t>(sm_count(), tiles));
     k_expert_tc<BN, GATED><<<grid, kTcThreads, smem, stream>>>(mx, ma, mb, a);
@@ -720,6 +739,20 @@ cudaError_t launch_mma(const ExpertLaunch &p, cudaStream_t stream) {
 
 }  // namespace
 
+uw_expert_plan expert_plan(bool plain, int experts, int64_t n, int64_t k, int64_t places) {
+    uw_expert_plan p{};
+    if (!plain) {
+        p.kernel = UW_KERNEL_MMA;
+        p.bn = k > 4096 ? 8 : 4;
+        return p;
+    }
+    p.kernel = UW_KERNEL_TC;
+    p.bn = 256;
+    p.rows = places <= 16 * int64_t(experts) ? 32 : 128;
+    p.sort = places > 16 * int64_t(experts);
+    return p;
+}
+
 size_t expert_entry_bytes() { return sizeof(Planes); }
 
 void expert_fill_entry(void *entry, const uw_dmat &w) {
@@ -733,7 +766,29 @@ void expert_fill_entry(void *entry, const uw_dmat &w) {
     memcpy(entry, &p, sizeof(p));
 }
 
-cudaError_t launch_expert(const ExpertLaunch &p, cudaStream_t stream) {
+// A row of x per place, in expert order: 16 bytes per thread, one warp a row.
+static __global__ void __launch_bounds__(256) k_expert_sort(const uint16_t *x, int64_t x_rows, int64_t x_stride, int64_t k, int per_row,
+                                                     const int32_t *offsets, int experts, int64_t places,
+                                                     const int32_t *order, uint16_t *out) {
+    const int64_t p = int64_t(blockIdx.x) * 8 + (threadIdx.x >> 5);
+    if (p >= min(places, int64_t(__ldg(offsets + experts)))) return;
+    const uint4 *src = reinterpret_cast<const uint4 *>(x + source_row(order, per_row, x_rows, int(p)) * x_stride);
+    uint4 *dst = reinterpret_cast<uint4 *>(out + p * k);
+    for (int64_t i = threadIdx.x & 31; i < k / 8; i += 32) dst[i] = __ldg(src + i);
+}
+
+cudaError_t launch_expert(const ExpertLaunch &given, cudaStream_t stream) {
+    ExpertLaunch p = given;
+    if (p.sorted) {
+        k_expert_sort<<<unsigned((p.places + 7) / 8), 256, 0, stream>>>(p.x, p.x_rows, p.x_stride, p.k, p.per_row, p.offsets,
+                                                                        p.experts, p.places, p.order, p.sorted);
+        const cudaError_t err = cudaGetLastError();
+        if (err != cudaSuccess) return err;
+        p.x = p.sorted;
+        p.x_rows = p.places;
+        p.x_stride = p.k;
+        p.order = nullptr;
+    }
     if (p.kernel == UW_KERNEL_MMA) {
         if (p.a.table) return p.gated ? launch_mma<true, true>(p, stream) : launch_mma<true, false>(p, stream);
         return p.gated ? launch_mma<false, true>(p, stream) : launch_mma<false, false>(p, stream);

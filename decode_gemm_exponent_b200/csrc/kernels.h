@@ -282,10 +282,12 @@ struct ExpertLaunch {
     int64_t y_stride;
     int kernel;                // UW_KERNEL_MMA or UW_KERNEL_TC
     int slices, width;         // MMA
-    int bn;                    // TC
+    int bn, bm;                // TC: weight rows and places per tile
+    uint16_t *sorted;          // TC: where the rows of x go in expert order first (null: gathered)
     uint64_t timeout_ns;
     uint32_t *status;
 };
+uw_expert_plan expert_plan(bool plain, int experts, int64_t n, int64_t k, int64_t places);   // the default
 size_t expert_entry_bytes();
 void expert_fill_entry(void *entry, const uw_dmat &w);
 cudaError_t launch_expert(const ExpertLaunch &p, cudaStream_t stream);

@@ -48,6 +48,7 @@ EXPORTS = ("uw_status_str", "uw_version", "uw_encode", "uw_blob_data", "uw_blob_
            "uw_sm_split_create", "uw_sm_split_get", "uw_sm_split_destroy", "uw_stack_tune_split",
            "uw_fused_matmul_batched", "uw_route_workspace_size", "uw_route_experts", "uw_group_workspace_size",
            "uw_group_rows", "uw_lora_workspace_size", "uw_lora_add", "uw_expert_table", "uw_expert_plan_default",
+           "uw_expert_workspace_size",
            "uw_expert_matmul", "uw_expert_gate_up", "uw_expert_combine")
 
 
@@ -120,6 +121,11 @@ class ExpertRows(ctypes.Structure):
                 ("x_stride", ctypes.c_int64)]
 
 
+class ExpertPlan(ctypes.Structure):
+    _fields_ = [("kernel", ctypes.c_int32), ("bn", ctypes.c_int32), ("width", ctypes.c_int32), ("rows", ctypes.c_int32),
+                ("sort", ctypes.c_int32), ("timeout_ns", ctypes.c_int64)]
+
+
 class Adapters(ctypes.Structure):
     _fields_ = [("n", ctypes.c_int64), ("k", ctypes.c_int64), ("count", ctypes.c_int32), ("max_rank", ctypes.c_int32),
                 ("a_dev", ctypes.c_void_p), ("b_dev", ctypes.c_void_p), ("ranks_dev", ctypes.c_void_p),
@@ -172,11 +178,13 @@ def lib() -> ctypes.CDLL:
         "uw_lora_workspace_size": (ctypes.c_int, [I64, ctypes.POINTER(Adapters), ctypes.POINTER(SZ)]),
         "uw_lora_add": (ctypes.c_int, [P, I64, I64, ctypes.POINTER(Adapters), P, P, P, P, I64, P, I64, P, SZ, P]),
         "uw_expert_table": (ctypes.c_int, [ctypes.POINTER(ctypes.POINTER(DMat)), I32, P, SZ]),
-        "uw_expert_plan_default": (ctypes.c_int, [ctypes.POINTER(ExpertSetArgs), I64, ctypes.POINTER(Plan)]),
+        "uw_expert_plan_default": (ctypes.c_int, [ctypes.POINTER(ExpertSetArgs), I64, ctypes.POINTER(ExpertPlan)]),
+        "uw_expert_workspace_size": (ctypes.c_int, [ctypes.POINTER(ExpertRows), ctypes.POINTER(ExpertSetArgs),
+                                                    ctypes.POINTER(ExpertPlan), ctypes.POINTER(SZ)]),
         "uw_expert_matmul": (ctypes.c_int, [ctypes.POINTER(ExpertRows), ctypes.POINTER(ExpertSetArgs), P, I64,
-                                            ctypes.POINTER(Plan), P, P]),
+                                            ctypes.POINTER(ExpertPlan), P, SZ, P, P]),
         "uw_expert_gate_up": (ctypes.c_int, [ctypes.POINTER(ExpertRows), ctypes.POINTER(ExpertSetArgs),
-                                             ctypes.POINTER(ExpertSetArgs), P, I64, ctypes.POINTER(Plan), P, P]),
+                                             ctypes.POINTER(ExpertSetArgs), P, I64, ctypes.POINTER(ExpertPlan), P, SZ, P, P]),
         "uw_expert_combine": (ctypes.c_int, [P, I64, P, P, I64, I32, I64, P, I64, P, I64, P]),
         "uw_sm_split_create": (ctypes.c_int, [ctypes.c_int, ctypes.c_int, ctypes.POINTER(P)]),
         "uw_sm_split_get": (ctypes.c_int, [P, ctypes.POINTER(P), ctypes.POINTER(P), ctypes.POINTER(ctypes.c_int),
@@ -488,26 +496,45 @@ def autotune(mats: Sequence[Matrix], ms: Sequence[int], reps: int = 5, stream=No
 
 # ----------------------------------------------------------------------------- around the matmuls
 
+class _Here:
+    """Context of a call on the current device and stream: nothing to switch."""
+
+    def __enter__(self):
+        return None
+
+    def __exit__(self, *exc):
+        return False
+
+
+_HERE = _Here()
+
+
 def _enter(t, stream):
     """Context in which a call on `t`'s device runs: that device and `stream`
     (default: the device's current stream) are current inside, so that what is
     allocated there belongs to the stream that uses it."""
-    import contextlib
     import torch
-    if t.device.type != "cuda":
+    if not t.is_cuda:
         raise ValueError("tensors must be on a CUDA device, got %s" % t.device)
-    if stream is not None and stream.device != t.device:
+    if stream is None:
+        if t.get_device() == torch._C._cuda_getDevice():
+            return _HERE
+        return torch.cuda.stream(torch.cuda.current_stream(t.device))
+    if stream.device != t.device:
         raise ValueError("stream of %s for tensors of %s" % (stream.device, t.device))
-    current = torch.cuda.current_stream(t.device)
-    if t.device.index == torch.cuda.current_device() and (stream is None or stream == current):
-        return contextlib.nullcontext()
-    return torch.cuda.stream(current if stream is None else stream)
+    return torch.cuda.stream(stream)
+
+
+def _handle(t):
+    """The current stream of `t`'s device (inside _enter), as the C ABI takes it."""
+    import torch
+    return torch._C._cuda_getCurrentRawStream(t.get_device())
 
 
 def _need(t, name, shape, dtypes, like, rows=False):
     """Check a tensor argument: shape, type, device, and contiguity (rows=True:
     only of each row)."""
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError("%s: shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
     if t.dtype not in dtypes:
         raise ValueError("%s: type %s, expected %s" % (name, t.dtype, " or ".join(str(d) for d in dtypes)))
@@ -577,7 +604,7 @@ def route_experts(logits, top_k: int, *, score: str = "softmax", bias=None, n_gr
                                      None if bias is None else bias.data_ptr(), ctypes.byref(r), out.ids.data_ptr(),
                                      out.weights.data_ptr(), out.offsets.data_ptr(), out.order.data_ptr(),
                                      out.slot.data_ptr(), out.ws.data_ptr() if size.value else None, size.value,
-                                     _stream_handle()), "uw_route_experts")
+                                     _handle(logits)), "uw_route_experts")
     return out
 
 
@@ -603,7 +630,7 @@ def group_rows(ids, groups: int, out: Optional[Grouping] = None, stream=None) ->
             out.ws = torch.empty(size.value, dtype=torch.uint8, device=ids.device)
         check(lib().uw_group_rows(ids.data_ptr(), rows, per_row, groups, out.offsets.data_ptr(), out.order.data_ptr(),
                                   None if out.slot is None else out.slot.data_ptr(),
-                                  out.ws.data_ptr() if size.value else None, size.value, _stream_handle()), "uw_group_rows")
+                                  out.ws.data_ptr() if size.value else None, size.value, _handle(ids)), "uw_group_rows")
     return out
 
 
@@ -660,57 +687,72 @@ def _expert_rows(x, grouping: Grouping, set_: ExpertSetArgs, gather: bool) -> Ex
                       x.data_ptr(), rows, x.stride(0) if rows > 1 else set_.k)
 
 
-def expert_plan_default(w, places: int) -> Plan:
-    """uw_expert_plan_default for an ExpertSet or a BF16 [experts, n, k] tensor."""
-    p = Plan()
-    a = _expert_set(w, "w", w)
+def make_expert_plan(kernel=KERNEL_TC, bn=256, rows=None, sort=0, width=0, timeout_ns=0) -> ExpertPlan:
+    if rows is None:
+        rows = 128 if kernel == KERNEL_TC else 0
+    return ExpertPlan(kernel, bn, width, rows, sort, timeout_ns)
+
+
+def _default_plan(a: ExpertSetArgs, places: int) -> ExpertPlan:
+    p = ExpertPlan()
     check(lib().uw_expert_plan_default(ctypes.byref(a), places, ctypes.byref(p)), "uw_expert_plan_default")
     return p
 
 
-def expert_matmul(x, w, routing: Grouping, *, gather: bool = False, plan: Optional[Plan] = None, out=None, status=None,
-                  stream=None):
+def expert_plan_default(w, places: int) -> ExpertPlan:
+    """uw_expert_plan_default for an ExpertSet or a BF16 [experts, n, k] tensor."""
+    return _default_plan(_expert_set(w, "w", w), places)
+
+
+def expert_workspace_size(places: int, w, plan: ExpertPlan) -> int:
+    """uw_expert_workspace_size for `places` gathered rows."""
+    a, size = _expert_set(w, "w", w), ctypes.c_size_t()
+    r = ExpertRows(places, 1, None, 1, None, 0, 0)
+    check(lib().uw_expert_workspace_size(ctypes.byref(r), ctypes.byref(a), ctypes.byref(plan), ctypes.byref(size)),
+          "uw_expert_workspace_size")
+    return int(size.value)
+
+
+def _expert_call(fn, name, x, sets, routing, gather, plan, out, dtypes, status, ws, stream):
+    import torch
+    a = sets[0]
+    r = _expert_rows(x, routing, a, gather)
+    with _enter(x, stream):
+        if out is None:
+            out = torch.empty(r.places, a.n, dtype=dtypes[0], device=x.device)
+        else:
+            _need(out, "out", (r.places, a.n), dtypes, x, rows=True)
+        if status is not None:
+            _need(status, "status", status.shape, (torch.int32,), x)
+        if plan is None:
+            plan = _default_plan(a, r.places)
+        if ws is None and plan.sort and gather:
+            ws = torch.empty(r.places * a.k * 2 + 255, dtype=torch.uint8, device=x.device)
+        check(fn(ctypes.byref(r), *[ctypes.byref(v) for v in sets], out.data_ptr(), out.stride(0) if r.places > 1 else a.n,
+                 ctypes.byref(plan), None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel(),
+                 None if status is None else status.data_ptr(), _handle(x)), name)
+    return out
+
+
+def expert_matmul(x, w, routing: Grouping, *, gather: bool = False, plan: Optional[ExpertPlan] = None, out=None,
+                  status=None, ws=None, stream=None):
     """uw_expert_matmul: float32 [places, n] in expert order.  w: an ExpertSet or
     BF16 [experts, n, k].  x: rows in expert order, or with gather=True one row
     per token (the routed slots of a token share its row)."""
     import torch
-    a = _expert_set(w, "w", x)
-    r = _expert_rows(x, routing, a, gather)
-    with _enter(x, stream):
-        if out is None:
-            out = torch.empty(r.places, a.n, dtype=torch.float32, device=x.device)
-        else:
-            _need(out, "out", (r.places, a.n), (torch.float32,), x, rows=True)
-        if plan is None:
-            plan = Plan()
-            check(lib().uw_expert_plan_default(ctypes.byref(a), r.places, ctypes.byref(plan)), "uw_expert_plan_default")
-        check(lib().uw_expert_matmul(ctypes.byref(r), ctypes.byref(a), out.data_ptr(),
-                                     out.stride(0) if r.places > 1 else a.n, ctypes.byref(plan), _ptr(status),
-                                     _stream_handle()), "uw_expert_matmul")
-    return out
+    return _expert_call(lib().uw_expert_matmul, "uw_expert_matmul", x, (_expert_set(w, "w", x),), routing, gather, plan, out,
+                        (torch.float32,), status, ws, stream)
 
 
-def expert_gate_up(x, gate, up, routing: Grouping, *, gather: bool = True, plan: Optional[Plan] = None, out=None,
-                   status=None, stream=None):
+def expert_gate_up(x, gate, up, routing: Grouping, *, gather: bool = True, plan: Optional[ExpertPlan] = None, out=None,
+                   status=None, ws=None, stream=None):
     """uw_expert_gate_up: bfloat16 [places, n] in expert order, the routed
     experts' silu(gate x) * (up x); gate and up as expert_matmul's w."""
-    import torch
     a, b = _expert_set(gate, "gate", x), _expert_set(up, "up", x)
     if (a.n, a.k, a.experts) != (b.n, b.k, b.experts):
         raise ValueError("gate and up have different sizes")
-    r = _expert_rows(x, routing, a, gather)
-    with _enter(x, stream):
-        if out is None:
-            out = torch.empty(r.places, a.n, dtype=torch.bfloat16, device=x.device)
-        else:
-            _need(out, "out", (r.places, a.n), _bits(), x, rows=True)
-        if plan is None:
-            plan = Plan()
-            check(lib().uw_expert_plan_default(ctypes.byref(a), r.places, ctypes.byref(plan)), "uw_expert_plan_default")
-        check(lib().uw_expert_gate_up(ctypes.byref(r), ctypes.byref(a), ctypes.byref(b), out.data_ptr(),
-                                      out.stride(0) if r.places > 1 else a.n, ctypes.byref(plan), _ptr(status),
-                                      _stream_handle()), "uw_expert_gate_up")
-    return out
+    return _expert_call(lib().uw_expert_gate_up, "uw_expert_gate_up", x, (a, b), routing, gather, plan, out, _bits(), status,
+                        ws, stream)
 
 
 def expert_combine(y, routing: Routing, *, base=None, out=None, stream=None):
@@ -734,7 +776,7 @@ def expert_combine(y, routing: Routing, *, base=None, out=None, stream=None):
             _need(out, "out", (t, n), (torch.float32,), y, rows=True)
         check(lib().uw_expert_combine(y.data_ptr(), row(y), routing.slot.data_ptr(), routing.weights.data_ptr(), t, top_k, n,
                                       _ptr(base), 0 if base is None else row(base), out.data_ptr(), row(out),
-                                      _stream_handle()), "uw_expert_combine")
+                                      _handle(y)), "uw_expert_combine")
     return out
 
 
@@ -787,7 +829,7 @@ def lora_add(x, a, b, ids, y, *, ranks=None, scales=None, groups: Optional[Group
         check(lib().uw_lora_add(x.data_ptr(), row(x), t, ctypes.byref(d), None if groups is not None else ids.data_ptr(),
                                 None if groups is None else groups.offsets.data_ptr(),
                                 None if groups is None else groups.order.data_ptr(), y.data_ptr(), row(y),
-                                out.data_ptr(), row(out), ws.data_ptr(), ws.numel(), _stream_handle()), "uw_lora_add")
+                                out.data_ptr(), row(out), ws.data_ptr(), ws.numel(), _handle(x)), "uw_lora_add")
     return out
 
 

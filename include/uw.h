@@ -556,12 +556,23 @@ typedef struct uw_expert_set {
  * the matrices' device blobs.                                                      */
 uw_status uw_expert_table(const uw_dmat *const *mats, int32_t experts, void *table, size_t table_bytes);
 
-/* Plan of the calls below: UW_KERNEL_MMA (any set; bn warps 1..8 split K, stages as
- * in uw_plan), made for few rows per expert, and UW_KERNEL_TC (plain sets; bn = 128
- * or 256 weight rows per tile), for many.  pipeline is UW_PIPE_DIRECT_PALETTE (not
- * used by plain sets), split_k 1, stages 0 for TC.  The default decides by the rows
- * per expert.  places: routed slots, t * top_k.                                    */
-uw_status uw_expert_plan_default(const uw_expert_set *w, int64_t places, uw_plan *plan);
+/* How the calls below run. */
+typedef struct uw_expert_plan {
+    int32_t kernel;      /* UW_KERNEL_MMA: any set, made for few rows per expert; UW_KERNEL_TC:
+                            plain sets, any number of rows                              */
+    int32_t bn;          /* MMA: warps per CTA, 1..8, which split K; TC: weight rows per
+                            tile, 128 or 256 (gate_up: half of each matrix)             */
+    int32_t width;       /* MMA: 16 (1) or 32 (2, k a multiple of 128) weights per lane and
+                            row per step, 0 = 32 where k allows; TC: must be 0          */
+    int32_t rows;        /* TC: places per tile, 32, 64 or 128; MMA: must be 0          */
+    int32_t sort;        /* TC: non-zero = copy the rows of x into expert order first (into
+                            the workspace; no effect without order_dev); MMA: must be 0 */
+    int64_t timeout_ns;  /* TC: spin-wait limit (0 = 2 s)                               */
+} uw_expert_plan;
+
+/* A plan by the rows per expert, places / experts (places: routed slots, t * top_k):
+ * TC for plain sets, MMA for compressed ones.                                      */
+uw_status uw_expert_plan_default(const uw_expert_set *w, int64_t places, uw_expert_plan *plan);
 
 /* The routed rows: place j of the order (offsets and order as uw_route_experts or
  * uw_group_rows wrote them) belongs to the expert e with offsets[e] <= j <
@@ -570,7 +581,8 @@ uw_status uw_expert_plan_default(const uw_expert_set *w, int64_t places, uw_plan
  * rows of places that belong to no expert are left as they were.
  * x_dev: BF16 [x_rows, k], rows x_stride apart (>= k, a multiple of 8), 16-byte
  * aligned.  dev_status: device uint32 for kernel error bits, may be NULL.
- * places >= 0; 0 launches nothing.  Argument errors as in uw_fused_matmul.          */
+ * places >= 0; 0 launches nothing.  ws: >= uw_expert_workspace_size bytes (0 unless
+ * the plan sorts), 256-byte aligned; its contents do not matter.                    */
 typedef struct uw_expert_rows {
     int64_t places;           /* t * top_k, < 2^31                                    */
     int32_t per_row;          /* top_k                                                */
@@ -579,17 +591,21 @@ typedef struct uw_expert_rows {
     int64_t x_rows, x_stride;
 } uw_expert_rows;
 
+uw_status uw_expert_workspace_size(const uw_expert_rows *rows, const uw_expert_set *w, const uw_expert_plan *plan,
+                                   size_t *bytes);
+
 /* y[j] = W_e x: float [places, n], rows y_stride apart (>= n, a multiple of 4),
  * 16-byte aligned.  A compressed set's result is bit-identical to the plain set's
  * with the same plan.  Sums are kept in 32 bits.                                   */
 uw_status uw_expert_matmul(const uw_expert_rows *rows, const uw_expert_set *w, float *y_dev, int64_t y_stride,
-                           const uw_plan *plan, uint32_t *dev_status, void *stream);
+                           const uw_expert_plan *plan, void *ws, size_t ws_bytes, uint32_t *dev_status, void *stream);
 
 /* h[j] = silu(G_e x) * (U_e x) with silu(g) = g / (1 + exp(-g)), rounded once to
  * BF16: [places, n], rows h_stride apart (>= n, a multiple of 8), 16-byte aligned.
  * gate and up: sets of the same sizes and form.                                    */
 uw_status uw_expert_gate_up(const uw_expert_rows *rows, const uw_expert_set *gate, const uw_expert_set *up, uint16_t *h_dev,
-                            int64_t h_stride, const uw_plan *plan, uint32_t *dev_status, void *stream);
+                            int64_t h_stride, const uw_expert_plan *plan, void *ws, size_t ws_bytes,
+                            uint32_t *dev_status, void *stream);
 
 /* out[i] = (base[i] +) sum over s < top_k of weights[i, s] * y[slot[i, s]], in that
  * order; slots of -1 add nothing.  y: float [t * top_k, n] in expert order; base_dev

@@ -47,8 +47,9 @@ def normal(seed, *shape, std=1.0):
 
 
 def plans(uw):
-    return [uw.make_plan(uw.PIPE_DIRECT_PALETTE, uw.KERNEL_MMA, 4), uw.make_plan(uw.PIPE_DIRECT_PALETTE, uw.KERNEL_MMA, 1, 1, 1),
-            uw.make_plan(uw.PIPE_DIRECT_PALETTE, uw.KERNEL_TC, 128), uw.make_plan(uw.PIPE_DIRECT_PALETTE, uw.KERNEL_TC, 256), None]
+    P = uw.make_expert_plan
+    return [P(uw.KERNEL_MMA, 4), P(uw.KERNEL_MMA, 1, width=1), P(uw.KERNEL_TC, 128, 128), P(uw.KERNEL_TC, 256, 32),
+            P(uw.KERNEL_TC, 256, 64, sort=1), P(uw.KERNEL_TC, 128, 128, sort=1), None]
 
 
 def product(x, w, routing, gather, k_per_chain):
@@ -81,7 +82,7 @@ SHAPES = [(1, 4, 64, 64, 2), (3, 8, 192, 128, 3), (40, 16, 320, 256, 4), (33, 2,
           (700, 8, 256, 1024, 2), (300, 130, 64, 128, 8)]
 
 
-@pytest.mark.parametrize("which", range(5))
+@pytest.mark.parametrize("which", range(7))
 @pytest.mark.parametrize("t,e,n,k,top_k", SHAPES)
 def test_matmul(uw, which, t, e, n, k, top_k):
     plan = plans(uw)[which]
@@ -93,7 +94,7 @@ def test_matmul(uw, which, t, e, n, k, top_k):
     check(uw.expert_matmul(xs, w, r, plan=plan), want, bound)
 
 
-@pytest.mark.parametrize("which", range(5))
+@pytest.mark.parametrize("which", range(7))
 @pytest.mark.parametrize("t,e,n,k,top_k", SHAPES)
 def test_gate_up(uw, which, t, e, n, k, top_k):
     plan = plans(uw)[which]
@@ -112,7 +113,7 @@ def test_gate_up(uw, which, t, e, n, k, top_k):
     assert torch.equal(again.view(torch.int16), got.view(torch.int16)) and int(status) == 0
 
 
-@pytest.mark.parametrize("which", range(5))
+@pytest.mark.parametrize("which", range(7))
 def test_crowded_and_empty_experts_and_dropped_slots(uw, which):
     plan = plans(uw)[which]
     t, e, n, k = 150, 40, 128, 192
@@ -126,7 +127,7 @@ def test_crowded_and_empty_experts_and_dropped_slots(uw, which):
     assert last < 2 * t and bool((y[last:] == 7.0).all())      # rows behind the last expert are left as they were
 
 
-@pytest.mark.parametrize("which", range(5))
+@pytest.mark.parametrize("which", range(7))
 def test_no_slot_has_an_expert_and_no_tokens(uw, which):
     plan = plans(uw)[which]
     r = routed(uw, 20, 6, 2, 3, drop=1.1)
@@ -139,7 +140,7 @@ def test_no_slot_has_an_expert_and_no_tokens(uw, which):
     assert uw.expert_combine(torch.empty(0, 64, device="cuda"), none).shape == (0, 64)
 
 
-@pytest.mark.parametrize("which", [0, 2, 3])
+@pytest.mark.parametrize("which", [0, 2, 3, 4])
 def test_strides_and_guard_rows(uw, which):
     plan = plans(uw)[which]
     t, e, n, k = 90, 3, 128, 128
@@ -174,7 +175,7 @@ def test_nan_rows_stay_with_their_tokens(uw):
 def test_compressed_equals_plain_bit_for_bit(uw, slices, width, k):
     from decode_gemm_exponent_b200 import synth
     t, e, n = 23, 6, 192
-    plan = uw.make_plan(uw.PIPE_DIRECT_PALETTE, uw.KERNEL_MMA, slices, 1, width)
+    plan = uw.make_expert_plan(uw.KERNEL_MMA, slices, width=width)
     ws = [[synth.weights_bf16(n, k, 0.01 + 0.004 * i, 0.004, 1.0, seed=100 * j + i) for i in range(e)] for j in range(2)]
     sets = [uw.ExpertSet([uw.Matrix(uw.encode(w)) for w in row]) for row in ws]
     plain = [torch.from_numpy(np.stack(row).view(np.int16)).cuda() for row in ws]
@@ -270,9 +271,9 @@ def test_refusals(uw):
             uw.expert_matmul(full.pop("x"), full.pop("w"), r, **full)
     with pytest.raises(ValueError):
         uw.expert_gate_up(x, w, w[:, :32], r)
-    for plan in (uw.make_plan(uw.PIPE_DIRECT_PALETTE, uw.KERNEL_FMA, 1), uw.make_plan(uw.PIPE_DIRECT_PALETTE, uw.KERNEL_TC, 64),
-                 uw.make_plan(uw.PIPE_DIRECT_PALETTE, uw.KERNEL_TC, 128, 2), uw.make_plan(uw.PIPE_DECODE_GEMM, uw.KERNEL_MMA, 4),
-                 uw.make_plan(uw.PIPE_DIRECT_PALETTE, uw.KERNEL_MMA, 9)):
+    P = uw.make_expert_plan
+    for plan in (P(uw.KERNEL_FMA, 1, 0), P(uw.KERNEL_TC, 64), P(uw.KERNEL_TC, 128, 16), P(uw.KERNEL_TC, 128, width=1),
+                 P(uw.KERNEL_MMA, 9), P(uw.KERNEL_MMA, 4, 32), P(uw.KERNEL_MMA, 4, sort=1)):
         with pytest.raises(uw.UwError) as err:
             uw.expert_matmul(x, w, r, gather=True, plan=plan)
         assert err.value.status == uw.ERR_INVALID_ARG
@@ -280,7 +281,10 @@ def test_refusals(uw):
     mats = [uw.Matrix(uw.encode(synth.weights_bf16(64, 128, 0.02, 0.0, 1.0, seed=i))) for i in range(4)]
     s = uw.ExpertSet(mats)
     with pytest.raises(uw.UwError):            # tcgen05 plans take plain weights
-        uw.expert_matmul(x, s, r, gather=True, plan=uw.make_plan(uw.PIPE_DIRECT_PALETTE, uw.KERNEL_TC, 128))
+        uw.expert_matmul(x, s, r, gather=True, plan=P(uw.KERNEL_TC, 128))
+    with pytest.raises(uw.UwError) as err:     # the sorted rows need a workspace
+        uw.expert_matmul(x, w, r, gather=True, plan=P(uw.KERNEL_TC, 128, sort=1), ws=torch.empty(512, device="cuda").byte())
+    assert err.value.status == uw.ERR_WORKSPACE
     with pytest.raises(uw.UwError):            # one form for both
         uw.expert_gate_up(x, s, w, r)
     other = uw.Matrix(uw.encode(synth.weights_bf16(128, 128, 0.02, 0.0, 1.0, seed=9)))

@@ -103,11 +103,12 @@ def test_expert_calls(uw):
     def wset(n=64, k=128, e=4, w=FAKE, stride=64 * 128, table=None):
         return uw.ExpertSetArgs(n, k, e, w, stride, table)
 
-    ok = uw.make_plan(uw.PIPE_DIRECT_PALETTE, uw.KERNEL_MMA, 4)
+    P = uw.make_expert_plan
+    ok = P(uw.KERNEL_MMA, 4)
 
-    def run(r=None, w=None, y=FAKE, ys=64, plan=ok):
+    def run(r=None, w=None, y=FAKE, ys=64, plan=ok, ws=None, nbytes=0):
         r, w = r or rows(), w or wset()
-        return L.uw_expert_matmul(ctypes.byref(r), ctypes.byref(w), y, ys, ctypes.byref(plan), None, None)
+        return L.uw_expert_matmul(ctypes.byref(r), ctypes.byref(w), y, ys, ctypes.byref(plan), ws, nbytes, None, None)
 
     assert run(rows(places=0, off=None, order=None, x=None, x_rows=0)) == uw.UW_OK
     for r in (rows(places=-1), rows(per_row=0), rows(off=None), rows(x=None), rows(x_rows=0), rows(order=None), rows(xs=120),
@@ -120,24 +121,31 @@ def test_expert_calls(uw):
         assert run(w=w) == status
     assert run(y=None) == uw.ERR_INVALID_ARG and run(y=FAKE + 8) == uw.ERR_INVALID_ARG
     assert run(ys=60) == uw.ERR_INVALID_ARG and run(ys=66) == uw.ERR_INVALID_ARG
-    for plan in (uw.make_plan(4, uw.KERNEL_MMA, 0), uw.make_plan(4, uw.KERNEL_MMA, 9), uw.make_plan(4, uw.KERNEL_MMA, 4, 2),
-                 uw.make_plan(4, uw.KERNEL_MMA, 4, 1, 3), uw.make_plan(4, uw.KERNEL_TC, 64), uw.make_plan(4, uw.KERNEL_TC, 256, 1, 4),
-                 uw.make_plan(4, uw.KERNEL_TC_SK, 16), uw.make_plan(1, uw.KERNEL_MMA, 4), uw.make_plan(4, uw.KERNEL_MMA, 4, timeout_ns=-1)):
+    for plan in (P(uw.KERNEL_MMA, 0), P(uw.KERNEL_MMA, 9), P(uw.KERNEL_MMA, 4, 32), P(uw.KERNEL_MMA, 4, width=3),
+                 P(uw.KERNEL_MMA, 4, sort=1), P(uw.KERNEL_TC, 64), P(uw.KERNEL_TC, 256, 0), P(uw.KERNEL_TC, 256, 256),
+                 P(uw.KERNEL_TC, 256, width=1), P(uw.KERNEL_TC_SK, 16), P(uw.KERNEL_MMA, 4, timeout_ns=-1)):
         assert run(plan=plan) == uw.ERR_INVALID_ARG
-    assert run(w=wset(k=192, stride=64 * 192), r=rows(xs=192), plan=uw.make_plan(4, uw.KERNEL_MMA, 4, 1, 2)) == uw.ERR_INVALID_ARG
-    tc = uw.make_plan(4, uw.KERNEL_TC, 256)
+    assert run(w=wset(k=192, stride=64 * 192), r=rows(xs=192), plan=P(uw.KERNEL_MMA, 4, width=2)) == uw.ERR_INVALID_ARG
+    tc = P(uw.KERNEL_TC, 256)
     assert run(w=wset(w=None, table=FAKE), plan=tc) == uw.ERR_INVALID_ARG
+    assert run(w=wset(stride=1 << 39), plan=tc) == uw.ERR_UNSUPPORTED_SHAPE
+    sort, size = P(uw.KERNEL_TC, 256, sort=1), ctypes.c_size_t()
+    for r, want in ((rows(), 16 * 128 * 2), (rows(order=None), 0)):
+        assert L.uw_expert_workspace_size(ctypes.byref(r), ctypes.byref(wset()), ctypes.byref(sort), ctypes.byref(size)) == 0
+        assert size.value == want
+    for ws, nbytes in ((None, 0), (FAKE, 4095), (FAKE + 16, 1 << 20)):
+        assert run(plan=sort, ws=ws, nbytes=nbytes) == uw.ERR_WORKSPACE
 
     def gate_up(a, b, hs=64):
         r = rows()
         return L.uw_expert_gate_up(ctypes.byref(r), ctypes.byref(a), ctypes.byref(b) if b else None, FAKE, hs, ctypes.byref(ok),
-                                   None, None)
+                                   None, 0, None, None)
     for b in (None, wset(n=128, stride=1 << 20), wset(k=64), wset(e=5), wset(w=None, table=FAKE)):
         assert gate_up(wset(), b) == uw.ERR_INVALID_ARG
     assert gate_up(wset(), wset(), 68) == uw.ERR_INVALID_ARG
 
-    p = uw.Plan()
-    for w, places, kernel in ((wset(), 8, uw.KERNEL_MMA), (wset(), 100000, uw.KERNEL_TC),
+    p = uw.ExpertPlan()
+    for w, places, kernel in ((wset(), 8, uw.KERNEL_TC), (wset(), 100000, uw.KERNEL_TC),
                               (wset(w=None, table=FAKE), 100000, uw.KERNEL_MMA)):
         assert L.uw_expert_plan_default(ctypes.byref(w), places, ctypes.byref(p)) == 0 and p.kernel == kernel
     assert L.uw_expert_plan_default(ctypes.byref(wset()), -1, ctypes.byref(p)) == uw.ERR_INVALID_ARG
