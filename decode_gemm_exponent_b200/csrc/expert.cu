@@ -321,6 +321,21 @@ __device__ __forceinline__ void tma_gather4(void *dst, const CUtensorMap *map, i
         : "memory");
 }
 
+// Place in the ring and its phase, as counters: a division per K-step (64-bit,
+// in one thread) took as long as the copies it stands between, 0.4 us.
+struct Slot {
+    int at = 0;
+    uint32_t phase = 0;
+    bool wrapped = false;      // every slot has been used
+    __device__ __forceinline__ void next(int stages) {
+        if (++at == stages) {
+            at = 0;
+            phase ^= 1u;
+            wrapped = true;
+        }
+    }
+};
+
 // BN: weight rows per tile (gate_up: half of them of G, half of U)
 template <int BN, bool GATED>
 __global__ void __launch_bounds__(kTcThreads, 1)
@@ -389,7 +404,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     const int ntn = int((a.n + kCols - 1) / kCols);
-    const int64_t tiles = int64_t(first[a.experts]) * ntn;
+    const int tiles = first[a.experts] * ntn;        // below 2^31: checked by the launch
 
     // row tile mt -> expert (the last one with first[e] <= mt that has tiles), rows
     auto locate = [&](int mt) {
@@ -404,21 +419,26 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         return Span{lo, p0 + skip, min(a.bm, p1 - p0 - skip)};
     };
 
+    // wait for the copies of the last S uses of the ring (all landed unless the
+    // kernel gives up)
+    auto drain = [&](const Slot &r, uint64_t *full) {
+        for (int s = 0; s < S; s++)
+            if (s < r.at) mbar_wait(&full[s], r.phase, T);
+            else if (r.wrapped) mbar_wait(&full[s], r.phase ^ 1u, T);
+    };
+
     if (warp == 0) {
         // ------------------------------------------------ weights
         if (lane == 0) {
-            int64_t it = 0;
+            Slot r;
             bool ok = true;
-            for (int64_t tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x) {
-                const Span t = locate(int(tile / ntn));
-                const int n0 = int(tile % ntn) * kCols;
-                for (int ks = 0; ks < a.ksteps; ks++, it++) {
-                    const int s = int(it % S);
-                    if (it >= S) ok = mbar_wait_or_abort(&empty[s], (uint32_t(it / S) & 1u) ^ 1u, T, abort_flag);
-                    if (!ok || *abort_flag) {
-                        ok = false;
-                        break;
-                    }
+            for (int tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x) {
+                const int mt = tile / ntn, n0 = (tile - mt * ntn) * kCols;
+                const Span t = locate(mt);
+                for (int ks = 0; ks < a.ksteps; ks++, r.next(S)) {
+                    const int s = r.at;
+                    ok = mbar_wait_or_abort(&empty[s], r.phase ^ 1u, T, abort_flag) && !*abort_flag;
+                    if (!ok) break;
                     uint8_t *st = wring + size_t(s) * kW;
                     mbar_arrive_expect_tx(&wfull[s], uint32_t(kW));
                     if (GATED) {
@@ -433,7 +453,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 if (!*abort_flag) flag_error(a.status, UW_DEVERR_TIMEOUT);
                 *abort_flag = 1;
             }
-            for (int64_t i = max(int64_t(0), it - S); i < it; i++) mbar_wait(&wfull[i % S], uint32_t(i / S) & 1u, T);
+            drain(r, wfull);
         }
         __syncwarp();
     } else if (warp == 1) {
@@ -441,20 +461,20 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         if (lane == 0) {
             constexpr uint32_t idesc = idesc_bf16_f32(kBM, BN);
             const int chunk = GATED ? a.ksteps : kSumSteps;
-            int64_t it = 0;
+            Slot r;
             uint32_t acc = 0;
             bool ok = true;
-            for (int64_t tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x) {
+            for (int tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x) {
                 for (int k0 = 0; k0 < a.ksteps && ok; k0 += chunk, acc++) {
                     const uint32_t b = acc & 1u;
                     if (acc >= 2) ok = mbar_wait_or_abort(&acce[b], ((acc >> 1) & 1u) ^ 1u, T, abort_flag);
                     if (!ok) break;
                     tc_fence_after();
                     const int k1 = min(a.ksteps, k0 + chunk);
-                    for (int ks = k0; ks < k1; ks++, it++) {
-                        const int s = int(it % S);
-                        ok = mbar_wait_or_abort(&xfull[s], uint32_t(it / S) & 1u, T, abort_flag) &&
-                             mbar_wait_or_abort(&wfull[s], uint32_t(it / S) & 1u, T, abort_flag);
+                    for (int ks = k0; ks < k1; ks++, r.next(S)) {
+                        const int s = r.at;
+                        ok = mbar_wait_or_abort(&xfull[s], r.phase, T, abort_flag) &&
+                             mbar_wait_or_abort(&wfull[s], r.phase, T, abort_flag);
                         if (!ok) break;
                         tc_fence_after();
                         const uint32_t sx = smem_addr(ring + size_t(s) * xtile), sw = smem_addr(wring + size_t(s) * kW);
@@ -478,10 +498,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         __syncwarp();
     } else if (warp == 2) {
         // ------------------------------------------------ rows of x
-        int64_t it = 0;
+        Slot r;
         bool ok = true;
-        for (int64_t tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x) {
-            const Span t = locate(int(tile / ntn));
+        for (int tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x) {
+            const Span t = locate(tile / ntn);
             int32_t row[4];
             int copies, bytes;           // one copy per lane
             if (a.boxes) {
@@ -495,9 +515,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 for (int i = 0; i < 4; i++)
                     row[i] = int32_t(source_row(a.order, a.per_row, a.x_rows, t.pos + min(4 * lane + i, t.rows - 1)));
             }
-            for (int ks = 0; ks < a.ksteps; ks++, it++) {
-                const int s = int(it % S);
-                if (it >= S) ok = mbar_wait_or_abort(&empty[s], (uint32_t(it / S) & 1u) ^ 1u, T, abort_flag);
+            for (int ks = 0; ks < a.ksteps; ks++, r.next(S)) {
+                const int s = r.at;
+                ok = mbar_wait_or_abort(&empty[s], r.phase ^ 1u, T, abort_flag);
                 ok = __all_sync(kAll, ok && !*abort_flag);
                 if (!ok) break;
                 if (lane == 0) mbar_arrive_expect_tx(&xfull[s], uint32_t(copies * bytes));
@@ -513,8 +533,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             if (!*abort_flag) flag_error(a.status, UW_DEVERR_TIMEOUT);
             *abort_flag = 1;
         }
-        if (lane == 0)
-            for (int64_t i = max(int64_t(0), it - S); i < it; i++) mbar_wait(&xfull[i % S], uint32_t(i / S) & 1u, T);
+        if (lane == 0) drain(r, xfull);
         __syncwarp();
     } else if (warp >= 4) {
         // ------------------------------------------------ epilogue: lane = token
@@ -522,9 +541,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const uint32_t lane_base = tmem + (uint32_t(q * 32) << 16);
         uint32_t acc = 0;
         bool ok = true;
-        for (int64_t tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x) {
-            const Span t = locate(int(tile / ntn));
-            const int64_t n0 = (tile % ntn) * kCols;
+        for (int tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x) {
+            const int mt = tile / ntn;
+            const Span t = locate(mt);
+            const int64_t n0 = int64_t(tile - mt * ntn) * kCols;
             const int tok = q * 32 + lane;
             if constexpr (GATED) {
                 constexpr int kMine = kCols / 2;
@@ -704,6 +724,7 @@ cudaError_t launch_tc(const ExpertLaunch &p, cudaStream_t stream) {
     a.status = p.status;
     const int64_t row_tiles = (p.places + (bm - 1) * std::min<int64_t>(p.experts, p.places)) / bm;
     const int64_t tiles = row_tiles * ((p.n + (GATED ? BN / 2 : BN) - 1) / (GATED ? BN / 2 : BN));
+    if (tiles >= (int64_t(1) << 31) - 4096) return cudaErrorInvalidValue;
     const unsigned grid = unsigned(std::min<int64_t>(sm_count(), tiles));
     k_expert_tc<BN, GATED><<<grid, kTcThreads, smem, stream>>>(mx, ma, mb, a);
     return cudaGetLastError();
