@@ -295,6 +295,7 @@ struct TcExpertArgs {
     int experts, per_row, ksteps, stages;
     int bm;                    // rows per tile: 32, 64 or 128
     int boxes;                 // x is in expert order: tiled copies instead of gathers
+    int wide;                  // rows of y are 32-byte aligned
     int64_t places, x_rows, n;
     const int32_t *offsets, *order;
     void *y;
@@ -310,6 +311,13 @@ __device__ __forceinline__ void tma_load_3d(void *dst, const CUtensorMap *map, i
             smem_addr(dst)),
         "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_addr(bar))
         : "memory");
+}
+
+// 32 bytes, 32-byte aligned
+__device__ __forceinline__ void store32(void *p, const uint32_t (&v)[8]) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]),
+                 "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
 }
 
 // four rows of a 2-D tensor, one after the other in shared memory
@@ -350,8 +358,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     // least one weight tile) reaches only accumulator rows that are not read.
     const int S = a.stages, xtile = a.bm * kBK * 2;
     uint8_t *wring = ring + size_t(S) * xtile;
-    uint64_t *xfull = reinterpret_cast<uint64_t *>(wring + size_t(S) * kW);
-    uint64_t *wfull = xfull + S, *empty = wfull + S, *accf = empty + S, *acce = accf + 2;
+    uint64_t *full = reinterpret_cast<uint64_t *>(wring + size_t(S) * kW);
+    uint64_t *empty = full + S, *accf = empty + S, *acce = accf + 2;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(acce + 2);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
     int32_t *first = reinterpret_cast<int32_t *>(tmem_slot + 2);     // [experts + 1] row tiles before each expert
@@ -361,8 +369,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < S; s++) {
-            mbar_init(&xfull[s], 1);
-            mbar_init(&wfull[s], 1);
+            mbar_init(&full[s], 2);          // weights, rows of x
             mbar_init(&empty[s], 1);
         }
         for (int b = 0; b < 2; b++) {
@@ -420,8 +427,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     };
 
     // wait for the copies of the last S uses of the ring (all landed unless the
-    // kernel gives up)
-    auto drain = [&](const Slot &r, uint64_t *full) {
+    // kernel gives up; the limit covers a stage that the other producer left)
+    auto drain = [&](const Slot &r) {
         for (int s = 0; s < S; s++)
             if (s < r.at) mbar_wait(&full[s], r.phase, T);
             else if (r.wrapped) mbar_wait(&full[s], r.phase ^ 1u, T);
@@ -440,12 +447,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     ok = mbar_wait_or_abort(&empty[s], r.phase ^ 1u, T, abort_flag) && !*abort_flag;
                     if (!ok) break;
                     uint8_t *st = wring + size_t(s) * kW;
-                    mbar_arrive_expect_tx(&wfull[s], uint32_t(kW));
+                    mbar_arrive_expect_tx(&full[s], uint32_t(kW));
                     if (GATED) {
-                        tma_load_3d(st, &tmA, ks * kBK, n0, t.expert, &wfull[s]);
-                        tma_load_3d(st + kW / 2, &tmB, ks * kBK, n0, t.expert, &wfull[s]);
+                        tma_load_3d(st, &tmA, ks * kBK, n0, t.expert, &full[s]);
+                        tma_load_3d(st + kW / 2, &tmB, ks * kBK, n0, t.expert, &full[s]);
                     } else {
-                        tma_load_3d(st, &tmA, ks * kBK, n0, t.expert, &wfull[s]);
+                        tma_load_3d(st, &tmA, ks * kBK, n0, t.expert, &full[s]);
                     }
                 }
             }
@@ -453,7 +460,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 if (!*abort_flag) flag_error(a.status, UW_DEVERR_TIMEOUT);
                 *abort_flag = 1;
             }
-            drain(r, wfull);
+            drain(r);
         }
         __syncwarp();
     } else if (warp == 1) {
@@ -473,8 +480,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     const int k1 = min(a.ksteps, k0 + chunk);
                     for (int ks = k0; ks < k1; ks++, r.next(S)) {
                         const int s = r.at;
-                        ok = mbar_wait_or_abort(&xfull[s], r.phase, T, abort_flag) &&
-                             mbar_wait_or_abort(&wfull[s], r.phase, T, abort_flag);
+                        ok = mbar_wait_or_abort(&full[s], r.phase, T, abort_flag);
                         if (!ok) break;
                         tc_fence_after();
                         const uint32_t sx = smem_addr(ring + size_t(s) * xtile), sw = smem_addr(wring + size_t(s) * kW);
@@ -497,7 +503,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         }
         __syncwarp();
     } else if (warp == 2) {
-        // ------------------------------------------------ rows of x
+        // ------------------------------------------------ rows of x, TMA
         Slot r;
         bool ok = true;
         for (int tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x) {
@@ -520,12 +526,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 ok = mbar_wait_or_abort(&empty[s], r.phase ^ 1u, T, abort_flag);
                 ok = __all_sync(kAll, ok && !*abort_flag);
                 if (!ok) break;
-                if (lane == 0) mbar_arrive_expect_tx(&xfull[s], uint32_t(copies * bytes));
+                if (lane == 0) mbar_arrive_expect_tx(&full[s], uint32_t(copies * bytes));
                 __syncwarp();
                 if (lane < copies) {
                     uint8_t *dst = ring + size_t(s) * xtile + lane * bytes;
-                    if (a.boxes) tma_load_2d(dst, &tmX, ks * kBK, row[0], &xfull[s]);
-                    else tma_gather4(dst, &tmX, ks * kBK, row, &xfull[s]);
+                    if (a.boxes) tma_load_2d(dst, &tmX, ks * kBK, row[0], &full[s]);
+                    else tma_gather4(dst, &tmX, ks * kBK, row, &full[s]);
                 }
             }
         }
@@ -533,7 +539,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             if (!*abort_flag) flag_error(a.status, UW_DEVERR_TIMEOUT);
             *abort_flag = 1;
         }
-        if (lane == 0) drain(r, xfull);
+        if (lane == 0) drain(r);
         __syncwarp();
     } else if (warp >= 4) {
         // ------------------------------------------------ epilogue: lane = token
@@ -569,8 +575,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                             const __nv_bfloat162 p = __floats2bfloat162_rn(h0, h1);
                             o[i] = *reinterpret_cast<const uint32_t *>(&p);
                         }
-                        *reinterpret_cast<uint4 *>(out + c) = make_uint4(o[0], o[1], o[2], o[3]);
-                        *reinterpret_cast<uint4 *>(out + c + 8) = make_uint4(o[4], o[5], o[6], o[7]);
+                        if (a.wide) {
+                            store32(out + c, o);
+                        } else {
+                            *reinterpret_cast<uint4 *>(out + c) = make_uint4(o[0], o[1], o[2], o[3]);
+                            *reinterpret_cast<uint4 *>(out + c + 8) = make_uint4(o[4], o[5], o[6], o[7]);
+                        }
                     }
                 }
                 tc_fence_before();
@@ -604,9 +614,20 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 float *out = static_cast<float *>(a.y) + int64_t(t.pos + tok) * a.y_stride + n0 + half * kMine;
                 if (tok < t.rows) {
 #pragma unroll
-                    for (int c = 0; c < kMine; c += 4)
-                        if (n0 + half * kMine + c < a.n)
+                    for (int c = 0; c < kMine; c += 8) {
+                        if (n0 + half * kMine + c >= a.n) break;
+                        if (a.wide) {
+                            const uint32_t o[8] = {__float_as_uint(sum[c]),     __float_as_uint(sum[c + 1]),
+                                                   __float_as_uint(sum[c + 2]), __float_as_uint(sum[c + 3]),
+                                                   __float_as_uint(sum[c + 4]), __float_as_uint(sum[c + 5]),
+                                                   __float_as_uint(sum[c + 6]), __float_as_uint(sum[c + 7])};
+                            store32(out + c, o);
+                        } else {
                             *reinterpret_cast<float4 *>(out + c) = make_float4(sum[c], sum[c + 1], sum[c + 2], sum[c + 3]);
+                            *reinterpret_cast<float4 *>(out + c + 4) =
+                                make_float4(sum[c + 4], sum[c + 5], sum[c + 6], sum[c + 7]);
+                        }
+                    }
                 }
             }
         }
@@ -683,7 +704,7 @@ bool weight_map(CUtensorMap *map, const ExpertSet &s, int experts, int64_t n, in
 template <int BN, bool GATED>
 cudaError_t launch_tc(const ExpertLaunch &p, cudaStream_t stream) {
     constexpr int kMaxSmem = 232448;
-    const int bm = p.bm, stage = bm * kBK * 2 + BN * kBK * 2 + 24;      // tiles and three barriers
+    const int bm = p.bm, stage = bm * kBK * 2 + BN * kBK * 2 + 16;      // tiles and two barriers
     const int tail = 1024 + 64 + (p.experts + 4) * 4;
     const int stages = std::min(12, (kMaxSmem - tail) / stage);
     if (stages < 2) return cudaErrorInvalidValue;
@@ -713,6 +734,7 @@ cudaError_t launch_tc(const ExpertLaunch &p, cudaStream_t stream) {
     a.stages = stages;
     a.bm = bm;
     a.boxes = boxes;
+    a.wide = ((reinterpret_cast<uintptr_t>(p.y) | uintptr_t(p.y_stride) * (GATED ? 2 : 4)) & 31u) == 0;
     a.places = p.places;
     a.x_rows = p.x_rows;
     a.n = p.n;

@@ -20,7 +20,7 @@
 // Second product, out = y + V B^T: tokens are M, output columns N.  V keeps its
 // 32 bits: it is split into three BF16 parts (8 + 8 + 8 bits of mantissa), whose
 // products with B are exact in the MMA.  A warp takes 16 rows x 32 columns; the
-// four MMA column tiles interleave so that a thread owns eight consecutive
+// MMA column tiles interleave in pairs so that a thread owns runs of four
 // columns and reads y and writes out in 16-byte pieces.
 //
 // Bound: for many rows, the bytes of y and out (8 t n); for one token per
@@ -250,10 +250,11 @@ __global__ void __launch_bounds__(kExpandWarps * 32) k_lora_expand(const LoraArg
     }
     const int64_t n0 = (int64_t(blockIdx.y) * kExpandWarps + warp) * a.steps * 32;
     const int steps = int(max(int64_t(0), min(int64_t(a.steps), (a.n - n0) / 32)));
-    // column tile q, MMA column j is output column 8 (j / 2) + 2 q + j % 2 of the step's 32
-    const uint16_t *pb = a.b + (int64_t(min(tile.group, a.groups - 1)) * a.n + n0 + 8 * (g >> 1) + (g & 1)) * a.max_rank + 4 * c;
-    const float *py[2] = {a.y + row[0] * a.y_stride + n0 + 8 * c, a.y + row[1] * a.y_stride + n0 + 8 * c};
-    float *po[2] = {a.out + row[0] * a.out_stride + n0 + 8 * c, a.out + row[1] * a.out_stride + n0 + 8 * c};
+    // column tile q, MMA column j is output column 16 (q / 2) + 4 (j / 2) + 2 (q % 2) + j % 2
+    // of the step's 32: a row's four lanes read and write 64 bytes at a time
+    const uint16_t *pb = a.b + (int64_t(min(tile.group, a.groups - 1)) * a.n + n0 + 4 * (g >> 1) + (g & 1)) * a.max_rank + 4 * c;
+    const float *py[2] = {a.y + row[0] * a.y_stride + n0 + 4 * c, a.y + row[1] * a.y_stride + n0 + 4 * c};
+    float *po[2] = {a.out + row[0] * a.out_stride + n0 + 4 * c, a.out + row[1] * a.out_stride + n0 + 4 * c};
 
     // B of chunks [j0, j0 + C) for the step at column offset `n`; ranks past the
     // adapter's are zeroed, whatever its storage holds there
@@ -265,7 +266,7 @@ __global__ void __launch_bounds__(kExpandWarps * 32) k_lora_expand(const LoraArg
             for (int q = 0; q < 4; q++) {
                 w[j][q] = make_uint2(0u, 0u);
                 if (r < rank) {
-                    w[j][q] = __ldg(reinterpret_cast<const uint2 *>(pb + (n + 2 * q) * a.max_rank + 16 * (j0 + j)));
+                    w[j][q] = __ldg(reinterpret_cast<const uint2 *>(pb + (n + 16 * (q >> 1) + 2 * (q & 1)) * a.max_rank + 16 * (j0 + j)));
                     if (r + 4 > rank) {
                         const int left = rank - r;     // 1, 2 or 3 ranks
                         if (left < 2) w[j][q].x &= 0xFFFFu;
@@ -280,8 +281,8 @@ __global__ void __launch_bounds__(kExpandWarps * 32) k_lora_expand(const LoraArg
         for (int h = 0; h < 2; h++) {
             v[h][0] = v[h][1] = make_float4(0.f, 0.f, 0.f, 0.f);
             if (live[h]) {
-                v[h][0] = *reinterpret_cast<const float4 *>(py[h] + n);
-                v[h][1] = *reinterpret_cast<const float4 *>(py[h] + n + 4);
+                v[h][0] = __ldcs(reinterpret_cast<const float4 *>(py[h] + n));
+                v[h][1] = __ldcs(reinterpret_cast<const float4 *>(py[h] + n + 16));
             }
         }
     };
@@ -364,11 +365,10 @@ __global__ void __launch_bounds__(kExpandWarps * 32) k_lora_expand(const LoraArg
         for (int h = 0; h < 2; h++) {
             if (!live[h]) continue;
             float *o = po[h] + int64_t(s) * 32;
-            // columns 8 c + 2 q + {0, 1} come from column tile q
-            *reinterpret_cast<float4 *>(o) = make_float4(cy[h][0].x + d[0][2 * h], cy[h][0].y + d[0][2 * h + 1],
-                                                         cy[h][0].z + d[1][2 * h], cy[h][0].w + d[1][2 * h + 1]);
-            *reinterpret_cast<float4 *>(o + 4) = make_float4(cy[h][1].x + d[2][2 * h], cy[h][1].y + d[2][2 * h + 1],
-                                                             cy[h][1].z + d[3][2 * h], cy[h][1].w + d[3][2 * h + 1]);
+            __stcs(reinterpret_cast<float4 *>(o), make_float4(cy[h][0].x + d[0][2 * h], cy[h][0].y + d[0][2 * h + 1],
+                                                              cy[h][0].z + d[1][2 * h], cy[h][0].w + d[1][2 * h + 1]));
+            __stcs(reinterpret_cast<float4 *>(o + 16), make_float4(cy[h][1].x + d[2][2 * h], cy[h][1].y + d[2][2 * h + 1],
+                                                                   cy[h][1].z + d[3][2 * h], cy[h][1].w + d[3][2 * h + 1]));
         }
     }
 }
