@@ -23,7 +23,6 @@
 // accumulates (about 1.1e-9 per unit of K, relative, measured), so FP32 outputs
 // are summed in registers over chunks of 512 of K; BF16 outputs need no chunks.
 #include <algorithm>
-#include <atomic>
 #include <cstring>
 
 #include <cuda_bf16.h>
@@ -718,15 +717,9 @@ cudaError_t launch_tc(const ExpertLaunch &p, cudaStream_t stream) {
     if (!make_map(&mx, p.x, 2, xd, xs, xb) || !weight_map(&ma, p.a, p.experts, p.n, p.k, rows)) return cudaErrorInvalidValue;
     mb = ma;
     if (GATED && !weight_map(&mb, p.b, p.experts, p.n, p.k, rows)) return cudaErrorInvalidValue;
-    int dev = 0;
-    cudaError_t err = cudaGetDevice(&dev);
+    static std::atomic<uint64_t> allowed{0};
+    const cudaError_t err = allow_smem(k_expert_tc<BN, GATED>, kMaxSmem, allowed);
     if (err != cudaSuccess) return err;
-    static std::atomic<uint64_t> ready{0};           // devices whose shared-memory limit is raised
-    if (dev >= 64 || !(ready.load(std::memory_order_acquire) >> dev & 1u)) {
-        err = cudaFuncSetAttribute(k_expert_tc<BN, GATED>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
-        if (err != cudaSuccess) return err;
-        if (dev < 64) ready.fetch_or(uint64_t(1) << dev, std::memory_order_release);
-    }
     TcExpertArgs a{};
     a.experts = p.experts;
     a.per_row = p.per_row;

@@ -1,5 +1,6 @@
 // kernels.h -- host-side launch interface of the libuw CUDA kernels (internal).
 #pragma once
+#include <atomic>
 #include <utility>
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -156,6 +157,19 @@ cudaError_t launch_pdl(bool early, void (*kernel)(KArgs...), dim3 grid, dim3 blo
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
+}
+
+// Allow `kernel` up to `bytes` of dynamic shared memory on the current device, once
+// per device (`done`: a bit per device, one word per kernel).
+template <class K>
+cudaError_t allow_smem(K kernel, size_t bytes, std::atomic<uint64_t> &done) {
+    int dev = 0;
+    cudaError_t err = cudaGetDevice(&dev);
+    if (err != cudaSuccess) return err;
+    if (dev < 64 && (done.load(std::memory_order_acquire) >> dev & 1u)) return cudaSuccess;
+    err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(bytes));
+    if (err == cudaSuccess && dev < 64) done.fetch_or(uint64_t(1) << dev, std::memory_order_release);
+    return err;
 }
 
 struct TcLaunch {

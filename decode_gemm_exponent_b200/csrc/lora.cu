@@ -42,6 +42,8 @@ constexpr uint32_t kAll = 0xFFFFFFFFu;
 constexpr int kShrinkWarps = 8;
 constexpr int kExpandWarps = 4;
 constexpr int kTileM = 16;                // rows per tile of the second product
+constexpr int kAhead = 4;                 // steps of y in flight per warp
+constexpr size_t kExpandSmem = size_t(kAhead) * 4 * kExpandWarps * 32 * 16;
 
 struct LoraArgs {
     const uint16_t *x;
@@ -112,7 +114,7 @@ __device__ __forceinline__ int rank_of(const LoraArgs &a, int group) {
 
 // RT: 16-rank tiles, NT: 8-token tiles per CTA.  Grid: row tile, K slice, rank part.
 template <int RT, int NT>
-__global__ void __launch_bounds__(kShrinkWarps * 32) k_lora_shrink(const LoraArgs a) {
+__global__ void __launch_bounds__(kShrinkWarps * 32, 2) k_lora_shrink(const LoraArgs a) {
     __shared__ Tile s_tile;
     __shared__ float red[kShrinkWarps][RT * NT * 4][32];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
@@ -221,12 +223,17 @@ __device__ __forceinline__ void split3(float v, uint32_t (&p)[3]) {
     p[2] = bf16_bits((v - h) - __uint_as_float(p[1] << 16));
 }
 
-// C: 16-rank chunks whose B loads are in flight together.  Dynamic shared
-// memory: fragments of V, [chunk][part][lane] uint4.
+// C: 16-rank chunks whose B loads are in flight together.  Fragments of V:
+// [chunk][part][lane] uint4.
 template <int C>
-__global__ void __launch_bounds__(kExpandWarps * 32) k_lora_expand(const LoraArgs a) {
-    extern __shared__ uint4 s_frag[];
+__global__ void __launch_bounds__(kExpandWarps * 32, C == 4 ? 3 : 4) k_lora_expand(const LoraArgs a) {
+    // dynamic shared memory: y on its way, then the fragments of V
+    extern __shared__ uint4 s_dyn[];
     __shared__ Tile s_tile;
+    // y on its way: every thread copies the pieces that it will read itself, so
+    // a wait for its own copies is all the synchronisation there is
+    float4 (*s_y)[4][kExpandWarps * 32] = reinterpret_cast<float4 (*)[4][kExpandWarps * 32]>(s_dyn);
+    uint4 *s_frag = s_dyn + kAhead * 4 * kExpandWarps * 32;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
     if (warp == 0) {
         const Tile f = find_tile(a, kTileM, blockIdx.x, a.copy_rest != 0);
@@ -276,22 +283,21 @@ __global__ void __launch_bounds__(kExpandWarps * 32) k_lora_expand(const LoraArg
             }
         }
     };
-    auto load_y = [&](float4 (&v)[2][2], int64_t n) {
+    auto fetch_y = [&](int step) {
+        if (step < steps) {
 #pragma unroll
-        for (int h = 0; h < 2; h++) {
-            v[h][0] = v[h][1] = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (live[h]) {
-                v[h][0] = __ldcs(reinterpret_cast<const float4 *>(py[h] + n));
-                v[h][1] = __ldcs(reinterpret_cast<const float4 *>(py[h] + n + 16));
+            for (int h = 0; h < 2; h++) {
+                if (!live[h]) continue;
+                cp_async16(&s_y[step % kAhead][2 * h][threadIdx.x], py[h] + int64_t(step) * 32);
+                cp_async16(&s_y[step % kAhead][2 * h + 1][threadIdx.x], py[h] + int64_t(step) * 32 + 16);
             }
         }
+        asm volatile("cp.async.commit_group;" ::: "memory");
     };
     uint2 w[C][4];
-    float4 yv[2][2];
-    if (steps > 0) {
-        load_b(w, 0, 0);
-        load_y(yv, 0);
-    }
+    if (steps > 0) load_b(w, 0, 0);
+#pragma unroll
+    for (int s = 0; s < kAhead - 1; s++) fetch_y(s);
 
     pdl_wait();   // V is the previous kernel's; everything read so far is older
     // fragments: lane (g, c) holds ranks 16 j + 4 c .. + 3 of rows g and g + 8
@@ -357,10 +363,15 @@ __global__ void __launch_bounds__(kExpandWarps * 32) k_lora_expand(const LoraArg
                 }
             }
         }
+        // the slot of step s + kAhead - 1 was read in the step before this one
+        fetch_y(s + kAhead - 1);
+        asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory");
         float4 cy[2][2];
 #pragma unroll
-        for (int h = 0; h < 2; h++) cy[h][0] = yv[h][0], cy[h][1] = yv[h][1];
-        if (s + 1 < steps) load_y(yv, int64_t(s + 1) * 32);
+        for (int h = 0; h < 2; h++) {
+            cy[h][0] = s_y[s % kAhead][2 * h][threadIdx.x];
+            cy[h][1] = s_y[s % kAhead][2 * h + 1][threadIdx.x];
+        }
 #pragma unroll
         for (int h = 0; h < 2; h++) {
             if (!live[h]) continue;
@@ -371,6 +382,7 @@ __global__ void __launch_bounds__(kExpandWarps * 32) k_lora_expand(const LoraArg
                                                                    cy[h][1].z + d[3][2 * h], cy[h][1].w + d[3][2 * h + 1]));
         }
     }
+    asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
 // most tiles of `size` rows that t rows in at most `groups` groups can make
@@ -437,11 +449,16 @@ cudaError_t launch_lora(const LoraLaunch &p, cudaStream_t stream) {
     a.steps = int(std::max<int64_t>(1, std::min<int64_t>(16, total / (148 * 16))));
     const int64_t per_cta = int64_t(kExpandWarps) * a.steps * 32;
     const dim3 grid2(unsigned(geo.expand_tiles), unsigned((p.n + per_cta - 1) / per_cta));
-    const size_t smem = size_t(rt) * 3 * 32 * 16;
+    const size_t smem = size_t(rt) * 3 * 32 * 16 + kExpandSmem;
     const dim3 block2(kExpandWarps * 32);
-    if (rt == 1) err = launch_pdl(true, k_lora_expand<1>, grid2, block2, smem, stream, a);
-    else if (rt == 2) err = launch_pdl(true, k_lora_expand<2>, grid2, block2, smem, stream, a);
-    else err = launch_pdl(true, k_lora_expand<4>, grid2, block2, smem, stream, a);
+    static std::atomic<uint64_t> allowed[3];
+#define UW_EXPAND(C_, I_)                                                              \
+    err = allow_smem(k_lora_expand<C_>, kExpandSmem + 16 * 3 * 32 * 16, allowed[I_]); \
+    if (err == cudaSuccess) err = launch_pdl(true, k_lora_expand<C_>, grid2, block2, smem, stream, a)
+    if (rt == 1) { UW_EXPAND(1, 0); }
+    else if (rt == 2) { UW_EXPAND(2, 1); }
+    else { UW_EXPAND(4, 2); }
+#undef UW_EXPAND
     return err != cudaSuccess ? err : cudaGetLastError();
 }
 
