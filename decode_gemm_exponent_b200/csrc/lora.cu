@@ -41,8 +41,7 @@ using namespace dev;
 constexpr uint32_t kAll = 0xFFFFFFFFu;
 constexpr int kShrinkWarps = 8;
 constexpr int kExpandWarps = 4;
-constexpr int kTileM = 16;                // rows per tile of the second product
-constexpr int kAhead = 4;                 // steps of y in flight per warp
+constexpr int kAhead = 4;                 // units (16 rows x 32 columns) of y in flight per warp, with the current one
 constexpr size_t kExpandSmem = size_t(kAhead) * 4 * kExpandWarps * 32 * 16;
 
 struct LoraArgs {
@@ -223,21 +222,27 @@ __device__ __forceinline__ void split3(float v, uint32_t (&p)[3]) {
     p[2] = bf16_bits((v - h) - __uint_as_float(p[1] << 16));
 }
 
-// C: 16-rank chunks whose B loads are in flight together.  Fragments of V:
-// [chunk][part][lane] uint4.
-template <int C>
+// C: 16-rank chunks whose B loads are in flight together; MT: 16-row parts of a
+// tile, which share the loads of B.  Fragments of V: [part][chunk][piece][lane].
+template <int C, int MT>
 __global__ void __launch_bounds__(kExpandWarps * 32, C == 4 ? 3 : 4) k_lora_expand(const LoraArgs a) {
     // dynamic shared memory: y on its way, then the fragments of V
     extern __shared__ uint4 s_dyn[];
     __shared__ Tile s_tile;
+    __shared__ int32_t s_row[16 * MT];       // rows of the tile, -1: none
     // y on its way: every thread copies the pieces that it will read itself, so
     // a wait for its own copies is all the synchronisation there is
     float4 (*s_y)[4][kExpandWarps * 32] = reinterpret_cast<float4 (*)[4][kExpandWarps * 32]>(s_dyn);
     uint4 *s_frag = s_dyn + kAhead * 4 * kExpandWarps * 32;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
     if (warp == 0) {
-        const Tile f = find_tile(a, kTileM, blockIdx.x, a.copy_rest != 0);
+        const Tile f = find_tile(a, 16 * MT, blockIdx.x, a.copy_rest != 0);
         if (lane == 0) s_tile = f;
+        if (f.group >= 0)
+            for (int i = lane; i < 16 * MT; i += 32) {
+                const int32_t r = i < f.rows ? __ldg(a.order + f.pos + i) : -1;
+                s_row[i] = uint32_t(r) < uint32_t(a.t) ? r : -1;
+            }
     }
     __syncthreads();
     const Tile tile = s_tile;
@@ -246,22 +251,13 @@ __global__ void __launch_bounds__(kExpandWarps * 32, C == 4 ? 3 : 4) k_lora_expa
     if (rank == 0 && !a.copy_rest) return;
     const int chunks = (rank + 15) / 16;
 
-    // this thread's two rows of y and out
-    int64_t row[2];
-    bool live[2];
-#pragma unroll
-    for (int h = 0; h < 2; h++) {
-        live[h] = g + 8 * h < tile.rows;
-        row[h] = live[h] ? __ldg(a.order + tile.pos + g + 8 * h) : 0;
-        live[h] = live[h] && row[h] >= 0 && row[h] < a.t;
-    }
     const int64_t n0 = (int64_t(blockIdx.y) * kExpandWarps + warp) * a.steps * 32;
     const int steps = int(max(int64_t(0), min(int64_t(a.steps), (a.n - n0) / 32)));
+    const int parts = (tile.rows + 15) / 16;           // of this tile, <= MT
+    const int units = steps * parts;
     // column tile q, MMA column j is output column 16 (q / 2) + 4 (j / 2) + 2 (q % 2) + j % 2
     // of the step's 32: a row's four lanes read and write 64 bytes at a time
     const uint16_t *pb = a.b + (int64_t(min(tile.group, a.groups - 1)) * a.n + n0 + 4 * (g >> 1) + (g & 1)) * a.max_rank + 4 * c;
-    const float *py[2] = {a.y + row[0] * a.y_stride + n0 + 4 * c, a.y + row[1] * a.y_stride + n0 + 4 * c};
-    float *po[2] = {a.out + row[0] * a.out_stride + n0 + 4 * c, a.out + row[1] * a.out_stride + n0 + 4 * c};
 
     // B of chunks [j0, j0 + C) for the step at column offset `n`; ranks past the
     // adapter's are zeroed, whatever its storage holds there
@@ -273,7 +269,8 @@ __global__ void __launch_bounds__(kExpandWarps * 32, C == 4 ? 3 : 4) k_lora_expa
             for (int q = 0; q < 4; q++) {
                 w[j][q] = make_uint2(0u, 0u);
                 if (r < rank) {
-                    w[j][q] = __ldg(reinterpret_cast<const uint2 *>(pb + (n + 16 * (q >> 1) + 2 * (q & 1)) * a.max_rank + 16 * (j0 + j)));
+                    w[j][q] = __ldg(reinterpret_cast<const uint2 *>(pb + (n + 16 * (q >> 1) + 2 * (q & 1)) * a.max_rank +
+                                                                    16 * (j0 + j)));
                     if (r + 4 > rank) {
                         const int left = rank - r;     // 1, 2 or 3 ranks
                         if (left < 2) w[j][q].x &= 0xFFFFu;
@@ -283,13 +280,24 @@ __global__ void __launch_bounds__(kExpandWarps * 32, C == 4 ? 3 : 4) k_lora_expa
             }
         }
     };
-    auto fetch_y = [&](int step) {
-        if (step < steps) {
+    // units of 16 rows x 32 columns, the parts of a step one after the other
+    int fetch_part = 0, fetch_slot = 0, fetched = 0;
+    int64_t fetch_n = n0 + 4 * c;
+    auto fetch_y = [&]() {
+        if (fetched < units) {
 #pragma unroll
             for (int h = 0; h < 2; h++) {
-                if (!live[h]) continue;
-                cp_async16(&s_y[step % kAhead][2 * h][threadIdx.x], py[h] + int64_t(step) * 32);
-                cp_async16(&s_y[step % kAhead][2 * h + 1][threadIdx.x], py[h] + int64_t(step) * 32 + 16);
+                const int32_t r = s_row[16 * fetch_part + 8 * h + g];
+                if (r < 0) continue;
+                const float *p = a.y + r * a.y_stride + fetch_n;
+                cp_async16(&s_y[fetch_slot][2 * h][threadIdx.x], p);
+                cp_async16(&s_y[fetch_slot][2 * h + 1][threadIdx.x], p + 16);
+            }
+            fetched++;
+            fetch_slot = fetch_slot + 1 == kAhead ? 0 : fetch_slot + 1;
+            if (++fetch_part == parts) {
+                fetch_part = 0;
+                fetch_n += 32;
             }
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
@@ -297,21 +305,22 @@ __global__ void __launch_bounds__(kExpandWarps * 32, C == 4 ? 3 : 4) k_lora_expa
     uint2 w[C][4];
     if (steps > 0) load_b(w, 0, 0);
 #pragma unroll
-    for (int s = 0; s < kAhead - 1; s++) fetch_y(s);
+    for (int s = 0; s < kAhead - 1; s++) fetch_y();
 
     pdl_wait();   // V is the previous kernel's; everything read so far is older
-    // fragments: lane (g, c) holds ranks 16 j + 4 c .. + 3 of rows g and g + 8
+    // fragments: lane (g, c) holds ranks 16 j + 4 c .. + 3 of rows g and g + 8 of a part
     const float scale = a.scales && rank ? __ldg(a.scales + tile.group) : 1.f;
-    for (int u = threadIdx.x; u < chunks * 32; u += kExpandWarps * 32) {
-        const int j = u >> 5, l = u & 31, r = 16 * j + 4 * (l & 3);
-        uint32_t part[3][4];
+    for (int u = threadIdx.x; u < parts * chunks * 32; u += kExpandWarps * 32) {
+        const int l = u & 31, j = (u >> 5) % chunks, part = (u >> 5) / chunks, r = 16 * j + 4 * (l & 3);
+        uint32_t piece[3][4];
 #pragma unroll
         for (int h = 0; h < 2; h++) {
-            const int m = (l >> 2) + 8 * h;
+            const int m = 16 * part + (l >> 2) + 8 * h;
             float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
             if (m < tile.rows && r < rank) {
                 const float *pv = a.v + int64_t(tile.pos + m) * a.max_rank + r;
                 s = __ldcg(reinterpret_cast<const float4 *>(pv));
+#pragma unroll 4
                 for (int z = 1; z < a.splits; z++) {
                     const float4 o = __ldcg(reinterpret_cast<const float4 *>(pv + int64_t(z) * a.t * a.max_rank));
                     s.x += o.x;
@@ -327,59 +336,77 @@ __global__ void __launch_bounds__(kExpandWarps * 32, C == 4 ? 3 : 4) k_lora_expa
             for (int i = 0; i < 4; i++) split3(v[i], p[i]);
 #pragma unroll
             for (int z = 0; z < 3; z++) {
-                part[z][h] = p[0][z] | p[1][z] << 16;          // K slots 2 c, 2 c + 1
-                part[z][2 + h] = p[2][z] | p[3][z] << 16;      // K slots 2 c + 8, 2 c + 9
+                piece[z][h] = p[0][z] | p[1][z] << 16;          // K slots 2 c, 2 c + 1
+                piece[z][2 + h] = p[2][z] | p[3][z] << 16;      // K slots 2 c + 8, 2 c + 9
             }
         }
 #pragma unroll
         for (int z = 0; z < 3; z++)
-            s_frag[(j * 3 + z) * 32 + l] = make_uint4(part[z][0], part[z][1], part[z][2], part[z][3]);
+            s_frag[((part * chunks + j) * 3 + z) * 32 + l] = make_uint4(piece[z][0], piece[z][1], piece[z][2], piece[z][3]);
     }
     __syncthreads();
 
+    int slot = 0;
+    // adds unit (n, part)'s y and stores it
+    auto finish = [&](const float (&d)[4][4], int64_t n, int part) {
+        fetch_y();
+        asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory");
+#pragma unroll
+        for (int h = 0; h < 2; h++) {
+            const int32_t r = s_row[16 * part + 8 * h + g];
+            if (r < 0) continue;
+            const float4 y0 = s_y[slot][2 * h][threadIdx.x], y1 = s_y[slot][2 * h + 1][threadIdx.x];
+            float *o = a.out + r * a.out_stride + n0 + n + 4 * c;
+            __stcs(reinterpret_cast<float4 *>(o), make_float4(y0.x + d[0][2 * h], y0.y + d[0][2 * h + 1], y0.z + d[1][2 * h],
+                                                              y0.w + d[1][2 * h + 1]));
+            __stcs(reinterpret_cast<float4 *>(o + 16), make_float4(y1.x + d[2][2 * h], y1.y + d[2][2 * h + 1],
+                                                                   y1.z + d[3][2 * h], y1.w + d[3][2 * h + 1]));
+        }
+        slot = slot + 1 == kAhead ? 0 : slot + 1;
+    };
     for (int s = 0; s < steps; s++) {
-        float d[4][4];
-#pragma unroll
-        for (int q = 0; q < 4; q++)
-#pragma unroll
-            for (int i = 0; i < 4; i++) d[q][i] = 0.f;
-        for (int j0 = 0; j0 < chunks; j0 += C) {
+        const int64_t n = int64_t(s) * 32;
+        if (chunks <= C) {
+            // all ranks' B in registers: it serves every part, and the next step's
+            // comes in meanwhile
             uint2 cur[C][4];
 #pragma unroll
             for (int j = 0; j < C; j++)
 #pragma unroll
                 for (int q = 0; q < 4; q++) cur[j][q] = w[j][q];
-            if (j0 + C < chunks) load_b(w, int64_t(s) * 32, j0 + C);
-            else if (s + 1 < steps) load_b(w, int64_t(s + 1) * 32, 0);
+            if (s + 1 < steps) load_b(w, n + 32, 0);
+            for (int part = 0; part < parts; part++) {
+                float d[4][4] = {};
 #pragma unroll
-            for (int j = 0; j < C; j++) {
-                if (j0 + j >= chunks) break;
-                // smallest part first
+                for (int j = 0; j < C; j++) {
+                    if (j >= chunks) break;
 #pragma unroll
-                for (int z = 2; z >= 0; z--) {
-                    const uint4 f = s_frag[((j0 + j) * 3 + z) * 32 + lane];
+                    for (int z = 2; z >= 0; z--) {     // smallest piece first
+                        const uint4 f = s_frag[((part * chunks + j) * 3 + z) * 32 + lane];
 #pragma unroll
-                    for (int q = 0; q < 4; q++) mma_16816(d[q], f.x, f.y, f.z, f.w, cur[j][q].x, cur[j][q].y);
+                        for (int q = 0; q < 4; q++) mma_16816(d[q], f.x, f.y, f.z, f.w, cur[j][q].x, cur[j][q].y);
+                    }
                 }
+                finish(d, n, part);
             }
-        }
-        // the slot of step s + kAhead - 1 was read in the step before this one
-        fetch_y(s + kAhead - 1);
-        asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory");
-        float4 cy[2][2];
+        } else {
+            for (int part = 0; part < parts; part++) {
+                float d[4][4] = {};
+                for (int j0 = 0; j0 < chunks; j0 += C) {
+                    load_b(w, n, j0);
 #pragma unroll
-        for (int h = 0; h < 2; h++) {
-            cy[h][0] = s_y[s % kAhead][2 * h][threadIdx.x];
-            cy[h][1] = s_y[s % kAhead][2 * h + 1][threadIdx.x];
-        }
+                    for (int j = 0; j < C; j++) {
+                        if (j0 + j >= chunks) break;
 #pragma unroll
-        for (int h = 0; h < 2; h++) {
-            if (!live[h]) continue;
-            float *o = po[h] + int64_t(s) * 32;
-            __stcs(reinterpret_cast<float4 *>(o), make_float4(cy[h][0].x + d[0][2 * h], cy[h][0].y + d[0][2 * h + 1],
-                                                              cy[h][0].z + d[1][2 * h], cy[h][0].w + d[1][2 * h + 1]));
-            __stcs(reinterpret_cast<float4 *>(o + 16), make_float4(cy[h][1].x + d[2][2 * h], cy[h][1].y + d[2][2 * h + 1],
-                                                                   cy[h][1].z + d[3][2 * h], cy[h][1].w + d[3][2 * h + 1]));
+                        for (int z = 2; z >= 0; z--) {
+                            const uint4 f = s_frag[((part * chunks + j0 + j) * 3 + z) * 32 + lane];
+#pragma unroll
+                            for (int q = 0; q < 4; q++) mma_16816(d[q], f.x, f.y, f.z, f.w, w[j][q].x, w[j][q].y);
+                        }
+                    }
+                }
+                finish(d, n, part);
+            }
         }
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
@@ -398,7 +425,7 @@ LoraGeometry lora_geometry(int64_t t, int64_t k, int groups, int max_rank) {
     // are many; single tokens would only repeat themselves in them
     g.token_tiles = t >= 16 * int64_t(groups) && t >= 64 ? 4 : 1;
     g.shrink_tiles = most_tiles(t, groups, 8 * g.token_tiles);
-    g.expand_tiles = most_tiles(t, groups + 1, kTileM);
+    g.expand_tiles = most_tiles(t, groups + 1, 16 * g.token_tiles);
     const int rt = (max_rank + 15) / 16;
     g.rank_tiles = g.token_tiles == 4 && rt > 1 ? 2 : 1;
     const int64_t parts = (rt + g.rank_tiles - 1) / g.rank_tiles;
@@ -444,20 +471,26 @@ cudaError_t launch_lora(const LoraLaunch &p, cudaStream_t stream) {
     cudaError_t err = cudaGetLastError();
     if (err != cudaSuccess) return err;
     // enough steps per warp that the fragments of V are worth their set-up,
-    // few enough that all SMs have work
+    // few enough that all SMs have work and no wave of CTAs is nearly empty
     const int64_t total = geo.expand_tiles * (p.n / 32);
-    a.steps = int(std::max<int64_t>(1, std::min<int64_t>(16, total / (148 * 16))));
+    a.steps = int(std::max<int64_t>(1, std::min<int64_t>(geo.token_tiles == 4 ? 4 : 16, total / (148 * 16))));
     const int64_t per_cta = int64_t(kExpandWarps) * a.steps * 32;
     const dim3 grid2(unsigned(geo.expand_tiles), unsigned((p.n + per_cta - 1) / per_cta));
-    const size_t smem = size_t(rt) * 3 * 32 * 16 + kExpandSmem;
+    const size_t smem = kExpandSmem + size_t(geo.token_tiles) * rt * 3 * 32 * 16;
     const dim3 block2(kExpandWarps * 32);
-    static std::atomic<uint64_t> allowed[3];
-#define UW_EXPAND(C_, I_)                                                              \
-    err = allow_smem(k_lora_expand<C_>, kExpandSmem + 16 * 3 * 32 * 16, allowed[I_]); \
-    if (err == cudaSuccess) err = launch_pdl(true, k_lora_expand<C_>, grid2, block2, smem, stream, a)
-    if (rt == 1) { UW_EXPAND(1, 0); }
-    else if (rt == 2) { UW_EXPAND(2, 1); }
-    else { UW_EXPAND(4, 2); }
+    static std::atomic<uint64_t> allowed[6];
+#define UW_EXPAND(C_, M_, I_)                                                                    \
+    err = allow_smem(k_lora_expand<C_, M_>, kExpandSmem + M_ * 16 * 3 * 32 * 16, allowed[I_]);  \
+    if (err == cudaSuccess) err = launch_pdl(true, k_lora_expand<C_, M_>, grid2, block2, smem, stream, a)
+    if (geo.token_tiles == 4) {
+        if (rt == 1) { UW_EXPAND(1, 4, 0); }
+        else if (rt == 2) { UW_EXPAND(2, 4, 1); }
+        else { UW_EXPAND(4, 4, 2); }
+    } else {
+        if (rt == 1) { UW_EXPAND(1, 1, 3); }
+        else if (rt == 2) { UW_EXPAND(2, 1, 4); }
+        else { UW_EXPAND(4, 1, 5); }
+    }
 #undef UW_EXPAND
     return err != cudaSuccess ? err : cudaGetLastError();
 }
