@@ -257,7 +257,8 @@ extern "C" uw_status uw_lora_add(const uint16_t *x_dev, int64_t x_stride, int64_
     if (!ws || ws_bytes < w.bytes || !aligned(ws, 256)) return UW_ERR_WORKSPACE;
     uint8_t *base = static_cast<uint8_t *>(ws);
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (ids_dev) {
+    const bool ungrouped = ids_dev && t <= kLoraUngrouped;
+    if (ids_dev && !ungrouped) {
         GroupLaunch g{};
         g.ids = ids_dev;
         g.rows = t;
@@ -283,6 +284,7 @@ extern "C" uw_status uw_lora_add(const uint16_t *x_dev, int64_t x_stride, int64_
     p.max_rank = d.max_rank;
     p.ranks = d.ranks_dev;
     p.scales = d.scales_dev;
+    p.ids = ungrouped ? ids_dev : nullptr;
     p.offsets = offsets_dev;
     p.order = order_dev;
     p.y = y_dev;

@@ -252,6 +252,7 @@ cudaError_t launch_route(const RouteLaunch &p, cudaStream_t stream);
 
 // Low-rank adapters beside a projection (lora.cu): out = y + scale * B (A x)
 // per row of an adapter's group.  v: [splits][t][max_rank] floats.
+constexpr int64_t kLoraUngrouped = 32;   // up to so many rows a warp groups for itself
 struct LoraGeometry {
     int splits = 1;            // slices of K
     int token_tiles = 1;       // 8-token tiles of the first product's tile: 1 or 4
@@ -267,7 +268,8 @@ struct LoraLaunch {
     int groups, max_rank;
     const int32_t *ranks;      // may be null
     const float *scales;       // may be null
-    const int32_t *offsets, *order;
+    const int32_t *ids;        // t <= kLoraUngrouped: rows' adapters; else null
+    const int32_t *offsets, *order;   // with ids null: the rows' grouping
     const float *y;
     int64_t y_stride;
     float *out;

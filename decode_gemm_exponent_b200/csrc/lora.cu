@@ -51,6 +51,7 @@ struct LoraArgs {
     int groups, max_rank;
     const int32_t *ranks;
     const float *scales;
+    const int32_t *ids;        // t <= 32 and not grouped: each row's adapter
     const int32_t *offsets, *order;
     float *v;
     int splits;
@@ -68,11 +69,47 @@ struct Tile {
     int rows;
 };
 
-// The tile-th tile of at most `size` rows, found by one warp from the groups'
-// offsets (clamped to [0, t], so that no offsets lead out of bounds).
-__device__ __forceinline__ Tile find_tile(const LoraArgs &a, int size, int64_t tile, bool rest) {
+// The tile-th tile of at most `size` rows, found by one warp; rows[0..size)
+// receives its rows (-1 behind the last).  Grouped rows: from the groups' offsets
+// (clamped to [0, t], so that no offsets lead out of bounds).  Up to 32 rows with
+// their ids: the warp groups them itself, in the order of first occurrence.
+__device__ __forceinline__ Tile find_tile(const LoraArgs &a, int size, int64_t tile, bool rest, int32_t *rows) {
     const int lane = threadIdx.x & 31;
     const int t = int(a.t);
+    auto scan = [&](int v) {
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int u = __shfl_up_sync(kAll, v, d);
+            if (lane >= d) v += u;
+        }
+        return v;
+    };
+    if (a.ids) {
+        int id = -1 - lane;                     // lanes without a row: alone
+        if (lane < t) {
+            id = __ldg(a.ids + lane);
+            if (uint32_t(id) >= uint32_t(a.groups)) id = a.groups;
+        }
+        const uint32_t same = __match_any_sync(kAll, id);
+        const int cnt = lane < t && lane == __ffs(same) - 1 ? __popc(same) : 0;
+        const int pos = scan(cnt) - cnt;        // the same whether or not the rest has tiles
+        const int tiles = rest || id < a.groups ? (cnt + size - 1) / size : 0;
+        const int incl = scan(tiles);
+        const uint32_t hit = __ballot_sync(kAll, incl > tile);
+        if (!hit) return Tile{-1, 0, 0};
+        const int src = __ffs(hit) - 1;
+        const int skip = (int(tile) - (__shfl_sync(kAll, incl, src) - __shfl_sync(kAll, tiles, src))) * size;
+        Tile r;
+        r.group = __shfl_sync(kAll, id, src);
+        r.pos = __shfl_sync(kAll, pos, src) + skip;
+        r.rows = min(size, __shfl_sync(kAll, cnt, src) - skip);
+        for (int i = lane; i < size; i += 32) rows[i] = -1;
+        __syncwarp();
+        const int at = __popc(same & ((1u << lane) - 1u)) - skip;
+        if (__shfl_sync(kAll, same, src) >> lane & 1u)
+            if (at >= 0 && at < size) rows[at] = lane;
+        return r;
+    }
     int64_t run = 0;
     for (int g0 = 0; g0 <= a.groups; g0 += 32) {
         const int g = g0 + lane;
@@ -83,20 +120,19 @@ __device__ __forceinline__ Tile find_tile(const LoraArgs &a, int size, int64_t t
             cnt = max(hi - lo, 0);
         }
         const int tiles = (cnt + size - 1) / size;
-        int incl = tiles;
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            const int u = __shfl_up_sync(kAll, incl, d);
-            if (lane >= d) incl += u;
-        }
+        const int incl = scan(tiles);
         const int total = __shfl_sync(kAll, incl, 31);
         if (tile < run + total) {
             const int src = __ffs(__ballot_sync(kAll, run + incl > tile)) - 1;
             Tile r;
-            const int skip = int(tile - run) - (__shfl_sync(kAll, incl, src) - __shfl_sync(kAll, tiles, src));
+            const int skip = (int(tile - run) - (__shfl_sync(kAll, incl, src) - __shfl_sync(kAll, tiles, src))) * size;
             r.group = g0 + src;
-            r.pos = __shfl_sync(kAll, lo, src) + skip * size;
-            r.rows = min(size, __shfl_sync(kAll, cnt, src) - skip * size);
+            r.pos = __shfl_sync(kAll, lo, src) + skip;
+            r.rows = min(size, __shfl_sync(kAll, cnt, src) - skip);
+            for (int i = lane; i < size; i += 32) {
+                const int32_t row = i < r.rows ? __ldg(a.order + r.pos + i) : -1;
+                rows[i] = uint32_t(row) < uint32_t(t) ? row : -1;
+            }
             return r;
         }
         run += total;
@@ -115,11 +151,12 @@ __device__ __forceinline__ int rank_of(const LoraArgs &a, int group) {
 template <int RT, int NT>
 __global__ void __launch_bounds__(kShrinkWarps * 32, 2) k_lora_shrink(const LoraArgs a) {
     __shared__ Tile s_tile;
+    __shared__ int32_t s_row[8 * NT];
     __shared__ float red[kShrinkWarps][RT * NT * 4][32];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
     pdl_trigger();
     if (warp == 0) {
-        const Tile f = find_tile(a, 8 * NT, blockIdx.x, false);
+        const Tile f = find_tile(a, 8 * NT, blockIdx.x, false, s_row);
         if (lane == 0) s_tile = f;
     }
     __syncthreads();
@@ -143,7 +180,8 @@ __global__ void __launch_bounds__(kShrinkWarps * 32, 2) k_lora_shrink(const Lora
         }
 #pragma unroll
     for (int i = 0; i < NT; i++) {
-        const int row = min(max(__ldg(a.order + tile.pos + min(8 * i + g, tile.rows - 1)), 0), int(a.t) - 1);
+        // (columns behind the tile's last row repeat it; their results are not stored)
+        const int64_t row = max(s_row[min(8 * i + g, tile.rows - 1)], 0);
         px[i] = a.x + row * a.x_stride + k0 * 64 + 16 * c;
     }
     float d[RT][NT][4];
@@ -236,13 +274,8 @@ __global__ void __launch_bounds__(kExpandWarps * 32, C == 4 ? 3 : 4) k_lora_expa
     uint4 *s_frag = s_dyn + kAhead * 4 * kExpandWarps * 32;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
     if (warp == 0) {
-        const Tile f = find_tile(a, 16 * MT, blockIdx.x, a.copy_rest != 0);
+        const Tile f = find_tile(a, 16 * MT, blockIdx.x, a.copy_rest != 0, s_row);
         if (lane == 0) s_tile = f;
-        if (f.group >= 0)
-            for (int i = lane; i < 16 * MT; i += 32) {
-                const int32_t r = i < f.rows ? __ldg(a.order + f.pos + i) : -1;
-                s_row[i] = uint32_t(r) < uint32_t(a.t) ? r : -1;
-            }
     }
     __syncthreads();
     const Tile tile = s_tile;
@@ -453,6 +486,7 @@ cudaError_t launch_lora(const LoraLaunch &p, cudaStream_t stream) {
     a.max_rank = p.max_rank;
     a.ranks = p.ranks;
     a.scales = p.scales;
+    a.ids = p.ids;
     a.offsets = p.offsets;
     a.order = p.order;
     a.v = p.v;

@@ -415,8 +415,10 @@ __global__ void __launch_bounds__(route_threads<NV>()) k_route(const RouteArgs a
     }
 }
 
-// ranking warps for `groups` groups, at most `most`
-int rank_warps(int groups, int most) { return std::max(1, std::min(most, kGroupCells / (groups + 1))); }
+// ranking warps for `groups` groups and `items` items per block, at most `most`
+int rank_warps(int groups, int64_t items, int most) {
+    return int(std::max<int64_t>(1, std::min<int64_t>(std::min(most, kGroupCells / (groups + 1)), (items + 31) / 32)));
+}
 
 size_t group_smem(int groups, int warps) { return size_t(warps + 2) * size_t(groups + 1) * 4; }
 
@@ -424,9 +426,10 @@ size_t group_smem(int groups, int warps) { return size_t(warps + 2) * size_t(gro
 
 GroupGeometry group_geometry(int64_t rows, int per_row, int groups) {
     GroupGeometry g;
-    // One block takes what its 32 warps rank in a few steps; beyond that one
-    // block per SM, so that the sum over blocks stays short.
-    if (rows * per_row <= 2048) {
+    // One block takes what its 32 warps rank in a few steps (4096 items: 5 us in
+    // one block, 8 us in two launches); beyond that one block per SM, so that
+    // the sum over blocks stays short.
+    if (rows * per_row <= 8192) {
         g.blocks = 1;
         g.rows_per_block = std::max<int64_t>(rows, 1);
         g.bytes = 0;
@@ -445,7 +448,7 @@ GroupGeometry group_geometry(int64_t rows, int per_row, int groups) {
 // one block are quicker than a second launch; more are not.
 GroupGeometry route_geometry(int64_t t, int top_k, int experts) {
     GroupGeometry g = group_geometry(t, top_k, experts);
-    if (t <= 64 && t * top_k <= 2048) return g;
+    if (t <= 64) return g;
     const int64_t most = 148;
     g.rows_per_block = std::max<int64_t>((t + most - 1) / most, 32);
     g.blocks = int((t + g.rows_per_block - 1) / g.rows_per_block);
@@ -465,7 +468,7 @@ cudaError_t launch_group_rows(const GroupLaunch &p, cudaStream_t stream) {
     a.order = p.order;
     a.slot = p.slot;
     const int threads = 1024;
-    a.warps = rank_warps(p.groups, 32);
+    a.warps = rank_warps(p.groups, a.per_block, 32);
     const size_t smem = group_smem(p.groups, a.warps);
     if (geo.bytes) {
         int32_t *counts = static_cast<int32_t *>(p.ws);
@@ -513,7 +516,7 @@ cudaError_t launch_route(const RouteLaunch &p, cudaStream_t stream) {
     g.order = p.order;
     g.slot = p.slot;
     a.counts = geo.bytes ? static_cast<int32_t *>(p.ws) : nullptr;
-    g.warps = rank_warps(r.experts, threads / 32);
+    g.warps = rank_warps(r.experts, g.per_block, threads / 32);
     const size_t smem = geo.bytes ? size_t(r.experts + 1) * 4 : group_smem(r.experts, g.warps);
     // 64-bit keys where the selection compares computed scores
     const bool wide = p.bias != nullptr || (r.n_groups > 1 && a.top2);
@@ -535,7 +538,7 @@ cudaError_t launch_route(const RouteLaunch &p, cudaStream_t stream) {
     cudaError_t err = cudaGetLastError();
     if (err != cudaSuccess || !geo.bytes) return err;
     g.counts = a.counts;
-    g.warps = rank_warps(r.experts, 32);
+    g.warps = rank_warps(r.experts, g.per_block, 32);
     err = launch_pdl(true, k_group, grid, dim3(1024), group_smem(r.experts, g.warps), stream, g);
     return err != cudaSuccess ? err : cudaGetLastError();
 }
