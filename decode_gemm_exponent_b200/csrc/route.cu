@@ -17,9 +17,12 @@
 // routes nowhere.  +inf counts as the largest finite float.
 //
 // Exactness of the selection.  Logits compare exactly.  Choices with a bias
-// and sums of two scores are compared in 64 bits: two experts a few units of
+// and sums of two scores are defined in 64 bits: two experts a few units of
 // 2^-24 apart are common at thousands of tokens times hundreds of experts, and
-// a 32-bit sigmoid would order them by its own rounding.
+// a 32-bit sigmoid would order them by its own rounding.  A row is compared in
+// 32 bits first; where two neighbours of the order, or the last one chosen and
+// the first one left out, are nearer than the error bound, it is compared again
+// in 64 bits.
 //
 // One warp per token; lane l holds experts l, l + 32, ...  A value is kept as
 // an unsigned key of the same order (0 = not there), so a selection step is a
@@ -49,6 +52,7 @@ using namespace dev;
 constexpr uint32_t kAll = 0xFFFFFFFFu;
 constexpr float kMaxFloat = 3.402823466e38f;
 constexpr int kGroupCells = 10240;      // 40 KB of per-warp counters
+constexpr size_t kRouteSmem = 160 * 1024;   // 16 warps x 1024 experts x 8 bytes, and the counts
 
 struct GroupArgs {
     const int32_t *ids;     // [items]; outside [0, groups): no group
@@ -72,6 +76,7 @@ struct RouteArgs {
     float *weights;
     int64_t rows_per_block;
     int32_t *counts;        // [blocks][experts + 1]; null: one block, which also orders
+    int scratch_at, scratch_words;   // per-warp keys in shared memory (with groups): words before, words each
     GroupArgs group;
 };
 
@@ -108,12 +113,20 @@ __device__ __forceinline__ void order_block(const GroupArgs &a, int64_t block, i
     __syncthreads();
     int32_t *mine = cell + warp * g1;
     if (warp < a.warps) {
-        for (int64_t i0 = w0; i0 < w1; i0 += 32) {
-            const bool live = i0 + lane < w1;
-            const int key = live ? group_of(a.ids[begin + i0 + lane], a.groups) : -1;
-            const uint32_t same = __match_any_sync(kAll, key);
-            if (live && lane == __ffs(same) - 1) mine[key] += __popc(same);
-            __syncwarp();
+        for (int64_t j0 = w0; j0 < w1; j0 += 128) {
+            int key[4];                      // four loads at a time
+#pragma unroll
+            for (int q = 0; q < 4; q++) {
+                const int64_t i = j0 + 32 * q + lane;
+                key[q] = i < w1 ? group_of(a.ids[begin + i], a.groups) : -1;
+            }
+#pragma unroll
+            for (int q = 0; q < 4; q++) {
+                if (j0 + 32 * q >= w1) break;
+                const uint32_t same = __match_any_sync(kAll, key[q]);
+                if (key[q] >= 0 && lane == __ffs(same) - 1) mine[key[q]] += __popc(same);
+                __syncwarp();
+            }
         }
     }
     __syncthreads();
@@ -173,20 +186,28 @@ __device__ __forceinline__ void order_block(const GroupArgs &a, int64_t block, i
     }
     __syncthreads();
     if (warp < a.warps) {
-        for (int64_t i0 = w0; i0 < w1; i0 += 32) {
-            const bool live = i0 + lane < w1;
-            const int64_t item = begin + i0 + lane;
-            const int key = live ? group_of(a.ids[item], a.groups) : -1;
-            const uint32_t same = __match_any_sync(kAll, key);
-            int32_t pos = 0;
-            if (live) pos = mine[key] + __popc(same & ((1u << lane) - 1u));
-            __syncwarp();
-            if (live) {
-                if (lane == __ffs(same) - 1) mine[key] += __popc(same);
-                a.order[pos] = int32_t(item);
-                if (a.slot) a.slot[item] = key < a.groups ? pos : -1;
+        for (int64_t j0 = w0; j0 < w1; j0 += 128) {
+            int key[4];
+#pragma unroll
+            for (int q = 0; q < 4; q++) {
+                const int64_t i = j0 + 32 * q + lane;
+                key[q] = i < w1 ? group_of(a.ids[begin + i], a.groups) : -1;
             }
-            __syncwarp();
+#pragma unroll
+            for (int q = 0; q < 4; q++) {
+                if (j0 + 32 * q >= w1) break;
+                const int64_t item = begin + j0 + 32 * q + lane;
+                const uint32_t same = __match_any_sync(kAll, key[q]);
+                int32_t pos = 0;
+                if (key[q] >= 0) pos = mine[key[q]] + __popc(same & ((1u << lane) - 1u));
+                __syncwarp();
+                if (key[q] >= 0) {
+                    if (lane == __ffs(same) - 1) mine[key[q]] += __popc(same);
+                    a.order[pos] = int32_t(item);
+                    if (a.slot) a.slot[item] = key[q] < a.groups ? pos : -1;
+                }
+                __syncwarp();
+            }
         }
     }
 }
@@ -256,11 +277,36 @@ __device__ __forceinline__ double score_of(const RouteArgs &a, float l, float m,
     return a.softmax ? exp(double(l) - double(m)) / sum : 1.0 / (1.0 + exp(-double(l)));
 }
 
-// NV: experts per lane; Key: uint32_t compares logits, uint64_t choices in 64 bits
-template <int NV, class Key>
-__device__ __forceinline__ void route_row(const RouteArgs &a, int64_t row, int32_t *count) {
+// How a row's choices are compared.
+enum Mode {
+    kLogits,      // the logits themselves, 32-bit keys: exact
+    kFast,        // choices in 32 bits, given up where two are within the error bound
+    kExact        // choices in 64 bits
+};
+template <int MODE> struct KeyOf { using type = uint32_t; };
+template <> struct KeyOf<kExact> { using type = uint64_t; };
+
+// kFast: s_e in 32 bits.  Error, absolute, u = 2^-24.  Sigmoid: expf is within 2
+// units of 2 u, so s moves by s (1 - s) 4 u at most; the sum and the reciprocal
+// round once each: below 4 u.  Softmax, with d = max - l: d rounds to d u, d
+// exp(-d) < 0.4; the sum's terms err alike, by their mean d (at most ln 1024),
+// and add up in at most 37 roundings: below 64 u.
+__device__ __forceinline__ float fast_score(const RouteArgs &a, float l, float m, float inv_sum) {
+    return a.softmax ? expf(l - m) * inv_sum : __frcp_rn(1.f + expf(-l));
+}
+__device__ __forceinline__ float score_error(const RouteArgs &a) { return (a.softmax ? 64.f : 4.f) * 0x1p-24f; }
+
+__device__ __forceinline__ float value_of(uint32_t key) { return __uint_as_float(key & 0x80000000u ? key & 0x7FFFFFFFu : ~key); }
+
+// Routes one row; NV: experts per lane; group: the groups of the lane's experts, a
+// byte each; warp_scratch: a key per expert (with groups only).  False (kFast only):
+// nothing written, the row has to be compared exactly.
+template <int NV, int MODE>
+__device__ __forceinline__ bool route_row(const RouteArgs &a, int64_t row, int32_t *count,
+                                          const uint32_t (&group)[(NV + 3) / 4], void *warp_scratch) {
+    using Key = typename KeyOf<MODE>::type;
     const int lane = threadIdx.x & 31;
-    constexpr bool kWide = sizeof(Key) == 8;
+    Key *scratch = static_cast<Key *>(warp_scratch);
     float l[NV];
     float m = -INFINITY;
 #pragma unroll
@@ -272,22 +318,24 @@ __device__ __forceinline__ void route_row(const RouteArgs &a, int64_t row, int32
         m = fmaxf(m, v);
     }
     double sum = 1.0;
+    float inv_sum = 1.f;
     if (a.softmax) {
 #pragma unroll
         for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(kAll, m, d));
-        if (kWide) {
+        if (MODE == kExact) {
             double s = 0.0;
 #pragma unroll
             for (int i = 0; i < NV; i++)
                 if (l[i] >= -kMaxFloat) s += exp(double(l[i]) - double(m));
             sum = warp_sum(s);
         } else {
-            // the sum only scales the weights here: 32 bits, all terms positive
             float s = 0.f;
 #pragma unroll
             for (int i = 0; i < NV; i++)
                 if (l[i] >= -kMaxFloat) s += expf(l[i] - m);
-            sum = double(warp_sum(s));
+            s = warp_sum(s);
+            sum = double(s);
+            inv_sum = __frcp_rn(s);
         }
     }
     Key key[NV];
@@ -295,109 +343,166 @@ __device__ __forceinline__ void route_row(const RouteArgs &a, int64_t row, int32
     for (int i = 0; i < NV; i++) {
         key[i] = 0;
         if (l[i] >= -kMaxFloat) {
-            if constexpr (kWide) {
-                if (a.bias) {
-                    const double c = score_of(a, l[i], m, sum) + double(__ldg(a.bias + 32 * i + lane));
-                    key[i] = c > -INFINITY ? key_of(c) : 0;   // a bias of -inf or NaN: never chosen
-                } else {
-                    key[i] = key_of(double(l[i]));
-                }
+            if (MODE == kLogits || !a.bias) {
+                if constexpr (MODE == kExact) key[i] = key_of(double(l[i]));
+                else key[i] = key_of(l[i]);
             } else {
-                key[i] = key_of(l[i]);
+                const float bias = __ldg(a.bias + 32 * i + lane);      // -inf or NaN: never chosen
+                if constexpr (MODE == kExact) {
+                    const double c = score_of(a, l[i], m, sum) + double(bias);
+                    key[i] = c > -INFINITY ? key_of(c) : 0;
+                } else {
+                    const float c = fast_score(a, l[i], m, inv_sum) + bias;
+                    key[i] = c > -INFINITY ? key_of(c) : 0;
+                }
             }
         }
     }
+    const float eps = score_error(a);
+    bool unsure = false;
 
     if (a.n_groups > 1) {
-        // lane g keeps group g's value as a key of its own order
-        uint64_t value = 0;
-        for (int g = 0; g < a.n_groups; g++) {
-            const int lo = g * a.group_size, hi = lo + a.group_size;
-            Key best = 0;
-            int at = 0;
+        // The keys go through shared memory, so that P neighbouring lanes take one
+        // group each (P = 32 / n_groups, a power of two): the two largest of a
+        // group are a short scan and log2(P) exchanges, for all groups at once.
+        int P = 1;
+        while (2 * P * a.n_groups <= 32) P *= 2;
+        const int g = lane / P;
+        __syncwarp();
 #pragma unroll
-            for (int i = 0; i < NV; i++) {
-                if (32 * i + 31 < lo || 32 * i >= hi) continue;
-                const int e = 32 * i + lane;
-                if (e >= lo && e < hi && key[i] > best) {
-                    best = key[i];
-                    at = e;
-                }
+        for (int i = 0; i < NV; i++)
+            if (32 * i + lane < a.experts) scratch[32 * i + lane] = key[i];
+        __syncwarp();
+        Key first = 0, second = 0;
+        if (g < a.n_groups) {
+            const Key *mine = scratch + g * a.group_size;
+            for (int j = lane % P; j < a.group_size; j += P) {
+                const Key k = mine[j];
+                second = max(second, min(first, k));
+                first = max(first, k);
             }
-            const Key first = warp_max(best);
-            uint64_t v = uint64_t(first);
-            if (kWide && a.top2 && first != 0) {
-                // the second largest: the first's lowest place left out
-                const int where = __reduce_min_sync(kAll, best == first ? at : 0x7FFFFFFF);
-                Key next = 0;
-#pragma unroll
-                for (int i = 0; i < NV; i++) {
-                    if (32 * i + 31 < lo || 32 * i >= hi) continue;
-                    const int e = 32 * i + lane;
-                    if (e >= lo && e < hi && e != where && key[i] > next) next = key[i];
-                }
-                const Key second = warp_max(next);
-                double s;
-                if (a.bias) {
-                    s = value_of(uint64_t(first)) + (second ? value_of(uint64_t(second)) : 0.0);
-                } else {
-                    // the keys are logits: the two scores are summed
-                    s = score_of(a, float(value_of(uint64_t(first))), m, sum) +
-                        (second ? score_of(a, float(value_of(uint64_t(second))), m, sum) : 0.0);
-                }
-                v = key_of(s);
-            }
-            if (lane == g) value = v;
         }
-        uint32_t keep = 0;
+        for (int d = 1; d < P; d *= 2) {
+            const Key f = __shfl_xor_sync(kAll, first, d), n = __shfl_xor_sync(kAll, second, d);
+            second = max(max(second, n), min(first, f));
+            first = max(first, f);
+        }
+        Key value = first;
+        float size = 0.f;                  // kFast: what the value's error scales with
+        if (first != 0) {
+            if (MODE == kFast) size = fabsf(float(value_of(first)));
+            if (MODE != kLogits && a.top2) {
+                // without a bias the keys are logits, and their scores are summed
+                if constexpr (MODE == kExact) {
+                    double u = value_of(first), v = second ? value_of(second) : 0.0;
+                    if (!a.bias) {
+                        u = score_of(a, float(u), m, sum);
+                        v = second ? score_of(a, float(v), m, sum) : 0.0;
+                    }
+                    value = key_of(u + v);
+                } else {
+                    float u = value_of(uint32_t(first)), v = second ? value_of(uint32_t(second)) : 0.f;
+                    if (!a.bias) {
+                        u = fast_score(a, u, m, inv_sum);
+                        v = second ? fast_score(a, v, m, inv_sum) : 0.f;
+                    }
+                    value = key_of(u + v);
+                    size = fabsf(u) + fabsf(v);
+                }
+            }
+        }
+        if (lane % P) value = 0;           // one lane per group
+        uint32_t keep = 0;                 // its lanes
+        Key last = 0;
         for (int j = 0; j < a.top_groups; j++) {
-            const uint64_t live = (keep >> lane) & 1u ? 0 : value;
-            const uint64_t best = warp_max(live);
-            if (best == 0) break;    // groups that are left hold nothing to choose
+            const Key live = (keep >> lane) & 1u ? 0 : value;
+            const Key best = warp_max(live);
+            if (best == 0) break;          // groups that are left hold nothing to choose
+            last = best;
             keep |= 1u << (__ffs(__ballot_sync(kAll, live == best)) - 1);
         }
-#pragma unroll
-        for (int i = 0; i < NV; i++) {
-            const int e = 32 * i + lane;
-            if (e < a.experts && !((keep >> (e / a.group_size)) & 1u)) key[i] = 0;
+        if (MODE == kFast) {
+            // each value is off by two scores' errors and three roundings at most
+            const uint32_t next = __reduce_max_sync(kAll, (keep >> lane) & 1u ? 0u : uint32_t(value));
+            const float scale = __uint_as_float(__reduce_max_sync(kAll, __float_as_uint(size)));
+            if (last != 0 && next != 0)
+                unsure = !(value_of(uint32_t(last)) - value_of(next) > 4.f * eps + 0x1p-21f * scale);
         }
+#pragma unroll
+        for (int i = 0; i < NV; i++)
+            if (!((keep >> (P * ((group[i / 4] >> (8 * (i % 4))) & 255u))) & 1u)) key[i] = 0;
     }
+    if (MODE == kFast && unsure) return false;
 
-    int32_t my_id = -1;
-    for (int s = 0; s < a.top_k; s++) {
+    // kFast with a bias looks one place further, at what it leaves out
+    const int places = a.top_k + (MODE == kFast && a.bias ? 1 : 0);
+    int32_t my_id = -1, beyond = -1;          // slot s is lane s's; `beyond`: place 32
+    Key my_key = 0, beyond_key = 0;
+    int win = -1;
+    for (int s = 0; s < places; s++) {
         Key best = 0;
         int at = 0;
 #pragma unroll
-        for (int i = 0; i < NV; i++)
+        for (int i = 0; i < NV; i++) {
+            if (win == 32 * i + lane) key[i] = 0;      // the last one chosen
             if (key[i] > best) {
                 best = key[i];
                 at = 32 * i + lane;
             }
+        }
         const Key top = warp_max(best);
         if (top == 0) break;
-        const int win = __reduce_min_sync(kAll, best == top ? at : 0x7FFFFFFF);
-        if (lane == s) my_id = win;
-#pragma unroll
-        for (int i = 0; i < NV; i++)
-            if (win == 32 * i + lane) key[i] = 0;
+        win = __reduce_min_sync(kAll, best == top ? at : 0x7FFFFFFF);
+        if (lane == s) {
+            my_id = win;
+            my_key = top;
+        }
+        if (s == 32) {
+            beyond = win;
+            beyond_key = top;
+        }
     }
-    // slot s is lane s's
+    const float my_logit = my_id >= 0 ? fminf(load_logit(a, row, my_id), kMaxFloat) : 0.f;
+    if (MODE == kFast && a.bias) {
+        // neighbours further apart than both errors are in order; so are equal
+        // ones with the same logit and bias, inside the chosen (lowest index first)
+        const float c = my_id >= 0 ? value_of(uint32_t(my_key)) : 0.f;
+        const float b = my_id >= 0 ? __ldg(a.bias + my_id) : 0.f;
+        const float c0 = __shfl_up_sync(kAll, c, 1), b0 = __shfl_up_sync(kAll, b, 1);
+        const float l0 = __shfl_up_sync(kAll, my_logit, 1);
+        const float margin = 2.f * eps + 0x1p-22f * fmaxf(fabsf(c), fabsf(c0));
+        bool bad = lane > 0 && my_id >= 0 && !(c0 - c > margin) && !(lane < a.top_k && b == b0 && my_logit == l0);
+        if (lane == 31 && beyond >= 0) {
+            const float cb = value_of(uint32_t(beyond_key));
+            bad |= !(c - cb > 2.f * eps + 0x1p-22f * fmaxf(fabsf(c), fabsf(cb)));
+        }
+        if (__any_sync(kAll, bad)) return false;
+        if (lane >= a.top_k) my_id = -1;
+    }
     double w = 0.0;
-    if (my_id >= 0) w = score_of(a, fminf(load_logit(a, row, my_id), kMaxFloat), m, sum);
+    if (my_id >= 0) w = score_of(a, my_logit, m, sum);
     if (a.renorm) w = w / (warp_sum(w) + 1e-20);
     if (lane < a.top_k) {
         a.ids[row * a.top_k + lane] = my_id;
         a.weights[row * a.top_k + lane] = float(w * double(a.scale));
         if (count) atomicAdd(&count[my_id < 0 ? a.experts : my_id], 1);
     }
+    return true;
+}
+
+// the rare rows of kFast, out of its way (its 64-bit keys take the registers)
+template <int NV>
+__device__ __noinline__ void route_row_exact(const RouteArgs &a, int64_t row, int32_t *count,
+                                             const uint32_t (&group)[(NV + 3) / 4], void *scratch) {
+    route_row<NV, kExact>(a, row, count, group, scratch);
 }
 
 template <int NV>
 constexpr int route_threads() { return NV <= 8 ? 1024 : 512; }
 
-template <int NV, class Key>
-__global__ void __launch_bounds__(route_threads<NV>()) k_route(const RouteArgs a) {
-    const int warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+template <int NV, int MODE>
+__global__ void __launch_bounds__(route_threads<NV>()) k_route(const __grid_constant__ RouteArgs a) {
+    const int warp = threadIdx.x >> 5, warps = blockDim.x >> 5, lane = threadIdx.x & 31;
     const int64_t begin = blockIdx.x * a.rows_per_block, end = min(a.t, begin + a.rows_per_block);
     int32_t *count = a.counts ? smem_route : nullptr;
     pdl_trigger();
@@ -405,7 +510,14 @@ __global__ void __launch_bounds__(route_threads<NV>()) k_route(const RouteArgs a
         for (int i = threadIdx.x; i <= a.experts; i += blockDim.x) count[i] = 0;
         __syncthreads();
     }
-    for (int64_t row = begin + warp; row < end; row += warps) route_row<NV, Key>(a, row, count);
+    uint32_t group[(NV + 3) / 4] = {};
+    if (a.n_groups > 1) {
+#pragma unroll
+        for (int i = 0; i < NV; i++) group[i / 4] |= (min(32 * i + lane, a.experts - 1) / a.group_size) << (8 * (i % 4));
+    }
+    void *scratch = smem_route + a.scratch_at + warp * a.scratch_words;
+    for (int64_t row = begin + warp; row < end; row += warps)
+        if (!route_row<NV, MODE>(a, row, count, group, scratch)) route_row_exact<NV>(a, row, count, group, scratch);
     __syncthreads();
     if (count) {
         for (int i = threadIdx.x; i <= a.experts; i += blockDim.x)
@@ -517,25 +629,39 @@ cudaError_t launch_route(const RouteLaunch &p, cudaStream_t stream) {
     g.slot = p.slot;
     a.counts = geo.bytes ? static_cast<int32_t *>(p.ws) : nullptr;
     g.warps = rank_warps(r.experts, g.per_block, threads / 32);
-    const size_t smem = geo.bytes ? size_t(r.experts + 1) * 4 : group_smem(r.experts, g.warps);
-    // 64-bit keys where the selection compares computed scores
-    const bool wide = p.bias != nullptr || (r.n_groups > 1 && a.top2);
+    // counts (or the ordering, which starts when the routing is done), and with
+    // groups a key of up to 8 bytes per expert and warp
+    a.scratch_at = geo.bytes ? (r.experts + 2) / 2 * 2 : 0;
+    a.scratch_words = r.n_groups > 1 ? 2 * r.experts : 0;
+    const size_t route_smem = size_t(a.scratch_at + threads / 32 * a.scratch_words) * 4;
+    const size_t smem = geo.bytes ? std::max(route_smem, size_t(r.experts + 1) * 4)
+                                  : std::max(route_smem, group_smem(r.experts, g.warps));
+    cudaError_t err = cudaSuccess;
+    // whether the selection compares computed scores
+    const bool computed = p.bias != nullptr || (r.n_groups > 1 && a.top2);
     const dim3 grid(static_cast<unsigned>(geo.blocks)), block(static_cast<unsigned>(threads));
-#define UW_ROUTE(NV_)                                                    \
-    case NV_:                                                            \
-        if (wide) k_route<NV_, uint64_t><<<grid, block, smem, stream>>>(a); \
-        else k_route<NV_, uint32_t><<<grid, block, smem, stream>>>(a);   \
+    static std::atomic<uint64_t> allowed[12];
+#define UW_ROUTE_ONE(NV_, MODE_, I_)                                                            \
+    {                                                                                          \
+        if (smem > 48 * 1024) err = allow_smem(k_route<NV_, MODE_>, kRouteSmem, allowed[I_]);  \
+        if (err == cudaSuccess) k_route<NV_, MODE_><<<grid, block, smem, stream>>>(a);         \
+    }
+#define UW_ROUTE(NV_, I_)                              \
+    case NV_:                                          \
+        if (computed) UW_ROUTE_ONE(NV_, kFast, I_)     \
+        else UW_ROUTE_ONE(NV_, kLogits, I_ + 6)        \
         break;
     switch (nv) {
-        UW_ROUTE(1)
-        UW_ROUTE(2)
-        UW_ROUTE(4)
-        UW_ROUTE(8)
-        UW_ROUTE(16)
-        UW_ROUTE(32)
+        UW_ROUTE(1, 0)
+        UW_ROUTE(2, 1)
+        UW_ROUTE(4, 2)
+        UW_ROUTE(8, 3)
+        UW_ROUTE(16, 4)
+        UW_ROUTE(32, 5)
     }
 #undef UW_ROUTE
-    cudaError_t err = cudaGetLastError();
+#undef UW_ROUTE_ONE
+    if (err == cudaSuccess) err = cudaGetLastError();
     if (err != cudaSuccess || !geo.bytes) return err;
     g.counts = a.counts;
     g.warps = rank_warps(r.experts, g.per_block, 32);
