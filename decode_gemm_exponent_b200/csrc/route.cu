@@ -328,6 +328,7 @@ __device__ __forceinline__ bool route_row(const RouteArgs &a, int64_t row, int32
             for (int i = 0; i < NV; i++)
                 if (l[i] >= -kMaxFloat) s += exp(double(l[i]) - double(m));
             sum = warp_sum(s);
+            inv_sum = float(1.0 / sum);
         } else {
             float s = 0.f;
 #pragma unroll
@@ -360,6 +361,15 @@ __device__ __forceinline__ bool route_row(const RouteArgs &a, int64_t row, int32
     }
     const float eps = score_error(a);
     bool unsure = false;
+    // the sum in 64 bits, for the rows that need it
+    auto row_sum = [&]() -> double {
+        if (!a.softmax || MODE == kExact) return sum;
+        double s = 0.0;
+#pragma unroll
+        for (int i = 0; i < NV; i++)
+            if (l[i] >= -kMaxFloat) s += exp(double(l[i]) - double(m));
+        return warp_sum(s);
+    };
 
     if (a.n_groups > 1) {
         // The keys go through shared memory, so that P neighbouring lanes take one
@@ -422,11 +432,11 @@ __device__ __forceinline__ bool route_row(const RouteArgs &a, int64_t row, int32
             keep |= 1u << (__ffs(__ballot_sync(kAll, live == best)) - 1);
         }
         if (MODE == kFast) {
-            // each value is off by two scores' errors and three roundings at most
+            // each value is off by two scores' errors and 2 u of its size in roundings
             const uint32_t next = __reduce_max_sync(kAll, (keep >> lane) & 1u ? 0u : uint32_t(value));
             const float scale = __uint_as_float(__reduce_max_sync(kAll, __float_as_uint(size)));
             if (last != 0 && next != 0)
-                unsure = !(value_of(uint32_t(last)) - value_of(next) > 4.f * eps + 0x1p-21f * scale);
+                unsure = !(value_of(uint32_t(last)) - value_of(next) > 4.f * eps + 0x1p-22f * scale);
         }
 #pragma unroll
         for (int i = 0; i < NV; i++)
@@ -434,12 +444,13 @@ __device__ __forceinline__ bool route_row(const RouteArgs &a, int64_t row, int32
     }
     if (MODE == kFast && unsure) return false;
 
-    // kFast with a bias looks one place further, at what it leaves out
-    const int places = a.top_k + (MODE == kFast && a.bias ? 1 : 0);
-    int32_t my_id = -1, beyond = -1;          // slot s is lane s's; `beyond`: place 32
-    Key my_key = 0, beyond_key = 0;
-    int win = -1;
-    for (int s = 0; s < places; s++) {
+    // kFast with a bias goes on past the last place until what it leaves out is
+    // further away than the errors; the candidates so far are then put in exact order
+    const bool fast = MODE == kFast && a.bias;
+    int32_t my_id = -1;                    // slot s is lane s's
+    Key last_key = 0;                      // fast: the last place's
+    int win = -1, found = 0;
+    for (;;) {
         Key best = 0;
         int at = 0;
 #pragma unroll
@@ -452,39 +463,58 @@ __device__ __forceinline__ bool route_row(const RouteArgs &a, int64_t row, int32
         }
         const Key top = warp_max(best);
         if (top == 0) break;
+        if (found >= a.top_k) {
+            const float c0 = value_of(uint32_t(last_key)), c1 = value_of(uint32_t(top));
+            if (c0 - c1 > 2.f * eps + 0x1p-22f * fmaxf(fabsf(c0), fabsf(c1))) break;
+            if (found == 32) return false;
+        }
         win = __reduce_min_sync(kAll, best == top ? at : 0x7FFFFFFF);
-        if (lane == s) {
-            my_id = win;
-            my_key = top;
-        }
-        if (s == 32) {
-            beyond = win;
-            beyond_key = top;
-        }
+        if (lane == found) my_id = win;
+        if (fast && found < a.top_k) last_key = top;
+        if (++found == a.top_k && !fast) break;
     }
-    const float my_logit = my_id >= 0 ? fminf(load_logit(a, row, my_id), kMaxFloat) : 0.f;
-    if (MODE == kFast && a.bias) {
-        // neighbours further apart than both errors are in order; so are equal
-        // ones with the same logit and bias, inside the chosen (lowest index first)
-        const float c = my_id >= 0 ? value_of(uint32_t(my_key)) : 0.f;
+    float my_logit = my_id >= 0 ? fminf(load_logit(a, row, my_id), kMaxFloat) : 0.f;
+    if (fast) {
+        // in order already, by more than the errors?  The same logit and bias tie
+        // exactly, and were taken lowest index first.
         const float b = my_id >= 0 ? __ldg(a.bias + my_id) : 0.f;
+        const float c = fast_score(a, my_logit, m, inv_sum) + b;
         const float c0 = __shfl_up_sync(kAll, c, 1), b0 = __shfl_up_sync(kAll, b, 1);
         const float l0 = __shfl_up_sync(kAll, my_logit, 1);
-        const float margin = 2.f * eps + 0x1p-22f * fmaxf(fabsf(c), fabsf(c0));
-        bool bad = lane > 0 && my_id >= 0 && !(c0 - c > margin) && !(lane < a.top_k && b == b0 && my_logit == l0);
-        if (lane == 31 && beyond >= 0) {
-            const float cb = value_of(uint32_t(beyond_key));
-            bad |= !(c - cb > 2.f * eps + 0x1p-22f * fmaxf(fabsf(c), fabsf(cb)));
+        const bool sure = lane == 0 || my_id < 0 || c0 - c > 2.f * eps + 0x1p-22f * fmaxf(fabsf(c), fabsf(c0)) ||
+                          (b == b0 && my_logit == l0);
+        if (found > a.top_k || !__all_sync(kAll, sure)) {
+            const double all = row_sum();      // by every lane: it holds shuffles
+            const double exact = my_id >= 0 ? score_of(a, my_logit, m, all) + double(b) : 0.0;
+            int place = 0;
+            for (int s = 0; s < found; s++) {
+                const double o = __shfl_sync(kAll, exact, s);
+                const int32_t id = __shfl_sync(kAll, my_id, s);
+                place += o > exact || (o == exact && id < my_id);
+            }
+            if (lane >= found) place = lane;
+            int from = 0;                  // the lane that holds this lane's slot
+            for (int s = 0; s < found; s++)
+                if (__shfl_sync(kAll, place, s) == lane) from = s;
+            const int32_t id = __shfl_sync(kAll, my_id, from);
+            const float lo = __shfl_sync(kAll, my_logit, from);
+            my_id = lane < min(found, a.top_k) ? id : -1;
+            my_logit = lo;
         }
-        if (__any_sync(kAll, bad)) return false;
-        if (lane >= a.top_k) my_id = -1;
     }
-    double w = 0.0;
-    if (my_id >= 0) w = score_of(a, my_logit, m, sum);
-    if (a.renorm) w = w / (warp_sum(w) + 1e-20);
+    // weights in 32 bits unless the scores are so small that those lose them
+    float w = my_id >= 0 ? fast_score(a, my_logit, m, inv_sum) : 0.f;
+    if (__any_sync(kAll, my_id >= 0 && w < 1e-30f)) {
+        double x = my_id >= 0 ? score_of(a, my_logit, m, sum) : 0.0;
+        if (a.renorm) x = x / (warp_sum(x) + 1e-20);
+        w = float(x * double(a.scale));
+    } else {
+        if (a.renorm) w = __fdividef(w, warp_sum(w) + 1e-20f);
+        w *= a.scale;
+    }
     if (lane < a.top_k) {
         a.ids[row * a.top_k + lane] = my_id;
-        a.weights[row * a.top_k + lane] = float(w * double(a.scale));
+        a.weights[row * a.top_k + lane] = w;
         if (count) atomicAdd(&count[my_id < 0 ? a.experts : my_id], 1);
     }
     return true;
