@@ -450,15 +450,55 @@ __device__ __forceinline__ bool route_row(const RouteArgs &a, int64_t row, int32
     int32_t my_id = -1;                    // slot s is lane s's
     Key last_key = 0;                      // fast: the last place's
     int win = -1, found = 0;
+    // Up to eight experts per lane are sorted once (largest first, ties to the lowest
+    // expert): a selection step then looks at the lane's head, 28 instructions where
+    // a scan of the keys takes 73 (8192 tokens, 256 experts in 8 groups, top 8: 33 -> 30 us).
+    constexpr bool kSorted = NV <= 8 && MODE != kExact;
+    int place[NV];
+    if constexpr (kSorted) {
+#pragma unroll
+        for (int i = 0; i < NV; i++) place[i] = i;
+#pragma unroll
+        for (int p = 1; p < NV; p *= 2)
+#pragma unroll
+            for (int k = p; k >= 1; k /= 2)
+#pragma unroll
+                for (int j = k % p; j + k < NV; j += 2 * k)
+#pragma unroll
+                    for (int i = 0; i < k; i++)
+                        if (i + j + k < NV && (i + j) / (2 * p) == (i + j + k) / (2 * p)) {
+                            const int x = i + j, y = i + j + k;
+                            const bool swap = key[y] > key[x] || (key[y] == key[x] && place[y] < place[x]);
+                            const Key kx = swap ? key[y] : key[x], ky = swap ? key[x] : key[y];
+                            const int px = swap ? place[y] : place[x], py = swap ? place[x] : place[y];
+                            key[x] = kx;
+                            key[y] = ky;
+                            place[x] = px;
+                            place[y] = py;
+                        }
+    }
     for (;;) {
         Key best = 0;
         int at = 0;
+        if constexpr (kSorted) {
+            if (win == 32 * place[0] + lane) {         // the last one chosen
 #pragma unroll
-        for (int i = 0; i < NV; i++) {
-            if (win == 32 * i + lane) key[i] = 0;      // the last one chosen
-            if (key[i] > best) {
-                best = key[i];
-                at = 32 * i + lane;
+                for (int i = 0; i + 1 < NV; i++) {
+                    key[i] = key[i + 1];
+                    place[i] = place[i + 1];
+                }
+                key[NV - 1] = 0;
+            }
+            best = key[0];
+            at = 32 * place[0] + lane;
+        } else {
+#pragma unroll
+            for (int i = 0; i < NV; i++) {
+                if (win == 32 * i + lane) key[i] = 0;
+                if (key[i] > best) {
+                    best = key[i];
+                    at = 32 * i + lane;
+                }
             }
         }
         const Key top = warp_max(best);
