@@ -11,8 +11,10 @@ the host, torch ``int16`` (same bits) on the device.
 from __future__ import annotations
 
 import ctypes
+import functools
 import json
 import os
+import sys
 from typing import Optional, Sequence
 
 import numpy as np
@@ -509,11 +511,15 @@ class _Here:
 _HERE = _Here()
 
 
+def _torch():
+    return sys.modules["torch"]     # whoever holds a tensor has imported it
+
+
 def _enter(t, stream):
     """Context in which a call on `t`'s device runs: that device and `stream`
     (default: the device's current stream) are current inside, so that what is
     allocated there belongs to the stream that uses it."""
-    import torch
+    torch = _torch()
     if not t.is_cuda:
         raise ValueError("tensors must be on a CUDA device, got %s" % t.device)
     if stream is None:
@@ -527,14 +533,16 @@ def _enter(t, stream):
 
 def _handle(t):
     """The current stream of `t`'s device (inside _enter), as the C ABI takes it."""
-    import torch
-    return torch._C._cuda_getCurrentRawStream(t.get_device())
+    return _torch()._C._cuda_getCurrentRawStream(t.get_device())
 
 
 def _need(t, name, shape, dtypes, like, rows=False):
     """Check a tensor argument: shape, type, device, and contiguity (rows=True:
     only of each row)."""
-    if t.shape != shape:
+    if t.shape == shape and t.dtype in dtypes and t.get_device() == like.get_device() and t.is_contiguous():
+        if t.is_cuda == like.is_cuda:
+            return
+    if tuple(t.shape) != tuple(shape):
         raise ValueError("%s: shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
     if t.dtype not in dtypes:
         raise ValueError("%s: type %s, expected %s" % (name, t.dtype, " or ".join(str(d) for d in dtypes)))
@@ -544,18 +552,37 @@ def _need(t, name, shape, dtypes, like, rows=False):
         raise ValueError("%s: not contiguous" % name)
 
 
-def _bits():
-    import torch
-    return (torch.bfloat16, torch.int16)
+@functools.lru_cache(maxsize=None)
+def _types():
+    torch = _torch()
+    return (torch.int32,), (torch.float32,), (torch.bfloat16, torch.int16)
+
+
+def _stride(t):
+    """Elements between the rows of a [rows, n] tensor (n where there is one row)."""
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
 
 
 class Grouping:
     """Items grouped by an id (uw_group_rows): offsets int32[groups + 1],
-    order int32[items], slot int32 in the ids' shape (or None)."""
+    order int32[items], slot int32 in the ids' shape (or None).  Keeps the
+    workspaces of the calls that wrote it, one per stream: a captured graph
+    may still use them."""
 
     def __init__(self, offsets, order, slot=None):
         self.offsets, self.order, self.slot = offsets, order, slot
-        self.ws = None
+        self._ws, self._kept = {}, []
+
+    def _workspace(self, nbytes, like, handle):
+        if not nbytes:
+            return None
+        key = (like.get_device(), handle)
+        ws = self._ws.get(key)
+        if ws is None or ws.numel() < nbytes:
+            if ws is not None:
+                self._kept.append(ws)
+            ws = self._ws[key] = _torch().empty(nbytes, dtype=_torch().uint8, device=like.device)
+        return ws.data_ptr()
 
 
 class Routing(Grouping):
@@ -567,70 +594,88 @@ class Routing(Grouping):
         self.ids, self.weights = ids, weights
 
 
+@functools.lru_cache(maxsize=256)
+def _router(*fields):
+    return Router(*fields)
+
+
+@functools.lru_cache(maxsize=1024)
+def _route_bytes(t, *fields):
+    size = ctypes.c_size_t()
+    check(lib().uw_route_workspace_size(t, ctypes.byref(_router(*fields)), ctypes.byref(size)), "uw_route_workspace_size")
+    return size.value
+
+
+@functools.lru_cache(maxsize=1024)
+def _group_bytes(rows, per_row, groups):
+    size = ctypes.c_size_t()
+    check(lib().uw_group_workspace_size(rows, per_row, groups, ctypes.byref(size)), "uw_group_workspace_size")
+    return size.value
+
+
 def route_experts(logits, top_k: int, *, score: str = "softmax", bias=None, n_groups: int = 1, top_groups: int = 1,
                   group_score: str = "max", renormalize: bool = True, scale: float = 1.0, out: Optional[Routing] = None,
                   stream=None) -> Routing:
     """uw_route_experts: logits [t, experts] (float32 or bfloat16; rows may be
     strided) -> Routing.  `out`: a Routing of the same sizes to write into
     (its workspace is kept with it)."""
-    import torch
+    torch = _torch()
+    i32, f32, _ = _types()
     if logits.dim() != 2 or logits.dtype not in (torch.float32, torch.bfloat16):
         raise ValueError("logits: a [t, experts] tensor of float32 or bfloat16")
     if score not in SCORES or group_score not in GROUP_SCORES:
         raise ValueError("unknown score %r or group score %r" % (score, group_score))
     t, e = logits.shape
-    if t > 1 and (logits.stride(1) != 1 and e > 1 or logits.stride(0) < e):
-        raise ValueError("logits: rows must be contiguous and must not overlap")
-    if t == 1 and e > 1 and logits.stride(1) != 1:
-        raise ValueError("logits: rows must be contiguous and must not overlap")
+    stride = e
+    if not logits.is_contiguous():
+        if (e > 1 and logits.stride(1) != 1) or (t > 1 and logits.stride(0) < e):
+            raise ValueError("logits: rows must be contiguous and must not overlap")
+        stride = logits.stride(0) if t > 1 else e
     if bias is not None:
-        _need(bias, "bias", (e,), (torch.float32,), logits)
-    r = Router(e, top_k, n_groups, top_groups, SCORES[score], GROUP_SCORES[group_score], int(renormalize),
-               TYPE_BF16 if logits.dtype == torch.bfloat16 else TYPE_F32, scale)
-    size = ctypes.c_size_t()
-    check(lib().uw_route_workspace_size(t, ctypes.byref(r), ctypes.byref(size)), "uw_route_workspace_size")
+        _need(bias, "bias", (e,), f32, logits)
+    fields = (e, top_k, n_groups, top_groups, SCORES[score], GROUP_SCORES[group_score], 1 if renormalize else 0,
+              TYPE_BF16 if logits.dtype == torch.bfloat16 else TYPE_F32, scale)
+    nbytes = _route_bytes(t, *fields)
     with _enter(logits, stream):
         if out is None:
-            i32 = dict(dtype=torch.int32, device=logits.device)
-            out = Routing(torch.empty(t, top_k, **i32), torch.empty(t, top_k, dtype=torch.float32, device=logits.device),
-                          torch.empty(e + 1, **i32), torch.empty(t * top_k, **i32), torch.empty(t, top_k, **i32))
+            new = lambda *shape, d=torch.int32: torch.empty(shape, dtype=d, device=logits.device)
+            out = Routing(new(t, top_k), new(t, top_k, d=torch.float32), new(e + 1), new(t * top_k), new(t, top_k))
         else:
-            for f, shape in (("ids", (t, top_k)), ("offsets", (e + 1,)), ("order", (t * top_k,)), ("slot", (t, top_k))):
-                _need(getattr(out, f), "out." + f, shape, (torch.int32,), logits)
-            _need(out.weights, "out.weights", (t, top_k), (torch.float32,), logits)
-        if size.value and (out.ws is None or out.ws.numel() < size.value or out.ws.device != logits.device):
-            out.ws = torch.empty(size.value, dtype=torch.uint8, device=logits.device)
-        check(lib().uw_route_experts(logits.data_ptr(), t, logits.stride(0) if t > 1 else e,
-                                     None if bias is None else bias.data_ptr(), ctypes.byref(r), out.ids.data_ptr(),
-                                     out.weights.data_ptr(), out.offsets.data_ptr(), out.order.data_ptr(),
-                                     out.slot.data_ptr(), out.ws.data_ptr() if size.value else None, size.value,
-                                     _handle(logits)), "uw_route_experts")
+            _need(out.ids, "out.ids", (t, top_k), i32, logits)
+            _need(out.weights, "out.weights", (t, top_k), f32, logits)
+            _need(out.offsets, "out.offsets", (e + 1,), i32, logits)
+            _need(out.order, "out.order", (t * top_k,), i32, logits)
+            _need(out.slot, "out.slot", (t, top_k), i32, logits)
+        handle = _handle(logits)
+        check(lib().uw_route_experts(logits.data_ptr(), t, stride, None if bias is None else bias.data_ptr(),
+                                     _router(*fields), out.ids.data_ptr(), out.weights.data_ptr(),
+                                     out.offsets.data_ptr(), out.order.data_ptr(), out.slot.data_ptr(),
+                                     out._workspace(nbytes, logits, handle), nbytes, handle), "uw_route_experts")
     return out
 
 
 def group_rows(ids, groups: int, out: Optional[Grouping] = None, stream=None) -> Grouping:
     """uw_group_rows: int32 ids [rows] or [rows, per_row] -> Grouping of their
     items by id; ids outside [0, groups) belong to no group."""
-    import torch
+    torch = _torch()
+    i32 = _types()[0]
     if ids.dim() not in (1, 2) or ids.dtype != torch.int32 or not ids.is_contiguous():
         raise ValueError("ids: a contiguous int32 tensor [rows] or [rows, per_row]")
     rows, per_row = ids.shape[0], ids.shape[1] if ids.dim() == 2 else 1
-    size = ctypes.c_size_t()
-    check(lib().uw_group_workspace_size(rows, per_row, groups, ctypes.byref(size)), "uw_group_workspace_size")
+    nbytes = _group_bytes(rows, per_row, groups)
     with _enter(ids, stream):
         if out is None:
-            i32 = dict(dtype=torch.int32, device=ids.device)
-            out = Grouping(torch.empty(groups + 1, **i32), torch.empty(ids.numel(), **i32), torch.empty(ids.shape, **i32))
+            new = lambda *shape: torch.empty(shape, dtype=torch.int32, device=ids.device)
+            out = Grouping(new(groups + 1), new(ids.numel()), new(*ids.shape))
         else:
-            _need(out.offsets, "out.offsets", (groups + 1,), (torch.int32,), ids)
-            _need(out.order, "out.order", (ids.numel(),), (torch.int32,), ids)
+            _need(out.offsets, "out.offsets", (groups + 1,), i32, ids)
+            _need(out.order, "out.order", (ids.numel(),), i32, ids)
             if out.slot is not None:
-                _need(out.slot, "out.slot", ids.shape, (torch.int32,), ids)
-        if size.value and (out.ws is None or out.ws.numel() < size.value or out.ws.device != ids.device):
-            out.ws = torch.empty(size.value, dtype=torch.uint8, device=ids.device)
+                _need(out.slot, "out.slot", ids.shape, i32, ids)
+        handle = _handle(ids)
         check(lib().uw_group_rows(ids.data_ptr(), rows, per_row, groups, out.offsets.data_ptr(), out.order.data_ptr(),
-                                  None if out.slot is None else out.slot.data_ptr(),
-                                  out.ws.data_ptr() if size.value else None, size.value, _handle(ids)), "uw_group_rows")
+                                  None if out.slot is None else out.slot.data_ptr(), out._workspace(nbytes, ids, handle),
+                                  nbytes, handle), "uw_group_rows")
     return out
 
 
@@ -656,25 +701,26 @@ def _expert_set(w, name, like) -> ExpertSetArgs:
         if w.device != like.device:
             raise ValueError("%s: on %s, expected %s" % (name, w.device, like.device))
         return ExpertSetArgs(w.n, w.k, w.experts, None, 0, w.table.data_ptr())
-    if w.dim() != 3 or w.dtype not in _bits():
+    if w.dim() != 3 or w.dtype not in _types()[2]:
         raise ValueError("%s: an ExpertSet or BF16 [experts, n, k]" % name)
     e, n, k = w.shape
     if w.device != like.device:
         raise ValueError("%s: on %s, expected %s" % (name, w.device, like.device))
-    if w.stride(2) != 1 or w.stride(1) != k or (e > 1 and w.stride(0) < n * k):
+    step, row, one = w.stride()
+    if one != 1 or row != k or (e > 1 and step < n * k):
         raise ValueError("%s: each expert's matrix must be contiguous" % name)
-    return ExpertSetArgs(n, k, e, w.data_ptr(), w.stride(0) if e > 1 else n * k, None)
+    return ExpertSetArgs(n, k, e, w.data_ptr(), step if e > 1 else n * k, None)
 
 
 def _expert_rows(x, grouping: Grouping, set_: ExpertSetArgs, gather: bool) -> ExpertRows:
-    import torch
+    i32, _, bf16 = _types()
     places = grouping.order.numel()
     if x.dim() != 2:
         raise ValueError("x: [rows, k]")
-    _need(x, "x", (x.shape[0], set_.k), _bits(), x, rows=True)
-    _need(grouping.offsets, "offsets", (set_.experts + 1,), (torch.int32,), x)
-    _need(grouping.order, "order", (places,), (torch.int32,), x)
     rows = x.shape[0]
+    _need(x, "x", (rows, set_.k), bf16, x, rows=True)
+    _need(grouping.offsets, "offsets", (set_.experts + 1,), i32, x)
+    _need(grouping.order, "order", (places,), i32, x)
     if gather:
         if (rows == 0) != (places == 0) or (rows and places % rows):
             raise ValueError("x: %d rows do not share %d routed slots evenly" % (rows, places))
@@ -693,7 +739,10 @@ def make_expert_plan(kernel=KERNEL_TC, bn=256, rows=None, sort=0, width=0, timeo
     return ExpertPlan(kernel, bn, width, rows, sort, timeout_ns)
 
 
-def _default_plan(a: ExpertSetArgs, places: int) -> ExpertPlan:
+@functools.lru_cache(maxsize=1024)
+def _default_plan(plain: bool, experts: int, n: int, k: int, places: int) -> ExpertPlan:
+    # the plan depends on the form and the sizes alone
+    a = ExpertSetArgs(n, k, experts, 16 if plain else None, n * k, None if plain else 16)
     p = ExpertPlan()
     check(lib().uw_expert_plan_default(ctypes.byref(a), places, ctypes.byref(p)), "uw_expert_plan_default")
     return p
@@ -701,7 +750,8 @@ def _default_plan(a: ExpertSetArgs, places: int) -> ExpertPlan:
 
 def expert_plan_default(w, places: int) -> ExpertPlan:
     """uw_expert_plan_default for an ExpertSet or a BF16 [experts, n, k] tensor."""
-    return _default_plan(_expert_set(w, "w", w), places)
+    a = _expert_set(w, "w", w)
+    return ExpertPlan.from_buffer_copy(_default_plan(a.w_dev is not None, a.experts, a.n, a.k, places))
 
 
 def expert_workspace_size(places: int, w, plan: ExpertPlan) -> int:
@@ -714,7 +764,7 @@ def expert_workspace_size(places: int, w, plan: ExpertPlan) -> int:
 
 
 def _expert_call(fn, name, x, sets, routing, gather, plan, out, dtypes, status, ws, stream):
-    import torch
+    torch = _torch()
     a = sets[0]
     r = _expert_rows(x, routing, a, gather)
     with _enter(x, stream):
@@ -723,13 +773,12 @@ def _expert_call(fn, name, x, sets, routing, gather, plan, out, dtypes, status, 
         else:
             _need(out, "out", (r.places, a.n), dtypes, x, rows=True)
         if status is not None:
-            _need(status, "status", status.shape, (torch.int32,), x)
+            _need(status, "status", status.shape, _types()[0], x)
         if plan is None:
-            plan = _default_plan(a, r.places)
+            plan = _default_plan(a.w_dev is not None, a.experts, a.n, a.k, r.places)
         if ws is None and plan.sort and gather:
             ws = torch.empty(r.places * a.k * 2 + 255, dtype=torch.uint8, device=x.device)
-        check(fn(ctypes.byref(r), *[ctypes.byref(v) for v in sets], out.data_ptr(), out.stride(0) if r.places > 1 else a.n,
-                 ctypes.byref(plan), None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel(),
+        check(fn(r, *sets, out.data_ptr(), out.stride(0) if r.places > 1 else a.n, plan, None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel(),
                  None if status is None else status.data_ptr(), _handle(x)), name)
     return out
 
@@ -739,9 +788,8 @@ def expert_matmul(x, w, routing: Grouping, *, gather: bool = False, plan: Option
     """uw_expert_matmul: float32 [places, n] in expert order.  w: an ExpertSet or
     BF16 [experts, n, k].  x: rows in expert order, or with gather=True one row
     per token (the routed slots of a token share its row)."""
-    import torch
     return _expert_call(lib().uw_expert_matmul, "uw_expert_matmul", x, (_expert_set(w, "w", x),), routing, gather, plan, out,
-                        (torch.float32,), status, ws, stream)
+                        _types()[1], status, ws, stream)
 
 
 def expert_gate_up(x, gate, up, routing: Grouping, *, gather: bool = True, plan: Optional[ExpertPlan] = None, out=None,
@@ -751,36 +799,38 @@ def expert_gate_up(x, gate, up, routing: Grouping, *, gather: bool = True, plan:
     a, b = _expert_set(gate, "gate", x), _expert_set(up, "up", x)
     if (a.n, a.k, a.experts) != (b.n, b.k, b.experts):
         raise ValueError("gate and up have different sizes")
-    return _expert_call(lib().uw_expert_gate_up, "uw_expert_gate_up", x, (a, b), routing, gather, plan, out, _bits(), status,
-                        ws, stream)
+    return _expert_call(lib().uw_expert_gate_up, "uw_expert_gate_up", x, (a, b), routing, gather, plan, out, _types()[2],
+                        status, ws, stream)
 
 
 def expert_combine(y, routing: Routing, *, base=None, out=None, stream=None):
     """uw_expert_combine: float32 [t, n], each token's weighted sum of its
     slots' rows of y (float32 [places, n] in expert order), plus base."""
-    import torch
+    torch = _torch()
+    i32, f32, _ = _types()
     t, top_k = routing.slot.shape
     if y.dim() != 2:
         raise ValueError("y: [places, n]")
     n = y.shape[1]
-    _need(y, "y", (t * top_k, n), (torch.float32,), y, rows=True)
-    _need(routing.slot, "slot", (t, top_k), (torch.int32,), y)
-    _need(routing.weights, "weights", (t, top_k), (torch.float32,), y)
+    _need(y, "y", (t * top_k, n), f32, y, rows=True)
+    _need(routing.slot, "slot", (t, top_k), i32, y)
+    _need(routing.weights, "weights", (t, top_k), f32, y)
     if base is not None:
-        _need(base, "base", (t, n), (torch.float32,), y, rows=True)
-    row = (lambda v: v.stride(0) if v.shape[0] > 1 else n)
+        _need(base, "base", (t, n), f32, y, rows=True)
     with _enter(y, stream):
         if out is None:
             out = torch.empty(t, n, dtype=torch.float32, device=y.device)
         else:
-            _need(out, "out", (t, n), (torch.float32,), y, rows=True)
-        check(lib().uw_expert_combine(y.data_ptr(), row(y), routing.slot.data_ptr(), routing.weights.data_ptr(), t, top_k, n,
-                                      _ptr(base), 0 if base is None else row(base), out.data_ptr(), row(out),
-                                      _handle(y)), "uw_expert_combine")
+            _need(out, "out", (t, n), f32, y, rows=True)
+        check(lib().uw_expert_combine(y.data_ptr(), _stride(y), routing.slot.data_ptr(), routing.weights.data_ptr(), t, top_k,
+                                      n, None if base is None else base.data_ptr(), 0 if base is None else _stride(base),
+                                      out.data_ptr(), _stride(out), _handle(y)), "uw_expert_combine")
     return out
 
 
+@functools.lru_cache(maxsize=1024)
 def lora_workspace_size(t: int, k: int, n: int, adapters: int, max_rank: int) -> int:
+    """uw_lora_workspace_size for t rows and slots of these sizes."""
     d = Adapters(n, k, adapters, max_rank)
     size = ctypes.c_size_t()
     check(lib().uw_lora_workspace_size(t, ctypes.byref(d), ctypes.byref(size)), "uw_lora_workspace_size")
@@ -795,41 +845,39 @@ def lora_add(x, a, b, ids, y, *, ranks=None, scales=None, groups: Optional[Group
     each row's slot (outside: none), or `groups` holds the rows' grouping
     (group_rows(ids, adapters), then ids may be None).  out: where the result
     goes (y itself for an update in place)."""
-    import torch
+    torch = _torch()
+    i32, f32, bf16 = _types()
     if x.dim() != 2 or a.dim() != 3 or b.dim() != 3 or y.dim() != 2:
         raise ValueError("x [t, k], a [adapters, max_rank, k], b [adapters, n, max_rank], y [t, n]")
     t, k = x.shape
-    count, rank = a.shape[0], a.shape[1]
+    count, rank, _ = a.shape
     n = b.shape[1]
-    _need(x, "x", (t, k), _bits(), x, rows=True)
-    _need(a, "a", (count, rank, k), _bits(), x)
-    _need(b, "b", (count, n, rank), _bits(), x)
-    _need(y, "y", (t, n), (torch.float32,), x, rows=True)
+    _need(x, "x", (t, k), bf16, x, rows=True)
+    _need(a, "a", (count, rank, k), bf16, x)
+    _need(b, "b", (count, n, rank), bf16, x)
+    _need(y, "y", (t, n), f32, x, rows=True)
     if ranks is not None:
-        _need(ranks, "ranks", (count,), (torch.int32,), x)
+        _need(ranks, "ranks", (count,), i32, x)
     if scales is not None:
-        _need(scales, "scales", (count,), (torch.float32,), x)
+        _need(scales, "scales", (count,), f32, x)
     if groups is None:
-        _need(ids, "ids", (t,), (torch.int32,), x)
+        _need(ids, "ids", (t,), i32, x)
     else:
-        _need(groups.offsets, "groups.offsets", (count + 1,), (torch.int32,), x)
-        _need(groups.order, "groups.order", (t,), (torch.int32,), x)
+        _need(groups.offsets, "groups.offsets", (count + 1,), i32, x)
+        _need(groups.order, "groups.order", (t,), i32, x)
     d = Adapters(n, k, count, rank, a.data_ptr(), b.data_ptr(), None if ranks is None else ranks.data_ptr(),
                  None if scales is None else scales.data_ptr())
     with _enter(x, stream):
         if out is None:
             out = torch.empty(t, n, dtype=torch.float32, device=x.device)
-        else:
-            _need(out, "out", (t, n), (torch.float32,), x, rows=True)
+        elif out is not y:
+            _need(out, "out", (t, n), f32, x, rows=True)
         if ws is None:
-            size = ctypes.c_size_t()
-            check(lib().uw_lora_workspace_size(t, ctypes.byref(d), ctypes.byref(size)), "uw_lora_workspace_size")
-            ws = torch.empty(max(size.value, 1), dtype=torch.uint8, device=x.device)
-        row = (lambda v: v.stride(0) if t > 1 else v.shape[1])
-        check(lib().uw_lora_add(x.data_ptr(), row(x), t, ctypes.byref(d), None if groups is not None else ids.data_ptr(),
+            ws = torch.empty(max(lora_workspace_size(t, k, n, count, rank), 1), dtype=torch.uint8, device=x.device)
+        check(lib().uw_lora_add(x.data_ptr(), _stride(x), t, d, None if groups is not None else ids.data_ptr(),
                                 None if groups is None else groups.offsets.data_ptr(),
-                                None if groups is None else groups.order.data_ptr(), y.data_ptr(), row(y),
-                                out.data_ptr(), row(out), ws.data_ptr(), ws.numel(), _handle(x)), "uw_lora_add")
+                                None if groups is None else groups.order.data_ptr(), y.data_ptr(), _stride(y),
+                                out.data_ptr(), _stride(out), ws.data_ptr(), ws.numel(), _handle(x)), "uw_lora_add")
     return out
 
 
