@@ -267,6 +267,8 @@ __device__ __forceinline__ void expert_pass(const MmaExpertArgs &a, const HalfTi
 template <bool PAL, bool GATED, int Q>
 __global__ void __launch_bounds__(256) k_expert_mma(const MmaExpertArgs a) {
     extern __shared__ __align__(16) uint32_t smem_expert[];
+    pdl_trigger();
+    pdl_wait();
     const Span s = find_active(a.offsets, a.experts, a.places, int(blockIdx.y));
     if (s.expert < 0) return;
     uint32_t *f = smem_expert;
@@ -362,9 +364,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(acce + 2);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
     int32_t *first = reinterpret_cast<int32_t *>(tmem_slot + 2);     // [experts + 1] row tiles before each expert
+    int32_t *place = first + a.experts + 1;                          // [experts + 1] places before each expert
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint64_t T = a.timeout_ns;
     const int most = int(a.places);
+    pdl_trigger();
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < S; s++) {
@@ -385,6 +389,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         tmem_alloc(tmem_slot, 2 * BN);
         tmem_relinquish();
     }
+    pdl_wait();   // offsets, order, x and (a decode's output) the weights are older kernels'
     if (warp == 2) {
         int run = 0;
         for (int e0 = 0; e0 < a.experts; e0 += 32) {
@@ -393,6 +398,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 const int lo = min(max(__ldg(a.offsets + e0 + lane), 0), most);
                 const int hi = min(max(__ldg(a.offsets + e0 + lane + 1), 0), most);
                 tiles = (max(hi - lo, 0) + a.bm - 1) / a.bm;
+                place[e0 + lane] = lo;
+                if (e0 + lane + 1 == a.experts) place[a.experts] = hi;
             }
             int incl = tiles;
 #pragma unroll
@@ -420,9 +427,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             if (first[mid] <= mt) lo = mid;
             else hi = mid;
         }
-        const int p0 = min(max(__ldg(a.offsets + lo), 0), most), p1 = min(max(__ldg(a.offsets + lo + 1), 0), most);
         const int skip = (mt - first[lo]) * a.bm;
-        return Span{lo, p0 + skip, min(a.bm, p1 - p0 - skip)};
+        return Span{lo, place[lo] + skip, min(a.bm, place[lo + 1] - place[lo] - skip)};
     };
 
     // wait for the copies of the last S uses of the ring (all landed unless the
@@ -661,6 +667,8 @@ struct CombineArgs {
 // One token's columns in 16-byte pieces; the slots in order, so that the sum
 // does not vary.  The bytes of y bound it.
 __global__ void __launch_bounds__(256) k_expert_combine(const CombineArgs a) {
+    pdl_trigger();
+    pdl_wait();
     const int64_t t = blockIdx.x;
     const int64_t c = (int64_t(blockIdx.y) * blockDim.x + threadIdx.x) * 4;
     if (c >= a.n) return;
@@ -704,7 +712,7 @@ template <int BN, bool GATED>
 cudaError_t launch_tc(const ExpertLaunch &p, cudaStream_t stream) {
     constexpr int kMaxSmem = 232448;
     const int bm = p.bm, stage = bm * kBK * 2 + BN * kBK * 2 + 16;      // tiles and two barriers
-    const int tail = 1024 + 64 + (p.experts + 4) * 4;
+    const int tail = 1024 + 64 + 2 * (p.experts + 2) * 4;
     const int stages = std::min(12, (kMaxSmem - tail) / stage);
     if (stages < 2) return cudaErrorInvalidValue;
     const size_t smem = size_t(stages) * stage + tail;
@@ -718,7 +726,7 @@ cudaError_t launch_tc(const ExpertLaunch &p, cudaStream_t stream) {
     mb = ma;
     if (GATED && !weight_map(&mb, p.b, p.experts, p.n, p.k, rows)) return cudaErrorInvalidValue;
     static std::atomic<uint64_t> allowed{0};
-    const cudaError_t err = allow_smem(k_expert_tc<BN, GATED>, kMaxSmem, allowed);
+    cudaError_t err = allow_smem(k_expert_tc<BN, GATED>, kMaxSmem, allowed);
     if (err != cudaSuccess) return err;
     TcExpertArgs a{};
     a.experts = p.experts;
@@ -741,8 +749,8 @@ cudaError_t launch_tc(const ExpertLaunch &p, cudaStream_t stream) {
     const int64_t tiles = row_tiles * ((p.n + (GATED ? BN / 2 : BN) - 1) / (GATED ? BN / 2 : BN));
     if (tiles >= (int64_t(1) << 31) - 4096) return cudaErrorInvalidValue;
     const unsigned grid = unsigned(std::min<int64_t>(sm_count(), tiles));
-    k_expert_tc<BN, GATED><<<grid, kTcThreads, smem, stream>>>(mx, ma, mb, a);
-    return cudaGetLastError();
+    err = launch_pdl(true, k_expert_tc<BN, GATED>, dim3(grid), dim3(kTcThreads), smem, stream, mx, ma, mb, a);
+    return err != cudaSuccess ? err : cudaGetLastError();
 }
 
 template <bool PAL, bool GATED>
@@ -768,9 +776,9 @@ cudaError_t launch_mma(const ExpertLaunch &p, cudaStream_t stream) {
     if (smem > 48 * 1024) return cudaErrorInvalidValue;
     const dim3 grid(unsigned(p.n / (GATED ? 8 : 16)), unsigned(std::min<int64_t>(p.experts, p.places)));
     const dim3 block(unsigned(p.slices * 32));
-    if (q == 2) k_expert_mma<PAL, GATED, 2><<<grid, block, smem, stream>>>(a);
-    else k_expert_mma<PAL, GATED, 1><<<grid, block, smem, stream>>>(a);
-    return cudaGetLastError();
+    const cudaError_t err = q == 2 ? launch_pdl(true, k_expert_mma<PAL, GATED, 2>, grid, block, smem, stream, a)
+                                   : launch_pdl(true, k_expert_mma<PAL, GATED, 1>, grid, block, smem, stream, a);
+    return err != cudaSuccess ? err : cudaGetLastError();
 }
 
 }  // namespace
@@ -806,6 +814,8 @@ void expert_fill_entry(void *entry, const uw_dmat &w) {
 static __global__ void __launch_bounds__(256) k_expert_sort(const uint16_t *x, int64_t x_rows, int64_t x_stride, int64_t k, int per_row,
                                                      const int32_t *offsets, int experts, int64_t places,
                                                      const int32_t *order, uint16_t *out) {
+    pdl_trigger();
+    pdl_wait();
     const int64_t p = int64_t(blockIdx.x) * 8 + (threadIdx.x >> 5);
     if (p >= min(places, int64_t(__ldg(offsets + experts)))) return;
     const uint4 *src = reinterpret_cast<const uint4 *>(x + source_row(order, per_row, x_rows, int(p)) * x_stride);
@@ -816,9 +826,8 @@ static __global__ void __launch_bounds__(256) k_expert_sort(const uint16_t *x, i
 cudaError_t launch_expert(const ExpertLaunch &given, cudaStream_t stream) {
     ExpertLaunch p = given;
     if (p.sorted) {
-        k_expert_sort<<<unsigned((p.places + 7) / 8), 256, 0, stream>>>(p.x, p.x_rows, p.x_stride, p.k, p.per_row, p.offsets,
-                                                                        p.experts, p.places, p.order, p.sorted);
-        const cudaError_t err = cudaGetLastError();
+        const cudaError_t err = launch_pdl(true, k_expert_sort, dim3(unsigned((p.places + 7) / 8)), dim3(256), 0, stream, p.x, p.x_rows,
+                                           p.x_stride, p.k, p.per_row, p.offsets, p.experts, p.places, p.order, p.sorted);
         if (err != cudaSuccess) return err;
         p.x = p.sorted;
         p.x_rows = p.places;
@@ -836,8 +845,8 @@ cudaError_t launch_expert(const ExpertLaunch &given, cudaStream_t stream) {
 cudaError_t launch_expert_combine(const CombineLaunch &p, cudaStream_t stream) {
     CombineArgs a{p.y, p.y_stride, p.slot, p.weights, p.t, p.t * p.top_k, p.n, p.top_k, p.base, p.base_stride, p.out, p.out_stride};
     const dim3 grid(unsigned(p.t), unsigned((p.n / 4 + 255) / 256));
-    k_expert_combine<<<grid, 256, 0, stream>>>(a);
-    return cudaGetLastError();
+    const cudaError_t err = launch_pdl(true, k_expert_combine, grid, dim3(256), 0, stream, a);
+    return err != cudaSuccess ? err : cudaGetLastError();
 }
 
 }  // namespace uw

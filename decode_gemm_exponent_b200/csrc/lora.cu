@@ -279,9 +279,11 @@ __global__ void __launch_bounds__(kExpandWarps * 32, C == 4 ? 3 : 4) k_lora_expa
     }
     __syncthreads();
     const Tile tile = s_tile;
-    if (tile.group < 0) return;
-    const int rank = rank_of(a, tile.group);
-    if (rank == 0 && !a.copy_rest) return;
+    const int rank = tile.group < 0 ? 0 : rank_of(a, tile.group);
+    if (tile.group < 0 || (rank == 0 && !a.copy_rest)) {
+        pdl_wait();   // no CTA ends before the kernels that this one stands behind
+        return;
+    }
     const int chunks = (rank + 15) / 16;
 
     const int64_t n0 = (int64_t(blockIdx.y) * kExpandWarps + warp) * a.steps * 32;
