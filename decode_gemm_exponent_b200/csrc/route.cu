@@ -360,7 +360,6 @@ __device__ __forceinline__ bool route_row(const RouteArgs &a, int64_t row, int32
         }
     }
     const float eps = score_error(a);
-    bool unsure = false;
     // the sum in 64 bits, for the rows that need it
     auto row_sum = [&]() -> double {
         if (!a.softmax || MODE == kExact) return sum;
@@ -423,26 +422,53 @@ __device__ __forceinline__ bool route_row(const RouteArgs &a, int64_t row, int32
         }
         if (lane % P) value = 0;           // one lane per group
         uint32_t keep = 0;                 // its lanes
-        Key last = 0;
-        for (int j = 0; j < a.top_groups; j++) {
-            const Key live = (keep >> lane) & 1u ? 0 : value;
-            const Key best = warp_max(live);
-            if (best == 0) break;          // groups that are left hold nothing to choose
-            last = best;
-            keep |= 1u << (__ffs(__ballot_sync(kAll, live == best)) - 1);
-        }
+        auto choose_groups = [&](auto v) {
+            decltype(v) last = 0;
+            keep = 0;
+            for (int j = 0; j < a.top_groups; j++) {
+                const decltype(v) live = (keep >> lane) & 1u ? 0 : v;
+                const decltype(v) best = warp_max(live);
+                if (best == 0) break;      // groups that are left hold nothing to choose
+                last = best;
+                keep |= 1u << (__ffs(__ballot_sync(kAll, live == best)) - 1);
+            }
+            return last;
+        };
+        const Key last = choose_groups(value);
         if (MODE == kFast) {
             // each value is off by two scores' errors and 2 u of its size in roundings
             const uint32_t next = __reduce_max_sync(kAll, (keep >> lane) & 1u ? 0u : uint32_t(value));
             const float scale = __uint_as_float(__reduce_max_sync(kAll, __float_as_uint(size)));
-            if (last != 0 && next != 0)
-                unsure = !(value_of(uint32_t(last)) - value_of(next) > 4.f * eps + 0x1p-22f * scale);
+            if (last != 0 && next != 0 &&
+                !(value_of(uint32_t(last)) - value_of(next) > 4.f * eps + 0x1p-22f * scale)) {
+                // the same in 64 bits, each lane on its share of its group
+                const double all = row_sum();
+                uint64_t f = 0, n = 0;
+                if (g < a.n_groups)
+                    for (int j = lane % P; j < a.group_size; j += P) {
+                        const int e = g * a.group_size + j;
+                        const float v = load_logit(a, row, e);
+                        if (!(v > -INFINITY)) continue;
+                        const double c = score_of(a, fminf(v, kMaxFloat), m, all) + (a.bias ? double(__ldg(a.bias + e)) : 0.0);
+                        const uint64_t k = c > -INFINITY ? key_of(c) : 0;
+                        n = max(n, min(f, k));
+                        f = max(f, k);
+                    }
+                __syncwarp();
+                for (int d = 1; d < P; d *= 2) {
+                    const uint64_t fo = __shfl_xor_sync(kAll, f, d), no = __shfl_xor_sync(kAll, n, d);
+                    n = max(max(n, no), min(f, fo));
+                    f = max(f, fo);
+                }
+                uint64_t exact = f;
+                if (a.top2 && f != 0) exact = key_of(value_of(f) + (n ? value_of(n) : 0.0));
+                choose_groups(lane % P ? uint64_t(0) : exact);
+            }
         }
 #pragma unroll
         for (int i = 0; i < NV; i++)
             if (!((keep >> (P * ((group[i / 4] >> (8 * (i % 4))) & 255u))) & 1u)) key[i] = 0;
     }
-    if (MODE == kFast && unsure) return false;
 
     // kFast with a bias goes on past the last place until what it leaves out is
     // further away than the errors; the candidates so far are then put in exact order

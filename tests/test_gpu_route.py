@@ -248,3 +248,26 @@ def test_refusals(uw):
         uw.group_rows(torch.zeros(4, device="cuda"), 2)
     with pytest.raises(uw.UwError):
         uw.group_rows(torch.zeros(4, device="cuda", dtype=torch.int32), uw.MAX_GROUPS + 1)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("group_score", ["max", "top2"])
+@pytest.mark.parametrize("top_k", [3, 32])
+def test_choices_nearer_than_32_bits_tell_apart(uw, score, group_score, top_k):
+    """Scores plus biases that differ by less than 2^-24, in one group and across
+    groups: the order and the kept groups are those of 64 bits."""
+    g = torch.Generator().manual_seed(top_k)
+    logits = (torch.randint(0, 3, (60, 128), generator=g) * 1e-7 + torch.randn(60, 1, generator=g)).cuda()
+    for bias in (torch.full((128,), 0.5), torch.randint(0, 2, (128,), generator=g) * 2.0 ** -24 + 0.25):
+        check_route(uw, logits, top_k, bias.cuda(), score=score)
+        check_route(uw, logits, top_k, bias.cuda(), score=score, n_groups=8, top_groups=3, group_score=group_score)
+    check_route(uw, logits, top_k, score=score, n_groups=16, top_groups=5, group_score=group_score)
+
+
+@pytest.mark.parametrize("n_groups", [1, 3, 5, 7, 12, 20, 31])
+def test_odd_group_counts(uw, n_groups):
+    e = n_groups * 11
+    bias = torch.randn(e, generator=torch.Generator().manual_seed(e)).mul(0.1).cuda()
+    for group_score in ("max", "top2"):
+        check_route(uw, random_logits(75, e, e), 4, bias, score="sigmoid", n_groups=n_groups, top_groups=(n_groups + 1) // 2,
+                    group_score=group_score)
