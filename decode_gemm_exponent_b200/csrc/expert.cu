@@ -289,7 +289,6 @@ __global__ void __launch_bounds__(256) k_expert_mma(const MmaExpertArgs a) {
 
 constexpr int kBM = 128, kBK = 64;
 constexpr int kTcThreads = 384;       // W producer, MMA, two x producers, eight epilogue warps
-constexpr int kBox = 32;              // rows of x per tiled copy
 constexpr int kSumSteps = 8;          // K-steps per FP32 chunk
 
 struct TcExpertArgs {
@@ -372,7 +371,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < S; s++) {
-            mbar_init(&full[s], 2);          // weights, rows of x
+            mbar_init(&full[s], a.boxes ? 1 : 2);   // weights (with a box of x), gathered rows
             mbar_init(&empty[s], 1);
         }
         for (int b = 0; b < 2; b++) {
@@ -452,7 +451,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     ok = mbar_wait_or_abort(&empty[s], r.phase ^ 1u, T, abort_flag) && !*abort_flag;
                     if (!ok) break;
                     uint8_t *st = wring + size_t(s) * kW;
-                    mbar_arrive_expect_tx(&full[s], uint32_t(kW));
+                    mbar_arrive_expect_tx(&full[s], uint32_t(a.boxes ? kW + xtile : kW));
+                    // one box per tile of x: rows behind the tile's last are the next
+                    // expert's (or zeros) and reach only accumulator rows that are not read
+                    if (a.boxes) tma_load_2d(ring + size_t(s) * xtile, &tmX, ks * kBK, t.pos, &full[s]);
                     if (GATED) {
                         tma_load_3d(st, &tmA, ks * kBK, n0, t.expert, &full[s]);
                         tma_load_3d(st + kW / 2, &tmB, ks * kBK, n0, t.expert, &full[s]);
@@ -507,25 +509,18 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             }
         }
         __syncwarp();
-    } else if (warp == 2) {
-        // ------------------------------------------------ rows of x, TMA
+    } else if (warp == 2 && !a.boxes) {
+        // ------------------------------------------------ rows of x, gathered
         Slot r;
         bool ok = true;
         for (int tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x) {
             const Span t = locate(tile / ntn);
             int32_t row[4];
-            int copies, bytes;           // one copy per lane
-            if (a.boxes) {
-                copies = (t.rows + kBox - 1) / kBox;
-                bytes = kBox * kBK * 2;
-                row[0] = t.pos + lane * kBox;
-            } else {
-                copies = (t.rows + 3) / 4;
-                bytes = 4 * kBK * 2;
+            const int copies = (t.rows + 3) / 4;         // one per lane
+            constexpr int bytes = 4 * kBK * 2;
 #pragma unroll
-                for (int i = 0; i < 4; i++)
-                    row[i] = int32_t(source_row(a.order, a.per_row, a.x_rows, t.pos + min(4 * lane + i, t.rows - 1)));
-            }
+            for (int i = 0; i < 4; i++)
+                row[i] = int32_t(source_row(a.order, a.per_row, a.x_rows, t.pos + min(4 * lane + i, t.rows - 1)));
             for (int ks = 0; ks < a.ksteps; ks++, r.next(S)) {
                 const int s = r.at;
                 ok = mbar_wait_or_abort(&empty[s], r.phase ^ 1u, T, abort_flag);
@@ -533,11 +528,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 if (!ok) break;
                 if (lane == 0) mbar_arrive_expect_tx(&full[s], uint32_t(copies * bytes));
                 __syncwarp();
-                if (lane < copies) {
-                    uint8_t *dst = ring + size_t(s) * xtile + lane * bytes;
-                    if (a.boxes) tma_load_2d(dst, &tmX, ks * kBK, row[0], &full[s]);
-                    else tma_gather4(dst, &tmX, ks * kBK, row, &full[s]);
-                }
+                if (lane < copies) tma_gather4(ring + size_t(s) * xtile + lane * bytes, &tmX, ks * kBK, row, &full[s]);
             }
         }
         if (!ok && lane == 0) {
@@ -720,7 +711,7 @@ cudaError_t launch_tc(const ExpertLaunch &p, cudaStream_t stream) {
     const bool boxes = p.order == nullptr;
     const cuuint64_t xd[2] = {cuuint64_t(p.k), cuuint64_t(p.x_rows)};
     const cuuint64_t xs[1] = {cuuint64_t(p.x_stride) * 2};
-    const cuuint32_t xb[2] = {kBK, boxes ? cuuint32_t(kBox) : 1};       // a gather's box is one row
+    const cuuint32_t xb[2] = {kBK, boxes ? cuuint32_t(bm) : 1};         // a gather's box is one row
     const int rows = GATED ? BN / 2 : BN;
     if (!make_map(&mx, p.x, 2, xd, xs, xb) || !weight_map(&ma, p.a, p.experts, p.n, p.k, rows)) return cudaErrorInvalidValue;
     mb = ma;
