@@ -154,6 +154,9 @@ __global__ void __launch_bounds__(kShrinkWarps * 32, 2) k_lora_shrink(const Lora
     __shared__ int32_t s_row[8 * NT];
     __shared__ float red[kShrinkWarps][RT * NT * 4][32];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+    // The second kernel may start once every CTA is past its wait: what older
+    // kernels wrote (y, the rows' groups) it may then read without waiting itself.
+    pdl_wait();
     pdl_trigger();
     if (warp == 0) {
         const Tile f = find_tile(a, 8 * NT, blockIdx.x, false, s_row);
@@ -501,15 +504,16 @@ cudaError_t launch_lora(const LoraLaunch &p, cudaStream_t stream) {
     const int rt = (p.max_rank + 15) / 16;
     const dim3 grid1(unsigned(geo.shrink_tiles), unsigned(geo.splits), unsigned((rt + geo.rank_tiles - 1) / geo.rank_tiles));
     const dim3 block1(kShrinkWarps * 32);
-    if (geo.token_tiles == 1) k_lora_shrink<1, 1><<<grid1, block1, 0, stream>>>(a);
-    else if (geo.rank_tiles == 1) k_lora_shrink<1, 4><<<grid1, block1, 0, stream>>>(a);
-    else k_lora_shrink<2, 4><<<grid1, block1, 0, stream>>>(a);
-    cudaError_t err = cudaGetLastError();
+    cudaError_t err;
+    if (geo.token_tiles == 1) err = launch_pdl(true, k_lora_shrink<1, 1>, grid1, block1, 0, stream, a);
+    else if (geo.rank_tiles == 1) err = launch_pdl(true, k_lora_shrink<1, 4>, grid1, block1, 0, stream, a);
+    else err = launch_pdl(true, k_lora_shrink<2, 4>, grid1, block1, 0, stream, a);
+    if (err == cudaSuccess) err = cudaGetLastError();
     if (err != cudaSuccess) return err;
     // enough steps per warp that the fragments of V are worth their set-up,
     // few enough that all SMs have work and no wave of CTAs is nearly empty
     const int64_t total = geo.expand_tiles * (p.n / 32);
-    a.steps = int(std::max<int64_t>(1, std::min<int64_t>(geo.token_tiles == 4 ? 4 : 16, total / (148 * 16))));
+    a.steps = int(std::max<int64_t>(1, std::min<int64_t>(geo.token_tiles == 4 ? 4 : 16, total / (148 * 12))));
     const int64_t per_cta = int64_t(kExpandWarps) * a.steps * 32;
     const dim3 grid2(unsigned(geo.expand_tiles), unsigned((p.n + per_cta - 1) / per_cta));
     const size_t smem = kExpandSmem + size_t(geo.token_tiles) * rt * 3 * 32 * 16;

@@ -215,13 +215,15 @@ __device__ __forceinline__ void order_block(const GroupArgs &a, int64_t block, i
 extern __shared__ int32_t smem_route[];
 
 __global__ void __launch_bounds__(1024) k_group(const GroupArgs a) {
-    pdl_wait();   // ids and counts are the previous kernel's output
+    pdl_trigger();
+    pdl_wait();   // ids and counts are an older kernel's output
     order_block(a, blockIdx.x, smem_route, smem_route + a.groups + 1);
 }
 
 __global__ void __launch_bounds__(1024) k_group_count(const int32_t *ids, int64_t items, int groups, int64_t per_block,
                                                       int32_t *counts) {
     pdl_trigger();
+    pdl_wait();
     const int g1 = groups + 1;
     for (int i = threadIdx.x; i < g1; i += blockDim.x) smem_route[i] = 0;
     __syncthreads();
@@ -602,6 +604,7 @@ __global__ void __launch_bounds__(route_threads<NV>()) k_route(const __grid_cons
     const int64_t begin = blockIdx.x * a.rows_per_block, end = min(a.t, begin + a.rows_per_block);
     int32_t *count = a.counts ? smem_route : nullptr;
     pdl_trigger();
+    pdl_wait();
     if (count) {
         for (int i = threadIdx.x; i <= a.experts; i += blockDim.x) count[i] = 0;
         __syncthreads();
@@ -680,13 +683,13 @@ cudaError_t launch_group_rows(const GroupLaunch &p, cudaStream_t stream) {
     const size_t smem = group_smem(p.groups, a.warps);
     if (geo.bytes) {
         int32_t *counts = static_cast<int32_t *>(p.ws);
-        k_group_count<<<unsigned(geo.blocks), 1024, size_t(p.groups + 1) * 4, stream>>>(p.ids, a.items, p.groups,
-                                                                                       a.per_block, counts);
-        const cudaError_t err = cudaGetLastError();
+        cudaError_t err = launch_pdl(true, k_group_count, dim3(unsigned(geo.blocks)), dim3(1024), size_t(p.groups + 1) * 4,
+                                     stream, p.ids, a.items, p.groups, a.per_block, counts);
+        if (err == cudaSuccess) err = cudaGetLastError();
         if (err != cudaSuccess) return err;
         a.counts = counts;
     }
-    const cudaError_t err = launch_pdl(geo.bytes != 0, k_group, dim3(unsigned(geo.blocks)), dim3(threads), smem, stream, a);
+    const cudaError_t err = launch_pdl(true, k_group, dim3(unsigned(geo.blocks)), dim3(threads), smem, stream, a);
     return err != cudaSuccess ? err : cudaGetLastError();
 }
 
@@ -740,7 +743,7 @@ cudaError_t launch_route(const RouteLaunch &p, cudaStream_t stream) {
 #define UW_ROUTE_ONE(NV_, MODE_, I_)                                                            \
     {                                                                                          \
         if (smem > 48 * 1024) err = allow_smem(k_route<NV_, MODE_>, kRouteSmem, allowed[I_]);  \
-        if (err == cudaSuccess) k_route<NV_, MODE_><<<grid, block, smem, stream>>>(a);         \
+        if (err == cudaSuccess) err = launch_pdl(true, k_route<NV_, MODE_>, grid, block, smem, stream, a); \
     }
 #define UW_ROUTE(NV_, I_)                              \
     case NV_:                                          \

@@ -540,8 +540,7 @@ def _need(t, name, shape, dtypes, like, rows=False):
     """Check a tensor argument: shape, type, device, and contiguity (rows=True:
     only of each row)."""
     if t.shape == shape and t.dtype in dtypes and t.get_device() == like.get_device() and t.is_contiguous():
-        if t.is_cuda == like.is_cuda:
-            return
+        return
     if tuple(t.shape) != tuple(shape):
         raise ValueError("%s: shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
     if t.dtype not in dtypes:
