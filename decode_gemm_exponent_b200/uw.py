@@ -498,57 +498,46 @@ def autotune(mats: Sequence[Matrix], ms: Sequence[int], reps: int = 5, stream=No
 
 # ----------------------------------------------------------------------------- around the matmuls
 
-class _Here:
-    """Context of a call on the current device and stream: nothing to switch."""
-
-    def __enter__(self):
-        return None
-
-    def __exit__(self, *exc):
-        return False
-
-
-_HERE = _Here()
-
-
 def _torch():
     return sys.modules["torch"]     # whoever holds a tensor has imported it
 
 
 def _enter(t, stream):
-    """Context in which a call on `t`'s device runs: that device and `stream`
-    (default: the device's current stream) are current inside, so that what is
-    allocated there belongs to the stream that uses it."""
+    """Context in which `t`'s device and `stream` (default: the device's current
+    stream) are current, so that what a call allocates belongs to the stream
+    that uses it."""
     torch = _torch()
     if not t.is_cuda:
         raise ValueError("tensors must be on a CUDA device, got %s" % t.device)
     if stream is None:
-        if t.get_device() == torch._C._cuda_getDevice():
-            return _HERE
-        return torch.cuda.stream(torch.cuda.current_stream(t.device))
-    if stream.device != t.device:
+        stream = torch.cuda.current_stream(t.device)
+    elif stream.device != t.device:
         raise ValueError("stream of %s for tensors of %s" % (stream.device, t.device))
     return torch.cuda.stream(stream)
 
 
-def _handle(t):
-    """The current stream of `t`'s device (inside _enter), as the C ABI takes it."""
-    return _torch()._C._cuda_getCurrentRawStream(t.get_device())
+def _handle(dev):
+    """The current stream of device `dev`, as the C ABI takes it."""
+    return _torch()._C._cuda_getCurrentRawStream(dev)
 
 
-def _need(t, name, shape, dtypes, like, rows=False):
-    """Check a tensor argument: shape, type, device, and contiguity (rows=True:
-    only of each row)."""
-    if t.shape == shape and t.dtype in dtypes and t.get_device() == like.get_device() and t.is_contiguous():
-        return
+def _elsewhere(t, stream):
+    """Whether a call on `t` has to switch the device or the stream first."""
+    return stream is not None or t.get_device() != _torch()._C._cuda_getDevice()
+
+
+def _need(t, name, shape, dtypes, dev, rows=False):
+    """Check a tensor argument: shape, type, device index, and contiguity
+    (rows=True: only of each row).  Returns its address."""
+    if t.shape == shape and t.dtype in dtypes and t.get_device() == dev:
+        if t.is_contiguous() or (rows and t.dim() == 2 and t.stride(1) == 1):
+            return t.data_ptr()
+        raise ValueError("%s: not contiguous" % name)
     if tuple(t.shape) != tuple(shape):
         raise ValueError("%s: shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
     if t.dtype not in dtypes:
         raise ValueError("%s: type %s, expected %s" % (name, t.dtype, " or ".join(str(d) for d in dtypes)))
-    if t.device != like.device:
-        raise ValueError("%s: on %s, expected %s" % (name, t.device, like.device))
-    if not t.is_contiguous() and not (rows and t.dim() == 2 and t.stride(1) == 1):
-        raise ValueError("%s: not contiguous" % name)
+    raise ValueError("%s: on %s, expected cuda:%d" % (name, t.device, dev))
 
 
 @functools.lru_cache(maxsize=None)
@@ -568,19 +557,21 @@ class Grouping:
     workspaces of the calls that wrote it, one per stream: a captured graph
     may still use them."""
 
+    _ws = None
+
     def __init__(self, offsets, order, slot=None):
         self.offsets, self.order, self.slot = offsets, order, slot
-        self._ws, self._kept = {}, []
 
-    def _workspace(self, nbytes, like, handle):
+    def _workspace(self, nbytes, dev, handle):
         if not nbytes:
             return None
-        key = (like.get_device(), handle)
-        ws = self._ws.get(key)
+        if self._ws is None:
+            self._ws, self._kept = {}, []
+        ws = self._ws.get((dev, handle))
         if ws is None or ws.numel() < nbytes:
             if ws is not None:
                 self._kept.append(ws)
-            ws = self._ws[key] = _torch().empty(nbytes, dtype=_torch().uint8, device=like.device)
+            ws = self._ws[dev, handle] = _torch().empty(nbytes, dtype=_torch().uint8, device=dev)
         return ws.data_ptr()
 
 
@@ -589,20 +580,15 @@ class Routing(Grouping):
     [t, top_k], and the grouping of the t * top_k slots by expert."""
 
     def __init__(self, ids, weights, offsets, order, slot):
-        super().__init__(offsets, order, slot)
-        self.ids, self.weights = ids, weights
-
-
-@functools.lru_cache(maxsize=256)
-def _router(*fields):
-    return Router(*fields)
+        self.ids, self.weights, self.offsets, self.order, self.slot = ids, weights, offsets, order, slot
 
 
 @functools.lru_cache(maxsize=1024)
-def _route_bytes(t, *fields):
-    size = ctypes.c_size_t()
-    check(lib().uw_route_workspace_size(t, ctypes.byref(_router(*fields)), ctypes.byref(size)), "uw_route_workspace_size")
-    return size.value
+def _router(t, fields):
+    """The C struct of a router and the workspace of t tokens, by their values."""
+    r, size = Router(*fields), ctypes.c_size_t()
+    check(lib().uw_route_workspace_size(t, ctypes.byref(r), ctypes.byref(size)), "uw_route_workspace_size")
+    return r, size.value
 
 
 @functools.lru_cache(maxsize=1024)
@@ -619,37 +605,36 @@ def route_experts(logits, top_k: int, *, score: str = "softmax", bias=None, n_gr
     strided) -> Routing.  `out`: a Routing of the same sizes to write into
     (its workspace is kept with it)."""
     torch = _torch()
+    if _elsewhere(logits, stream):
+        with _enter(logits, stream):
+            return route_experts(logits, top_k, score=score, bias=bias, n_groups=n_groups, top_groups=top_groups,
+                                 group_score=group_score, renormalize=renormalize, scale=scale, out=out)
     i32, f32, _ = _types()
     if logits.dim() != 2 or logits.dtype not in (torch.float32, torch.bfloat16):
         raise ValueError("logits: a [t, experts] tensor of float32 or bfloat16")
     if score not in SCORES or group_score not in GROUP_SCORES:
         raise ValueError("unknown score %r or group score %r" % (score, group_score))
     t, e = logits.shape
+    dev = logits.get_device()
     stride = e
     if not logits.is_contiguous():
         if (e > 1 and logits.stride(1) != 1) or (t > 1 and logits.stride(0) < e):
             raise ValueError("logits: rows must be contiguous and must not overlap")
         stride = logits.stride(0) if t > 1 else e
-    if bias is not None:
-        _need(bias, "bias", (e,), f32, logits)
     fields = (e, top_k, n_groups, top_groups, SCORES[score], GROUP_SCORES[group_score], 1 if renormalize else 0,
               TYPE_BF16 if logits.dtype == torch.bfloat16 else TYPE_F32, scale)
-    nbytes = _route_bytes(t, *fields)
-    with _enter(logits, stream):
-        if out is None:
-            new = lambda *shape, d=torch.int32: torch.empty(shape, dtype=d, device=logits.device)
-            out = Routing(new(t, top_k), new(t, top_k, d=torch.float32), new(e + 1), new(t * top_k), new(t, top_k))
-        else:
-            _need(out.ids, "out.ids", (t, top_k), i32, logits)
-            _need(out.weights, "out.weights", (t, top_k), f32, logits)
-            _need(out.offsets, "out.offsets", (e + 1,), i32, logits)
-            _need(out.order, "out.order", (t * top_k,), i32, logits)
-            _need(out.slot, "out.slot", (t, top_k), i32, logits)
-        handle = _handle(logits)
-        check(lib().uw_route_experts(logits.data_ptr(), t, stride, None if bias is None else bias.data_ptr(),
-                                     _router(*fields), out.ids.data_ptr(), out.weights.data_ptr(),
-                                     out.offsets.data_ptr(), out.order.data_ptr(), out.slot.data_ptr(),
-                                     out._workspace(nbytes, logits, handle), nbytes, handle), "uw_route_experts")
+    router, nbytes = _router(t, fields)
+    if out is None:
+        new = lambda *shape, d=torch.int32: torch.empty(shape, dtype=d, device=logits.device)
+        out = Routing(new(t, top_k), new(t, top_k, d=torch.float32), new(e + 1), new(t * top_k), new(t, top_k))
+    handle = _handle(dev)
+    check(lib().uw_route_experts(logits.data_ptr(), t, stride, None if bias is None else _need(bias, "bias", (e,), f32, dev),
+                                 router, _need(out.ids, "out.ids", (t, top_k), i32, dev),
+                                 _need(out.weights, "out.weights", (t, top_k), f32, dev),
+                                 _need(out.offsets, "out.offsets", (e + 1,), i32, dev),
+                                 _need(out.order, "out.order", (t * top_k,), i32, dev),
+                                 _need(out.slot, "out.slot", (t, top_k), i32, dev), out._workspace(nbytes, dev, handle),
+                                 nbytes, handle), "uw_route_experts")
     return out
 
 
@@ -657,24 +642,23 @@ def group_rows(ids, groups: int, out: Optional[Grouping] = None, stream=None) ->
     """uw_group_rows: int32 ids [rows] or [rows, per_row] -> Grouping of their
     items by id; ids outside [0, groups) belong to no group."""
     torch = _torch()
+    if _elsewhere(ids, stream):
+        with _enter(ids, stream):
+            return group_rows(ids, groups, out)
     i32 = _types()[0]
     if ids.dim() not in (1, 2) or ids.dtype != torch.int32 or not ids.is_contiguous():
         raise ValueError("ids: a contiguous int32 tensor [rows] or [rows, per_row]")
-    rows, per_row = ids.shape[0], ids.shape[1] if ids.dim() == 2 else 1
+    rows, per_row, dev = ids.shape[0], ids.shape[1] if ids.dim() == 2 else 1, ids.get_device()
     nbytes = _group_bytes(rows, per_row, groups)
-    with _enter(ids, stream):
-        if out is None:
-            new = lambda *shape: torch.empty(shape, dtype=torch.int32, device=ids.device)
-            out = Grouping(new(groups + 1), new(ids.numel()), new(*ids.shape))
-        else:
-            _need(out.offsets, "out.offsets", (groups + 1,), i32, ids)
-            _need(out.order, "out.order", (ids.numel(),), i32, ids)
-            if out.slot is not None:
-                _need(out.slot, "out.slot", ids.shape, i32, ids)
-        handle = _handle(ids)
-        check(lib().uw_group_rows(ids.data_ptr(), rows, per_row, groups, out.offsets.data_ptr(), out.order.data_ptr(),
-                                  None if out.slot is None else out.slot.data_ptr(), out._workspace(nbytes, ids, handle),
-                                  nbytes, handle), "uw_group_rows")
+    if out is None:
+        new = lambda *shape: torch.empty(shape, dtype=torch.int32, device=ids.device)
+        out = Grouping(new(groups + 1), new(ids.numel()), new(*ids.shape))
+    handle = _handle(dev)
+    check(lib().uw_group_rows(ids.data_ptr(), rows, per_row, groups,
+                              _need(out.offsets, "out.offsets", (groups + 1,), i32, dev),
+                              _need(out.order, "out.order", (ids.numel(),), i32, dev),
+                              None if out.slot is None else _need(out.slot, "out.slot", ids.shape, i32, dev),
+                              out._workspace(nbytes, dev, handle), nbytes, handle), "uw_group_rows")
     return out
 
 
@@ -693,43 +677,42 @@ class ExpertSet:
             raise ValueError("the experts' matrices are on different devices")
         self.table = torch.from_numpy(host).to(device)
         self.experts, self.n, self.k, self.device = len(mats), mats[0].n, mats[0].k, device
+        self.args = ExpertSetArgs(self.n, self.k, self.experts, None, 0, self.table.data_ptr())
 
 
-def _expert_set(w, name, like) -> ExpertSetArgs:
+def _expert_set(w, name, dev) -> ExpertSetArgs:
     if isinstance(w, ExpertSet):
-        if w.device != like.device:
-            raise ValueError("%s: on %s, expected %s" % (name, w.device, like.device))
-        return ExpertSetArgs(w.n, w.k, w.experts, None, 0, w.table.data_ptr())
+        if w.table.get_device() != dev:
+            raise ValueError("%s: on %s, expected cuda:%d" % (name, w.device, dev))
+        return w.args
     if w.dim() != 3 or w.dtype not in _types()[2]:
         raise ValueError("%s: an ExpertSet or BF16 [experts, n, k]" % name)
     e, n, k = w.shape
-    if w.device != like.device:
-        raise ValueError("%s: on %s, expected %s" % (name, w.device, like.device))
+    if w.get_device() != dev:
+        raise ValueError("%s: on %s, expected cuda:%d" % (name, w.device, dev))
     step, row, one = w.stride()
     if one != 1 or row != k or (e > 1 and step < n * k):
         raise ValueError("%s: each expert's matrix must be contiguous" % name)
     return ExpertSetArgs(n, k, e, w.data_ptr(), step if e > 1 else n * k, None)
 
 
-def _expert_rows(x, grouping: Grouping, set_: ExpertSetArgs, gather: bool) -> ExpertRows:
+def _expert_rows(x, grouping: Grouping, set_: ExpertSetArgs, gather: bool, dev: int) -> ExpertRows:
     i32, _, bf16 = _types()
     places = grouping.order.numel()
     if x.dim() != 2:
         raise ValueError("x: [rows, k]")
-    rows = x.shape[0]
-    _need(x, "x", (rows, set_.k), bf16, x, rows=True)
-    _need(grouping.offsets, "offsets", (set_.experts + 1,), i32, x)
-    _need(grouping.order, "order", (places,), i32, x)
+    rows, k = x.shape[0], set_.k
+    per_row = 1
     if gather:
         if (rows == 0) != (places == 0) or (rows and places % rows):
             raise ValueError("x: %d rows do not share %d routed slots evenly" % (rows, places))
         per_row = places // rows if rows else 1
-    else:
-        if rows != places:
-            raise ValueError("x: %d rows in expert order, expected %d" % (rows, places))
-        per_row = 1
-    return ExpertRows(places, per_row, grouping.offsets.data_ptr(), grouping.order.data_ptr() if gather else None,
-                      x.data_ptr(), rows, x.stride(0) if rows > 1 else set_.k)
+    elif rows != places:
+        raise ValueError("x: %d rows in expert order, expected %d" % (rows, places))
+    order = _need(grouping.order, "order", (places,), i32, dev)
+    return ExpertRows(places, per_row, _need(grouping.offsets, "offsets", (set_.experts + 1,), i32, dev),
+                      order if gather else None, _need(x, "x", (rows, k), bf16, dev, True), rows,
+                      x.stride(0) if rows > 1 else k)
 
 
 def make_expert_plan(kernel=KERNEL_TC, bn=256, rows=None, sort=0, width=0, timeout_ns=0) -> ExpertPlan:
@@ -749,13 +732,14 @@ def _default_plan(plain: bool, experts: int, n: int, k: int, places: int) -> Exp
 
 def expert_plan_default(w, places: int) -> ExpertPlan:
     """uw_expert_plan_default for an ExpertSet or a BF16 [experts, n, k] tensor."""
-    a = _expert_set(w, "w", w)
+    a = _expert_set(w, "w", w.device.index if isinstance(w, ExpertSet) else w.get_device())
     return ExpertPlan.from_buffer_copy(_default_plan(a.w_dev is not None, a.experts, a.n, a.k, places))
 
 
 def expert_workspace_size(places: int, w, plan: ExpertPlan) -> int:
     """uw_expert_workspace_size for `places` gathered rows."""
-    a, size = _expert_set(w, "w", w), ctypes.c_size_t()
+    a = _expert_set(w, "w", w.device.index if isinstance(w, ExpertSet) else w.get_device())
+    size = ctypes.c_size_t()
     r = ExpertRows(places, 1, None, 1, None, 0, 0)
     check(lib().uw_expert_workspace_size(ctypes.byref(r), ctypes.byref(a), ctypes.byref(plan), ctypes.byref(size)),
           "uw_expert_workspace_size")
@@ -764,21 +748,26 @@ def expert_workspace_size(places: int, w, plan: ExpertPlan) -> int:
 
 def _expert_call(fn, name, x, sets, routing, gather, plan, out, dtypes, status, ws, stream):
     torch = _torch()
+    if _elsewhere(x, stream):
+        with _enter(x, stream):
+            return _expert_call(fn, name, x, sets, routing, gather, plan, out, dtypes, status, ws, None)
+    dev = x.get_device()
+    sets = [_expert_set(w, what, dev) for what, w in sets]
     a = sets[0]
-    r = _expert_rows(x, routing, a, gather)
-    with _enter(x, stream):
-        if out is None:
-            out = torch.empty(r.places, a.n, dtype=dtypes[0], device=x.device)
-        else:
-            _need(out, "out", (r.places, a.n), dtypes, x, rows=True)
-        if status is not None:
-            _need(status, "status", status.shape, _types()[0], x)
-        if plan is None:
-            plan = _default_plan(a.w_dev is not None, a.experts, a.n, a.k, r.places)
-        if ws is None and plan.sort and gather:
-            ws = torch.empty(r.places * a.k * 2 + 255, dtype=torch.uint8, device=x.device)
-        check(fn(r, *sets, out.data_ptr(), out.stride(0) if r.places > 1 else a.n, plan, None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel(),
-                 None if status is None else status.data_ptr(), _handle(x)), name)
+    if len(sets) == 2 and (a.n, a.k, a.experts) != (sets[1].n, sets[1].k, sets[1].experts):
+        raise ValueError("gate and up have different sizes")
+    r = _expert_rows(x, routing, a, gather, dev)
+    places, n = r.places, a.n
+    if out is None:
+        out = torch.empty(places, n, dtype=dtypes[0], device=x.device)
+    if status is not None:
+        status = _need(status, "status", status.shape, _types()[0], dev)
+    if plan is None:
+        plan = _default_plan(a.w_dev is not None, a.experts, n, a.k, places)
+    if ws is None and plan.sort and gather:
+        ws = torch.empty(places * a.k * 2 + 255, dtype=torch.uint8, device=x.device)
+    check(fn(r, *sets, _need(out, "out", (places, n), dtypes, dev, True), out.stride(0) if places > 1 else n, plan,
+             None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel(), status, _handle(dev)), name)
     return out
 
 
@@ -787,43 +776,38 @@ def expert_matmul(x, w, routing: Grouping, *, gather: bool = False, plan: Option
     """uw_expert_matmul: float32 [places, n] in expert order.  w: an ExpertSet or
     BF16 [experts, n, k].  x: rows in expert order, or with gather=True one row
     per token (the routed slots of a token share its row)."""
-    return _expert_call(lib().uw_expert_matmul, "uw_expert_matmul", x, (_expert_set(w, "w", x),), routing, gather, plan, out,
-                        _types()[1], status, ws, stream)
+    return _expert_call(lib().uw_expert_matmul, "uw_expert_matmul", x, (("w", w),), routing, gather, plan, out, _types()[1],
+                        status, ws, stream)
 
 
 def expert_gate_up(x, gate, up, routing: Grouping, *, gather: bool = True, plan: Optional[ExpertPlan] = None, out=None,
                    status=None, ws=None, stream=None):
     """uw_expert_gate_up: bfloat16 [places, n] in expert order, the routed
     experts' silu(gate x) * (up x); gate and up as expert_matmul's w."""
-    a, b = _expert_set(gate, "gate", x), _expert_set(up, "up", x)
-    if (a.n, a.k, a.experts) != (b.n, b.k, b.experts):
-        raise ValueError("gate and up have different sizes")
-    return _expert_call(lib().uw_expert_gate_up, "uw_expert_gate_up", x, (a, b), routing, gather, plan, out, _types()[2],
-                        status, ws, stream)
+    return _expert_call(lib().uw_expert_gate_up, "uw_expert_gate_up", x, (("gate", gate), ("up", up)), routing, gather, plan,
+                        out, _types()[2], status, ws, stream)
 
 
 def expert_combine(y, routing: Routing, *, base=None, out=None, stream=None):
     """uw_expert_combine: float32 [t, n], each token's weighted sum of its
     slots' rows of y (float32 [places, n] in expert order), plus base."""
     torch = _torch()
+    if _elsewhere(y, stream):
+        with _enter(y, stream):
+            return expert_combine(y, routing, base=base, out=out)
     i32, f32, _ = _types()
     t, top_k = routing.slot.shape
     if y.dim() != 2:
         raise ValueError("y: [places, n]")
-    n = y.shape[1]
-    _need(y, "y", (t * top_k, n), f32, y, rows=True)
-    _need(routing.slot, "slot", (t, top_k), i32, y)
-    _need(routing.weights, "weights", (t, top_k), f32, y)
-    if base is not None:
-        _need(base, "base", (t, n), f32, y, rows=True)
-    with _enter(y, stream):
-        if out is None:
-            out = torch.empty(t, n, dtype=torch.float32, device=y.device)
-        else:
-            _need(out, "out", (t, n), f32, y, rows=True)
-        check(lib().uw_expert_combine(y.data_ptr(), _stride(y), routing.slot.data_ptr(), routing.weights.data_ptr(), t, top_k,
-                                      n, None if base is None else base.data_ptr(), 0 if base is None else _stride(base),
-                                      out.data_ptr(), _stride(out), _handle(y)), "uw_expert_combine")
+    n, dev = y.shape[1], y.get_device()
+    if out is None:
+        out = torch.empty(t, n, dtype=torch.float32, device=y.device)
+    check(lib().uw_expert_combine(_need(y, "y", (t * top_k, n), f32, dev, True), _stride(y),
+                                  _need(routing.slot, "slot", (t, top_k), i32, dev),
+                                  _need(routing.weights, "weights", (t, top_k), f32, dev), t, top_k, n,
+                                  None if base is None else _need(base, "base", (t, n), f32, dev, True),
+                                  0 if base is None else _stride(base), _need(out, "out", (t, n), f32, dev, True),
+                                  _stride(out), _handle(dev)), "uw_expert_combine")
     return out
 
 
@@ -845,38 +829,31 @@ def lora_add(x, a, b, ids, y, *, ranks=None, scales=None, groups: Optional[Group
     (group_rows(ids, adapters), then ids may be None).  out: where the result
     goes (y itself for an update in place)."""
     torch = _torch()
+    if _elsewhere(x, stream):
+        with _enter(x, stream):
+            return lora_add(x, a, b, ids, y, ranks=ranks, scales=scales, groups=groups, out=out, ws=ws)
     i32, f32, bf16 = _types()
     if x.dim() != 2 or a.dim() != 3 or b.dim() != 3 or y.dim() != 2:
         raise ValueError("x [t, k], a [adapters, max_rank, k], b [adapters, n, max_rank], y [t, n]")
     t, k = x.shape
     count, rank, _ = a.shape
-    n = b.shape[1]
-    _need(x, "x", (t, k), bf16, x, rows=True)
-    _need(a, "a", (count, rank, k), bf16, x)
-    _need(b, "b", (count, n, rank), bf16, x)
-    _need(y, "y", (t, n), f32, x, rows=True)
-    if ranks is not None:
-        _need(ranks, "ranks", (count,), i32, x)
-    if scales is not None:
-        _need(scales, "scales", (count,), f32, x)
+    n, dev = y.shape[1], x.get_device()
+    d = Adapters(n, k, count, rank, _need(a, "a", (count, rank, k), bf16, dev), _need(b, "b", (count, n, rank), bf16, dev),
+                 None if ranks is None else _need(ranks, "ranks", (count,), i32, dev),
+                 None if scales is None else _need(scales, "scales", (count,), f32, dev))
     if groups is None:
-        _need(ids, "ids", (t,), i32, x)
+        ids, offsets, order = _need(ids, "ids", (t,), i32, dev), None, None
     else:
-        _need(groups.offsets, "groups.offsets", (count + 1,), i32, x)
-        _need(groups.order, "groups.order", (t,), i32, x)
-    d = Adapters(n, k, count, rank, a.data_ptr(), b.data_ptr(), None if ranks is None else ranks.data_ptr(),
-                 None if scales is None else scales.data_ptr())
-    with _enter(x, stream):
-        if out is None:
-            out = torch.empty(t, n, dtype=torch.float32, device=x.device)
-        elif out is not y:
-            _need(out, "out", (t, n), f32, x, rows=True)
-        if ws is None:
-            ws = torch.empty(max(lora_workspace_size(t, k, n, count, rank), 1), dtype=torch.uint8, device=x.device)
-        check(lib().uw_lora_add(x.data_ptr(), _stride(x), t, d, None if groups is not None else ids.data_ptr(),
-                                None if groups is None else groups.offsets.data_ptr(),
-                                None if groups is None else groups.order.data_ptr(), y.data_ptr(), _stride(y),
-                                out.data_ptr(), _stride(out), ws.data_ptr(), ws.numel(), _handle(x)), "uw_lora_add")
+        ids = None
+        offsets = _need(groups.offsets, "groups.offsets", (count + 1,), i32, dev)
+        order = _need(groups.order, "groups.order", (t,), i32, dev)
+    if out is None:
+        out = torch.empty(t, n, dtype=torch.float32, device=x.device)
+    if ws is None:
+        ws = torch.empty(max(lora_workspace_size(t, k, n, count, rank), 1), dtype=torch.uint8, device=x.device)
+    check(lib().uw_lora_add(_need(x, "x", (t, k), bf16, dev, True), _stride(x), t, d, ids, offsets, order,
+                            _need(y, "y", (t, n), f32, dev, True), _stride(y), _need(out, "out", (t, n), f32, dev, True),
+                            _stride(out), ws.data_ptr(), ws.numel(), _handle(dev)), "uw_lora_add")
     return out
 
 
