@@ -309,11 +309,11 @@ extern "C" uw_status uw_expert_table(const uw_dmat *const *mats, int32_t experts
     return UW_OK;
 }
 
-extern "C" uw_status uw_expert_plan_default(const uw_expert_set *w, int64_t places, uw_expert_plan *plan) {
+extern "C" uw_status uw_expert_plan_default(const uw_expert_set *w, int64_t places, int gated, uw_expert_plan *plan) {
     if (!plan || places < 0) return UW_ERR_INVALID_ARG;
     const uw_status st = check_set(w);
     if (st != UW_OK) return st;
-    *plan = expert_plan(w->w_dev != nullptr, w->experts, w->n, w->k, places);
+    *plan = expert_plan(w->w_dev != nullptr, gated != 0, w->experts, w->n, w->k, places);
     return UW_OK;
 }
 

@@ -264,7 +264,10 @@ __device__ __forceinline__ void expert_pass(const MmaExpertArgs &a, const HalfTi
         }
 }
 
-template <bool PAL, bool GATED, int Q>
+// NT: 8-token tiles per pass over the weights.  1 takes half the registers of 2, so
+// that twice the warps' loads are in flight, and repeats the pass after 8 rows
+// instead of 16: for one or two rows per expert on average.
+template <bool PAL, bool GATED, int Q, int NT>
 __global__ void __launch_bounds__(256) k_expert_mma(const MmaExpertArgs a) {
     extern __shared__ __align__(16) uint32_t smem_expert[];
     pdl_trigger();
@@ -278,10 +281,10 @@ __global__ void __launch_bounds__(256) k_expert_mma(const MmaExpertArgs a) {
                                             f + 3 * a.flag_words);
     if (PAL) __syncthreads();
     float *red = reinterpret_cast<float *>(f + 4 * a.flag_words);
-    for (int c0 = 0; c0 < s.rows; c0 += 16) {
+    for (int c0 = 0; c0 < s.rows; c0 += NT == 2 ? 16 : 8) {
         const int m = min(16, s.rows - c0);
-        if (m > 8) expert_pass<PAL, GATED, 2, Q>(a, ta, tb, s.pos + c0, m, red);
-        else expert_pass<PAL, GATED, 1, Q>(a, ta, tb, s.pos + c0, m, red);
+        if (NT == 2 && m > 8) expert_pass<PAL, GATED, 2, Q>(a, ta, tb, s.pos + c0, m, red);
+        else expert_pass<PAL, GATED, 1, Q>(a, ta, tb, s.pos + c0, min(m, 8), red);
     }
 }
 
@@ -767,24 +770,45 @@ cudaError_t launch_mma(const ExpertLaunch &p, cudaStream_t stream) {
     if (smem > 48 * 1024) return cudaErrorInvalidValue;
     const dim3 grid(unsigned(p.n / (GATED ? 8 : 16)), unsigned(std::min<int64_t>(p.experts, p.places)));
     const dim3 block(unsigned(p.slices * 32));
-    const cudaError_t err = q == 2 ? launch_pdl(true, k_expert_mma<PAL, GATED, 2>, grid, block, smem, stream, a)
-                                   : launch_pdl(true, k_expert_mma<PAL, GATED, 1>, grid, block, smem, stream, a);
+    const bool few = p.places <= std::max<int64_t>(8, 2 * int64_t(p.experts));
+    const auto kernel = q == 2 ? (few ? k_expert_mma<PAL, GATED, 2, 1> : k_expert_mma<PAL, GATED, 2, 2>)
+                               : (few ? k_expert_mma<PAL, GATED, 1, 1> : k_expert_mma<PAL, GATED, 1, 2>);
+    const cudaError_t err = launch_pdl(true, kernel, grid, block, smem, stream, a);
     return err != cudaSuccess ? err : cudaGetLastError();
 }
 
 }  // namespace
 
-uw_expert_plan expert_plan(bool plain, int experts, int64_t n, int64_t k, int64_t places) {
+// The default plan.  Measured on sets of 128 experts of 768 x 2048 (gate_up) and
+// 2048 x 768, top 8, and 16 of 4096 x 1408, top 2 (us):
+//   at most one row per expert on average: the warp-MMA kernel, whose launch is
+//   short (4 us for next to nothing, tcgen05 7) and whose CTAs are small: 1 token
+//   12.2 against 15.7, 4 tokens 37.1 / 38.6, 16 tokens 72.1 / 73.7; with two rows
+//   per expert on average it is behind (31.3 / 27.8).  Warps per CTA: as few as
+//   give every SM about eight (1 token: 1 warp 14.9, 2 warps 12.2, 4 warps 14.3),
+//   but FP32 chains of at most 512 of K.
+//   tcgen05: 256 weight rows per tile (64 tokens: 110 against 116 with 128) unless
+//   that leaves SMs without a tile; 64 places per tile up to 48 rows per expert on
+//   average, then 128 (1024 tokens: 167 / 156); a sorted copy of x pays from 24
+//   rows per expert (256 tokens 131 without, 134 with; 512 tokens 164 / 139).
+uw_expert_plan expert_plan(bool plain, bool gated, int experts, int64_t n, int64_t k, int64_t places) {
     uw_expert_plan p{};
-    if (!plain) {
+    const int64_t active = std::min<int64_t>(experts, std::max<int64_t>(places, 1));
+    if (!plain || places <= experts) {
         p.kernel = UW_KERNEL_MMA;
-        p.bn = k > 4096 ? 8 : 4;
+        const int64_t tiles = active * (n / (gated ? 8 : 16));
+        p.bn = tiles >= 148 * 8 ? 1 : tiles >= 148 * 4 ? 2 : 4;
+        if (!gated) p.bn = int(std::min<int64_t>(8, std::max<int64_t>(p.bn, (k + 1023) / 1024)));
+        // rebuilt weights: two warps hide more of the rebuild than one
+        if (!plain) p.bn = std::max(p.bn, 2);
+        p.width = places <= 2 * int64_t(experts) || k % 128 ? 1 : 2;
         return p;
     }
     p.kernel = UW_KERNEL_TC;
-    p.bn = 256;
-    p.rows = places <= 16 * int64_t(experts) ? 32 : 128;
-    p.sort = places > 16 * int64_t(experts);
+    const int64_t cols = gated ? 128 : 256;
+    p.bn = active * ((n + cols - 1) / cols) < 148 ? 128 : 256;
+    p.rows = places <= 48 * int64_t(experts) ? 64 : 128;
+    p.sort = places > 24 * int64_t(experts);
     return p;
 }
 

@@ -303,7 +303,7 @@ struct ExpertLaunch {
     uint64_t timeout_ns;
     uint32_t *status;
 };
-uw_expert_plan expert_plan(bool plain, int experts, int64_t n, int64_t k, int64_t places);   // the default
+uw_expert_plan expert_plan(bool plain, bool gated, int experts, int64_t n, int64_t k, int64_t places);   // the default
 size_t expert_entry_bytes();
 void expert_fill_entry(void *entry, const uw_dmat &w);
 cudaError_t launch_expert(const ExpertLaunch &p, cudaStream_t stream);

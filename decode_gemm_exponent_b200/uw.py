@@ -180,7 +180,8 @@ def lib() -> ctypes.CDLL:
         "uw_lora_workspace_size": (ctypes.c_int, [I64, ctypes.POINTER(Adapters), ctypes.POINTER(SZ)]),
         "uw_lora_add": (ctypes.c_int, [P, I64, I64, ctypes.POINTER(Adapters), P, P, P, P, I64, P, I64, P, SZ, P]),
         "uw_expert_table": (ctypes.c_int, [ctypes.POINTER(ctypes.POINTER(DMat)), I32, P, SZ]),
-        "uw_expert_plan_default": (ctypes.c_int, [ctypes.POINTER(ExpertSetArgs), I64, ctypes.POINTER(ExpertPlan)]),
+        "uw_expert_plan_default": (ctypes.c_int, [ctypes.POINTER(ExpertSetArgs), I64, ctypes.c_int,
+                                                  ctypes.POINTER(ExpertPlan)]),
         "uw_expert_workspace_size": (ctypes.c_int, [ctypes.POINTER(ExpertRows), ctypes.POINTER(ExpertSetArgs),
                                                     ctypes.POINTER(ExpertPlan), ctypes.POINTER(SZ)]),
         "uw_expert_matmul": (ctypes.c_int, [ctypes.POINTER(ExpertRows), ctypes.POINTER(ExpertSetArgs), P, I64,
@@ -722,18 +723,18 @@ def make_expert_plan(kernel=KERNEL_TC, bn=256, rows=None, sort=0, width=0, timeo
 
 
 @functools.lru_cache(maxsize=1024)
-def _default_plan(plain: bool, experts: int, n: int, k: int, places: int) -> ExpertPlan:
+def _default_plan(plain: bool, experts: int, n: int, k: int, places: int, gated: bool) -> ExpertPlan:
     # the plan depends on the form and the sizes alone
     a = ExpertSetArgs(n, k, experts, 16 if plain else None, n * k, None if plain else 16)
     p = ExpertPlan()
-    check(lib().uw_expert_plan_default(ctypes.byref(a), places, ctypes.byref(p)), "uw_expert_plan_default")
+    check(lib().uw_expert_plan_default(ctypes.byref(a), places, int(gated), ctypes.byref(p)), "uw_expert_plan_default")
     return p
 
 
-def expert_plan_default(w, places: int) -> ExpertPlan:
+def expert_plan_default(w, places: int, gated: bool = False) -> ExpertPlan:
     """uw_expert_plan_default for an ExpertSet or a BF16 [experts, n, k] tensor."""
     a = _expert_set(w, "w", w.device.index if isinstance(w, ExpertSet) else w.get_device())
-    return ExpertPlan.from_buffer_copy(_default_plan(a.w_dev is not None, a.experts, a.n, a.k, places))
+    return ExpertPlan.from_buffer_copy(_default_plan(a.w_dev is not None, a.experts, a.n, a.k, places, bool(gated)))
 
 
 def expert_workspace_size(places: int, w, plan: ExpertPlan) -> int:
@@ -763,7 +764,7 @@ def _expert_call(fn, name, x, sets, routing, gather, plan, out, dtypes, status, 
     if status is not None:
         status = _need(status, "status", status.shape, _types()[0], dev)
     if plan is None:
-        plan = _default_plan(a.w_dev is not None, a.experts, n, a.k, places)
+        plan = _default_plan(a.w_dev is not None, a.experts, n, a.k, places, len(sets) == 2)
     if ws is None and plan.sort and gather:
         ws = torch.empty(places * a.k * 2 + 255, dtype=torch.uint8, device=x.device)
     check(fn(r, *sets, _need(out, "out", (places, n), dtypes, dev, True), out.stride(0) if places > 1 else n, plan,

@@ -571,8 +571,9 @@ typedef struct uw_expert_plan {
 } uw_expert_plan;
 
 /* A plan by the rows per expert, places / experts (places: routed slots, t * top_k):
- * TC for plain sets, MMA for compressed ones.                                      */
-uw_status uw_expert_plan_default(const uw_expert_set *w, int64_t places, uw_expert_plan *plan);
+ * MMA for compressed sets and for plain ones up to one row per expert, TC beyond.
+ * gated: for uw_expert_gate_up.                                                    */
+uw_status uw_expert_plan_default(const uw_expert_set *w, int64_t places, int gated, uw_expert_plan *plan);
 
 /* The routed rows: place j of the order (offsets and order as uw_route_experts or
  * uw_group_rows wrote them) belongs to the expert e with offsets[e] <= j <

@@ -145,11 +145,14 @@ def test_expert_calls(uw):
     assert gate_up(wset(), wset(), 68) == uw.ERR_INVALID_ARG
 
     p = uw.ExpertPlan()
-    for w, places, kernel in ((wset(), 8, uw.KERNEL_TC), (wset(), 100000, uw.KERNEL_TC),
-                              (wset(w=None, table=FAKE), 100000, uw.KERNEL_MMA)):
-        assert L.uw_expert_plan_default(ctypes.byref(w), places, ctypes.byref(p)) == 0 and p.kernel == kernel
-    assert L.uw_expert_plan_default(ctypes.byref(wset()), -1, ctypes.byref(p)) == uw.ERR_INVALID_ARG
-    assert L.uw_expert_plan_default(ctypes.byref(wset()), 1, None) == uw.ERR_INVALID_ARG
+    for w, places, gated, kernel in ((wset(), 4, 0, uw.KERNEL_MMA), (wset(), 100000, 0, uw.KERNEL_TC), (wset(), 100, 1, uw.KERNEL_TC),
+                                     (wset(w=None, table=FAKE), 100000, 0, uw.KERNEL_MMA), (wset(k=192, stride=64 * 192), 1, 1, uw.KERNEL_MMA)):
+        assert L.uw_expert_plan_default(ctypes.byref(w), places, gated, ctypes.byref(p)) == 0 and p.kernel == kernel
+        # every default is a valid plan
+        size = ctypes.c_size_t()
+        assert L.uw_expert_workspace_size(ctypes.byref(rows(places=places)), ctypes.byref(w), ctypes.byref(p), ctypes.byref(size)) == 0
+    assert L.uw_expert_plan_default(ctypes.byref(wset()), -1, 0, ctypes.byref(p)) == uw.ERR_INVALID_ARG
+    assert L.uw_expert_plan_default(ctypes.byref(wset()), 1, 0, None) == uw.ERR_INVALID_ARG
 
 
 def test_expert_table(uw):
