@@ -316,13 +316,6 @@ __device__ __forceinline__ void tma_load_3d(void *dst, const CUtensorMap *map, i
         : "memory");
 }
 
-// 32 bytes, 32-byte aligned
-__device__ __forceinline__ void store32(void *p, const uint32_t (&v)[8]) {
-    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]),
-                 "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
-                 : "memory");
-}
-
 // four rows of a 2-D tensor, one after the other in shared memory
 __device__ __forceinline__ void tma_gather4(void *dst, const CUtensorMap *map, int32_t x, const int32_t (&row)[4], uint64_t *bar) {
     asm volatile(
@@ -616,10 +609,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     for (int c = 0; c < kMine; c += 8) {
                         if (n0 + half * kMine + c >= a.n) break;
                         if (a.wide) {
-                            const uint32_t o[8] = {__float_as_uint(sum[c]),     __float_as_uint(sum[c + 1]),
-                                                   __float_as_uint(sum[c + 2]), __float_as_uint(sum[c + 3]),
-                                                   __float_as_uint(sum[c + 4]), __float_as_uint(sum[c + 5]),
-                                                   __float_as_uint(sum[c + 6]), __float_as_uint(sum[c + 7])};
+                            const float o[8] = {sum[c],     sum[c + 1], sum[c + 2], sum[c + 3],
+                                                sum[c + 4], sum[c + 5], sum[c + 6], sum[c + 7]};
                             store32(out + c, o);
                         } else {
                             *reinterpret_cast<float4 *>(out + c) = make_float4(sum[c], sum[c + 1], sum[c + 2], sum[c + 3]);

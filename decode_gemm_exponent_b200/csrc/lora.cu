@@ -19,9 +19,9 @@
 //
 // Second product, out = y + V B^T: tokens are M, output columns N.  V keeps its
 // 32 bits: it is split into three BF16 parts (8 + 8 + 8 bits of mantissa), whose
-// products with B are exact in the MMA.  A warp takes 16 rows x 32 columns; the
-// MMA column tiles interleave in pairs so that a thread owns runs of four
-// columns and reads y and writes out in 16-byte pieces.
+// products with B are exact in the MMA.  A warp takes 16 rows x 32 columns at a
+// time; the MMA column tiles interleave so that a thread owns eight consecutive
+// columns.
 //
 // Bound: for many rows, the bytes of y and out (8 t n); for one token per
 // request, the adapters' bytes, which the many small tiles keep in flight.
@@ -42,7 +42,8 @@ constexpr uint32_t kAll = 0xFFFFFFFFu;
 constexpr int kShrinkWarps = 8;
 constexpr int kExpandWarps = 4;
 constexpr int kAhead = 4;                 // units (16 rows x 32 columns) of y in flight per warp, with the current one
-constexpr size_t kExpandSmem = size_t(kAhead) * 4 * kExpandWarps * 32 * 16;
+constexpr int kUnit = 16 * 128;           // its bytes
+constexpr size_t kExpandSmem = size_t(kAhead) * kUnit * kExpandWarps;
 
 struct LoraArgs {
     const uint16_t *x;
@@ -59,6 +60,7 @@ struct LoraArgs {
     int64_t y_stride;
     float *out;
     int64_t out_stride;
+    int wide;                  // rows of out are 32-byte aligned
     int copy_rest;             // rows without an adapter are copied (out is not y)
     int steps;                 // second product: 32-column steps per warp
 };
@@ -271,11 +273,12 @@ __global__ void __launch_bounds__(kExpandWarps * 32, C == 4 ? 3 : 4) k_lora_expa
     extern __shared__ uint4 s_dyn[];
     __shared__ Tile s_tile;
     __shared__ int32_t s_row[16 * MT];       // rows of the tile, -1: none
-    // y on its way: every thread copies the pieces that it will read itself, so
-    // a wait for its own copies is all the synchronisation there is
-    float4 (*s_y)[4][kExpandWarps * 32] = reinterpret_cast<float4 (*)[4][kExpandWarps * 32]>(s_dyn);
-    uint4 *s_frag = s_dyn + kAhead * 4 * kExpandWarps * 32;
+    // y on its way, a ring of units (16 rows of 128 bytes) per warp: eight lanes copy
+    // a row, so that every request is a whole line; the 16-byte pieces of odd rows
+    // are swapped in pairs to keep the reads free of bank conflicts
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+    uint8_t *s_y = reinterpret_cast<uint8_t *>(s_dyn) + warp * kAhead * kUnit;
+    uint4 *s_frag = s_dyn + kExpandSmem / 16;
     if (warp == 0) {
         const Tile f = find_tile(a, 16 * MT, blockIdx.x, a.copy_rest != 0, s_row);
         if (lane == 0) s_tile = f;
@@ -293,9 +296,9 @@ __global__ void __launch_bounds__(kExpandWarps * 32, C == 4 ? 3 : 4) k_lora_expa
     const int steps = int(max(int64_t(0), min(int64_t(a.steps), (a.n - n0) / 32)));
     const int parts = (tile.rows + 15) / 16;           // of this tile, <= MT
     const int units = steps * parts;
-    // column tile q, MMA column j is output column 16 (q / 2) + 4 (j / 2) + 2 (q % 2) + j % 2
-    // of the step's 32: a row's four lanes read and write 64 bytes at a time
-    const uint16_t *pb = a.b + (int64_t(min(tile.group, a.groups - 1)) * a.n + n0 + 4 * (g >> 1) + (g & 1)) * a.max_rank + 4 * c;
+    // column tile q, MMA column j is output column 8 (j / 2) + 2 q + j % 2 of the step's
+    // 32: a thread owns eight consecutive columns, a row's four lanes a whole line
+    const uint16_t *pb = a.b + (int64_t(min(tile.group, a.groups - 1)) * a.n + n0 + 8 * (g >> 1) + (g & 1)) * a.max_rank + 4 * c;
 
     // B of chunks [j0, j0 + C) for the step at column offset `n`; ranks past the
     // adapter's are zeroed, whatever its storage holds there
@@ -307,8 +310,7 @@ __global__ void __launch_bounds__(kExpandWarps * 32, C == 4 ? 3 : 4) k_lora_expa
             for (int q = 0; q < 4; q++) {
                 w[j][q] = make_uint2(0u, 0u);
                 if (r < rank) {
-                    w[j][q] = __ldg(reinterpret_cast<const uint2 *>(pb + (n + 16 * (q >> 1) + 2 * (q & 1)) * a.max_rank +
-                                                                    16 * (j0 + j)));
+                    w[j][q] = __ldg(reinterpret_cast<const uint2 *>(pb + (n + 2 * q) * a.max_rank + 16 * (j0 + j)));
                     if (r + 4 > rank) {
                         const int left = rank - r;     // 1, 2 or 3 ranks
                         if (left < 2) w[j][q].x &= 0xFFFFu;
@@ -320,16 +322,16 @@ __global__ void __launch_bounds__(kExpandWarps * 32, C == 4 ? 3 : 4) k_lora_expa
     };
     // units of 16 rows x 32 columns, the parts of a step one after the other
     int fetch_part = 0, fetch_slot = 0, fetched = 0;
-    int64_t fetch_n = n0 + 4 * c;
+    int64_t fetch_n = n0 + 4 * (lane & 7);
     auto fetch_y = [&]() {
         if (fetched < units) {
 #pragma unroll
-            for (int h = 0; h < 2; h++) {
-                const int32_t r = s_row[16 * fetch_part + 8 * h + g];
-                if (r < 0) continue;
-                const float *p = a.y + r * a.y_stride + fetch_n;
-                cp_async16(&s_y[fetch_slot][2 * h][threadIdx.x], p);
-                cp_async16(&s_y[fetch_slot][2 * h + 1][threadIdx.x], p + 16);
+            for (int i = 0; i < 4; i++) {
+                const int row = 4 * i + (lane >> 3);
+                const int32_t r = s_row[16 * fetch_part + row];
+                if (r >= 0)
+                    cp_async16(s_y + fetch_slot * kUnit + row * 128 + (((lane & 7) ^ (row & 1)) << 4),
+                               a.y + r * a.y_stride + fetch_n);
             }
             fetched++;
             fetch_slot = fetch_slot + 1 == kAhead ? 0 : fetch_slot + 1;
@@ -389,17 +391,26 @@ __global__ void __launch_bounds__(kExpandWarps * 32, C == 4 ? 3 : 4) k_lora_expa
     auto finish = [&](const float (&d)[4][4], int64_t n, int part) {
         fetch_y();
         asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory");
+        __syncwarp();
 #pragma unroll
         for (int h = 0; h < 2; h++) {
-            const int32_t r = s_row[16 * part + 8 * h + g];
+            const int row = 8 * h + g;
+            const int32_t r = s_row[16 * part + row];
             if (r < 0) continue;
-            const float4 y0 = s_y[slot][2 * h][threadIdx.x], y1 = s_y[slot][2 * h + 1][threadIdx.x];
-            float *o = a.out + r * a.out_stride + n0 + n + 4 * c;
-            __stcs(reinterpret_cast<float4 *>(o), make_float4(y0.x + d[0][2 * h], y0.y + d[0][2 * h + 1], y0.z + d[1][2 * h],
-                                                              y0.w + d[1][2 * h + 1]));
-            __stcs(reinterpret_cast<float4 *>(o + 16), make_float4(y1.x + d[2][2 * h], y1.y + d[2][2 * h + 1],
-                                                                   y1.z + d[3][2 * h], y1.w + d[3][2 * h + 1]));
+            const uint8_t *at = s_y + slot * kUnit + row * 128;
+            const float4 y0 = *reinterpret_cast<const float4 *>(at + (((2 * c) ^ (row & 1)) << 4));
+            const float4 y1 = *reinterpret_cast<const float4 *>(at + (((2 * c + 1) ^ (row & 1)) << 4));
+            const float v[8] = {y0.x + d[0][2 * h], y0.y + d[0][2 * h + 1], y0.z + d[1][2 * h], y0.w + d[1][2 * h + 1],
+                                y1.x + d[2][2 * h], y1.y + d[2][2 * h + 1], y1.z + d[3][2 * h], y1.w + d[3][2 * h + 1]};
+            float *o = a.out + r * a.out_stride + n0 + n + 8 * c;
+            if (a.wide) {
+                store32(o, v);
+            } else {
+                __stcs(reinterpret_cast<float4 *>(o), make_float4(v[0], v[1], v[2], v[3]));
+                __stcs(reinterpret_cast<float4 *>(o + 4), make_float4(v[4], v[5], v[6], v[7]));
+            }
         }
+        __syncwarp();   // the slot is written again by a later fetch
         slot = slot + 1 == kAhead ? 0 : slot + 1;
     };
     for (int s = 0; s < steps; s++) {
@@ -501,6 +512,7 @@ cudaError_t launch_lora(const LoraLaunch &p, cudaStream_t stream) {
     a.out = p.out;
     a.out_stride = p.out_stride;
     a.copy_rest = p.out != p.y;
+    a.wide = ((reinterpret_cast<uintptr_t>(p.out) | uintptr_t(p.out_stride) * 4) & 31u) == 0;
     const int rt = (p.max_rank + 15) / 16;
     const dim3 grid1(unsigned(geo.shrink_tiles), unsigned(geo.splits), unsigned((rt + geo.rank_tiles - 1) / geo.rank_tiles));
     const dim3 block1(kShrinkWarps * 32);
