@@ -292,8 +292,10 @@ __global__ void __launch_bounds__(kExpandWarps * 32, C == 4 ? 3 : 4) k_lora_expa
     }
     const int chunks = (rank + 15) / 16;
 
-    const int64_t n0 = (int64_t(blockIdx.y) * kExpandWarps + warp) * a.steps * 32;
-    const int steps = int(max(int64_t(0), min(int64_t(a.steps), (a.n - n0) / 32)));
+    // the CTA's warps take neighbouring columns, kStride of them per step
+    constexpr int kStride = kExpandWarps * 32;
+    const int64_t n0 = int64_t(blockIdx.y) * a.steps * kStride + warp * 32;
+    const int steps = int(max(int64_t(0), min(int64_t(a.steps), (a.n - n0 + kStride - 32) / kStride)));
     const int parts = (tile.rows + 15) / 16;           // of this tile, <= MT
     const int units = steps * parts;
     // column tile q, MMA column j is output column 8 (j / 2) + 2 q + j % 2 of the step's
@@ -337,7 +339,7 @@ __global__ void __launch_bounds__(kExpandWarps * 32, C == 4 ? 3 : 4) k_lora_expa
             fetch_slot = fetch_slot + 1 == kAhead ? 0 : fetch_slot + 1;
             if (++fetch_part == parts) {
                 fetch_part = 0;
-                fetch_n += 32;
+                fetch_n += kStride;
             }
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
@@ -414,7 +416,7 @@ __global__ void __launch_bounds__(kExpandWarps * 32, C == 4 ? 3 : 4) k_lora_expa
         slot = slot + 1 == kAhead ? 0 : slot + 1;
     };
     for (int s = 0; s < steps; s++) {
-        const int64_t n = int64_t(s) * 32;
+        const int64_t n = int64_t(s) * kStride;
         if (chunks <= C) {
             // all ranks' B in registers: it serves every part, and the next step's
             // comes in meanwhile
@@ -423,7 +425,7 @@ __global__ void __launch_bounds__(kExpandWarps * 32, C == 4 ? 3 : 4) k_lora_expa
             for (int j = 0; j < C; j++)
 #pragma unroll
                 for (int q = 0; q < 4; q++) cur[j][q] = w[j][q];
-            if (s + 1 < steps) load_b(w, n + 32, 0);
+            if (s + 1 < steps) load_b(w, n + kStride, 0);
             for (int part = 0; part < parts; part++) {
                 float d[4][4] = {};
 #pragma unroll
