@@ -63,17 +63,24 @@ uw_status check_expert_plan(const uw_expert_plan *p, const uw_expert_set *w) {
         // the raw-group bitmaps of a tile of rows are staged in 48 KB
         if (w->table_dev && w->k > 131072) return UW_ERR_UNSUPPORTED_SHAPE;
     } else if (p->kernel == UW_KERNEL_TC) {
-        if (!w->w_dev || (p->bn != 128 && p->bn != 256) || p->width) return UW_ERR_INVALID_ARG;
+        if ((p->bn != 128 && p->bn != 256) || p->width) return UW_ERR_INVALID_ARG;
         if (p->rows != 32 && p->rows != 64 && p->rows != 128) return UW_ERR_INVALID_ARG;
-        if (w->stride >= int64_t(1) << 39) return UW_ERR_UNSUPPORTED_SHAPE;   // a tensor map's largest stride
+        // a tensor map's largest stride
+        if ((w->w_dev ? w->stride : w->n * w->k) >= int64_t(1) << 39) return UW_ERR_UNSUPPORTED_SHAPE;
     } else {
         return UW_ERR_INVALID_ARG;
     }
     return UW_OK;
 }
 
-uint64_t expert_workspace(const uw_expert_rows *r, const uw_expert_set *w, const uw_expert_plan *p) {
+// sorted rows of x, then the rebuilt weights
+uint64_t sort_bytes(const uw_expert_rows *r, const uw_expert_set *w, const uw_expert_plan *p) {
     return p->sort && r->order_dev ? up256(uint64_t(r->places) * uint64_t(w->k) * 2) : 0;
+}
+uint64_t expert_workspace(const uw_expert_rows *r, const uw_expert_set *w, bool gated, const uw_expert_plan *p) {
+    const bool rebuild = p->kernel == UW_KERNEL_TC && !w->w_dev && r->places > 0;
+    return sort_bytes(r, w, p) +
+           (rebuild ? up256(uint64_t(gated ? 2 : 1) * uint64_t(w->experts) * uint64_t(w->n) * uint64_t(w->k) * 2) : 0);
 }
 
 uw_status check_expert_call(const uw_expert_rows *r, const uw_expert_set *a, const uw_expert_set *b, const void *out,
@@ -98,7 +105,7 @@ uw_status check_expert_call(const uw_expert_rows *r, const uw_expert_set *a, con
     if (p->kernel == UW_KERNEL_TC && r->x_stride >= int64_t(1) << 39) return UW_ERR_UNSUPPORTED_SHAPE;
     if (!aligned(r->x_dev, 16) || !aligned(out, 16) || !aligned(r->offsets_dev, 4) || !aligned(r->order_dev, 4))
         return UW_ERR_INVALID_ARG;
-    const uint64_t need = expert_workspace(r, a, p);
+    const uint64_t need = expert_workspace(r, a, b != nullptr, p);
     if (need && (!ws || ws_bytes < need || !aligned(ws, 256))) return UW_ERR_WORKSPACE;
     return UW_OK;
 }
@@ -126,7 +133,10 @@ ExpertLaunch expert_launch(const uw_expert_rows *r, const uw_expert_set *a, cons
     l.width = p->width;
     l.bn = p->bn;
     l.bm = p->rows;
-    l.sorted = expert_workspace(r, a, p) ? static_cast<uint16_t *>(ws) : nullptr;
+    const uint64_t sorted = sort_bytes(r, a, p);
+    if (sorted) l.sorted = static_cast<uint16_t *>(ws);
+    if (p->kernel == UW_KERNEL_TC && !a->w_dev)
+        l.rebuilt = reinterpret_cast<uint16_t *>(static_cast<uint8_t *>(ws) + sorted);
     l.timeout_ns = p->timeout_ns > 0 ? uint64_t(p->timeout_ns) : 2000000000ull;
     l.status = status;
     return l;
@@ -317,14 +327,14 @@ extern "C" uw_status uw_expert_plan_default(const uw_expert_set *w, int64_t plac
     return UW_OK;
 }
 
-extern "C" uw_status uw_expert_workspace_size(const uw_expert_rows *rows, const uw_expert_set *w,
+extern "C" uw_status uw_expert_workspace_size(const uw_expert_rows *rows, const uw_expert_set *w, int gated,
                                               const uw_expert_plan *plan, size_t *bytes) {
     if (!bytes || !rows || rows->places < 0) return UW_ERR_INVALID_ARG;
     uw_status st = check_set(w);
     if (st == UW_OK) st = check_expert_plan(plan, w);
     if (st != UW_OK) return st;
     if (rows->places > kMaxItems) return UW_ERR_UNSUPPORTED_SHAPE;
-    *bytes = size_t(expert_workspace(rows, w, plan));
+    *bytes = size_t(expert_workspace(rows, w, gated != 0, plan));
     return UW_OK;
 }
 

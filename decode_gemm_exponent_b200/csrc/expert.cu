@@ -15,8 +15,9 @@
 // as the dense warp-MMA kernel does; compressed weights are rebuilt in
 // registers.  Rows beyond 16 take further passes over the tile, from L2.
 //
-// Many rows per expert (k_expert_tc): persistent tcgen05 kernel, plain BF16
-// weights.  Tokens are the MMA's M (128 rows of one expert), weights its N, so
+// Many rows per expert (k_expert_tc): persistent tcgen05 kernel on plain BF16
+// weights (a compressed set's routed experts are rebuilt into the workspace first:
+// at this many rows the products hide what that moves).  Tokens are the MMA's M (128 rows of one expert), weights its N, so
 // that a token's outputs lie in one TMEM lane: its gate and up values meet in
 // one thread.  Two TMEM accumulators: the epilogue of a tile
 // overlaps the next tile's products.  The tensor core truncates as it
@@ -782,10 +783,12 @@ cudaError_t launch_mma(const ExpertLaunch &p, cudaStream_t stream) {
 //   that leaves SMs without a tile; 64 places per tile up to 48 rows per expert on
 //   average, then 128 (1024 tokens: 167 / 156); a sorted copy of x pays from 24
 //   rows per expert (256 tokens 131 without, 134 with; 512 tokens 164 / 139).
+//   Compressed sets (32 experts of 768 x 2048, gate_up): a pass of the warp-MMA
+//   kernel per 16 rows, until rebuilding the weights once costs less.
 uw_expert_plan expert_plan(bool plain, bool gated, int experts, int64_t n, int64_t k, int64_t places) {
     uw_expert_plan p{};
     const int64_t active = std::min<int64_t>(experts, std::max<int64_t>(places, 1));
-    if (!plain || places <= experts) {
+    if (places <= (plain ? 1 : 16) * int64_t(experts)) {
         p.kernel = UW_KERNEL_MMA;
         const int64_t tiles = active * (n / (gated ? 8 : 16));
         p.bn = tiles >= 148 * 8 ? 1 : tiles >= 148 * 4 ? 2 : 4;
@@ -816,6 +819,40 @@ void expert_fill_entry(void *entry, const uw_dmat &w) {
     memcpy(entry, &p, sizeof(p));
 }
 
+// The routed experts' matrices of a compressed set as BF16, expert e at out + e * nk:
+// 16 weights per thread and step.  The bytes read and written bound it.
+static __global__ void __launch_bounds__(256) k_expert_rebuild(const Planes *table, const int32_t *offsets, int experts,
+                                                               int64_t places, int64_t nk, uint16_t *out) {
+    constexpr int kSteps = 4;
+    pdl_trigger();
+    pdl_wait();
+    const Span s = find_active(offsets, experts, places, int(blockIdx.y));
+    if (s.expert < 0) return;
+    const Planes p = table[s.expert];
+    uint16_t *dst = out + int64_t(s.expert) * nk;
+    Half<1> h[kSteps];
+    bool raw[kSteps];
+#pragma unroll
+    for (int i = 0; i < kSteps; i++) {
+        const int64_t e0 = ((int64_t(blockIdx.x) * kSteps + i) * 256 + threadIdx.x) * 16;
+        raw[i] = false;
+        if (e0 >= nk) continue;
+        const int64_t g = e0 / kGroup;
+        raw[i] = (__ldg(p.flagbits + (g >> 5)) >> (uint32_t(g) & 31u)) & 1u;
+        h[i] = load_half<true, 1>(p.rawexp, p.sm + e0, p.pal + e0 / 8, nullptr, raw[i], g, int(e0 % kGroup), p.flagbits,
+                                  p.rawbase, 0);
+    }
+#pragma unroll
+    for (int i = 0; i < kSteps; i++) {
+        const int64_t e0 = ((int64_t(blockIdx.x) * kSteps + i) * 256 + threadIdx.x) * 16;
+        if (e0 >= nk) continue;
+        uint32_t w[8];
+        rebuild<true, 1>(h[i], raw[i], p.palette, w);
+        *reinterpret_cast<uint4 *>(dst + e0) = make_uint4(w[0], w[1], w[2], w[3]);
+        *reinterpret_cast<uint4 *>(dst + e0 + 8) = make_uint4(w[4], w[5], w[6], w[7]);
+    }
+}
+
 // A row of x per place, in expert order: 16 bytes per thread, one warp a row.
 static __global__ void __launch_bounds__(256) k_expert_sort(const uint16_t *x, int64_t x_rows, int64_t x_stride, int64_t k, int per_row,
                                                      const int32_t *offsets, int experts, int64_t places,
@@ -831,6 +868,18 @@ static __global__ void __launch_bounds__(256) k_expert_sort(const uint16_t *x, i
 
 cudaError_t launch_expert(const ExpertLaunch &given, cudaStream_t stream) {
     ExpertLaunch p = given;
+    if (p.rebuilt) {
+        const int64_t nk = p.n * p.k;
+        const dim3 grid(unsigned((nk + 4 * 256 * 16 - 1) / (4 * 256 * 16)), unsigned(std::min<int64_t>(p.experts, p.places)));
+        for (int i = 0; i < (p.gated ? 2 : 1); i++) {
+            ExpertSet &set = i ? p.b : p.a;
+            uint16_t *out = p.rebuilt + int64_t(i) * p.experts * nk;
+            const cudaError_t err = launch_pdl(true, k_expert_rebuild, grid, dim3(256), 0, stream,
+                                               static_cast<const Planes *>(set.table), p.offsets, p.experts, p.places, nk, out);
+            if (err != cudaSuccess) return err;
+            set = ExpertSet{out, nk, nullptr};
+        }
+    }
     if (p.sorted) {
         const cudaError_t err = launch_pdl(true, k_expert_sort, dim3(unsigned((p.places + 7) / 8)), dim3(256), 0, stream, p.x, p.x_rows,
                                            p.x_stride, p.k, p.per_row, p.offsets, p.experts, p.places, p.order, p.sorted);

@@ -300,6 +300,7 @@ struct ExpertLaunch {
     int slices, width;         // MMA
     int bn, bm;                // TC: weight rows and places per tile
     uint16_t *sorted;          // TC: where the rows of x go in expert order first (null: gathered)
+    uint16_t *rebuilt;         // TC on compressed sets: where their BF16 weights go, [sets][experts][n][k]
     uint64_t timeout_ns;
     uint32_t *status;
 };

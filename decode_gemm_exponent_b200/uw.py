@@ -182,7 +182,7 @@ def lib() -> ctypes.CDLL:
         "uw_expert_table": (ctypes.c_int, [ctypes.POINTER(ctypes.POINTER(DMat)), I32, P, SZ]),
         "uw_expert_plan_default": (ctypes.c_int, [ctypes.POINTER(ExpertSetArgs), I64, ctypes.c_int,
                                                   ctypes.POINTER(ExpertPlan)]),
-        "uw_expert_workspace_size": (ctypes.c_int, [ctypes.POINTER(ExpertRows), ctypes.POINTER(ExpertSetArgs),
+        "uw_expert_workspace_size": (ctypes.c_int, [ctypes.POINTER(ExpertRows), ctypes.POINTER(ExpertSetArgs), ctypes.c_int,
                                                     ctypes.POINTER(ExpertPlan), ctypes.POINTER(SZ)]),
         "uw_expert_matmul": (ctypes.c_int, [ctypes.POINTER(ExpertRows), ctypes.POINTER(ExpertSetArgs), P, I64,
                                             ctypes.POINTER(ExpertPlan), P, SZ, P, P]),
@@ -737,14 +737,16 @@ def expert_plan_default(w, places: int, gated: bool = False) -> ExpertPlan:
     return ExpertPlan.from_buffer_copy(_default_plan(a.w_dev is not None, a.experts, a.n, a.k, places, bool(gated)))
 
 
-def expert_workspace_size(places: int, w, plan: ExpertPlan) -> int:
-    """uw_expert_workspace_size for `places` gathered rows."""
-    a = _expert_set(w, "w", w.device.index if isinstance(w, ExpertSet) else w.get_device())
+def _expert_bytes(r: ExpertRows, a: ExpertSetArgs, gated: bool, plan: ExpertPlan) -> int:
     size = ctypes.c_size_t()
-    r = ExpertRows(places, 1, None, 1, None, 0, 0)
-    check(lib().uw_expert_workspace_size(ctypes.byref(r), ctypes.byref(a), ctypes.byref(plan), ctypes.byref(size)),
-          "uw_expert_workspace_size")
+    check(lib().uw_expert_workspace_size(r, a, int(gated), plan, ctypes.byref(size)), "uw_expert_workspace_size")
     return int(size.value)
+
+
+def expert_workspace_size(places: int, w, plan: ExpertPlan, gated: bool = False, gather: bool = True) -> int:
+    """uw_expert_workspace_size for `places` routed slots."""
+    a = _expert_set(w, "w", w.device.index if isinstance(w, ExpertSet) else w.get_device())
+    return _expert_bytes(ExpertRows(places, 1, None, 1 if gather else None, None, 0, 0), a, gated, plan)
 
 
 def _expert_call(fn, name, x, sets, routing, gather, plan, out, dtypes, status, ws, stream):
@@ -765,8 +767,8 @@ def _expert_call(fn, name, x, sets, routing, gather, plan, out, dtypes, status, 
         status = _need(status, "status", status.shape, _types()[0], dev)
     if plan is None:
         plan = _default_plan(a.w_dev is not None, a.experts, n, a.k, places, len(sets) == 2)
-    if ws is None and plan.sort and gather:
-        ws = torch.empty(places * a.k * 2 + 255, dtype=torch.uint8, device=x.device)
+    if ws is None and plan.kernel == KERNEL_TC and (plan.sort or a.w_dev is None):
+        ws = torch.empty(max(1, _expert_bytes(r, a, len(sets) == 2, plan)), dtype=torch.uint8, device=x.device)
     check(fn(r, *sets, _need(out, "out", (places, n), dtypes, dev, True), out.stride(0) if places > 1 else n, plan,
              None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel(), status, _handle(dev)), name)
     return out

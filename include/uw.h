@@ -558,8 +558,9 @@ uw_status uw_expert_table(const uw_dmat *const *mats, int32_t experts, void *tab
 
 /* How the calls below run. */
 typedef struct uw_expert_plan {
-    int32_t kernel;      /* UW_KERNEL_MMA: any set, made for few rows per expert; UW_KERNEL_TC:
-                            plain sets, any number of rows                              */
+    int32_t kernel;      /* UW_KERNEL_MMA: made for few rows per expert; UW_KERNEL_TC: any
+                            number of rows; a compressed set's routed experts are first
+                            rebuilt to BF16 in the workspace (2 n k bytes per expert)   */
     int32_t bn;          /* MMA: warps per CTA, 1..8, which split K; TC: weight rows per
                             tile, 128 or 256 (gate_up: half of each matrix)             */
     int32_t width;       /* MMA: 16 (1) or 32 (2, k a multiple of 128) weights per lane and
@@ -571,8 +572,8 @@ typedef struct uw_expert_plan {
 } uw_expert_plan;
 
 /* A plan by the rows per expert, places / experts (places: routed slots, t * top_k):
- * MMA for compressed sets and for plain ones up to one row per expert, TC beyond.
- * gated: for uw_expert_gate_up.                                                    */
+ * MMA up to one row per expert (compressed sets: 16), TC beyond.  gated: for
+ * uw_expert_gate_up.                                                               */
 uw_status uw_expert_plan_default(const uw_expert_set *w, int64_t places, int gated, uw_expert_plan *plan);
 
 /* The routed rows: place j of the order (offsets and order as uw_route_experts or
@@ -583,7 +584,7 @@ uw_status uw_expert_plan_default(const uw_expert_set *w, int64_t places, int gat
  * x_dev: BF16 [x_rows, k], rows x_stride apart (>= k, a multiple of 8), 16-byte
  * aligned.  dev_status: device uint32 for kernel error bits, may be NULL.
  * places >= 0; 0 launches nothing.  ws: >= uw_expert_workspace_size bytes (0 unless
- * the plan sorts), 256-byte aligned; its contents do not matter.                    */
+ * the plan sorts or rebuilds), 256-byte aligned; its contents do not matter.       */
 typedef struct uw_expert_rows {
     int64_t places;           /* t * top_k, < 2^31                                    */
     int32_t per_row;          /* top_k                                                */
@@ -592,8 +593,8 @@ typedef struct uw_expert_rows {
     int64_t x_rows, x_stride;
 } uw_expert_rows;
 
-uw_status uw_expert_workspace_size(const uw_expert_rows *rows, const uw_expert_set *w, const uw_expert_plan *plan,
-                                   size_t *bytes);
+uw_status uw_expert_workspace_size(const uw_expert_rows *rows, const uw_expert_set *w, int gated,
+                                   const uw_expert_plan *plan, size_t *bytes);
 
 /* y[j] = W_e x: float [places, n], rows y_stride apart (>= n, a multiple of 4),
  * 16-byte aligned.  A compressed set's result is bit-identical to the plain set's

@@ -170,12 +170,13 @@ def test_nan_rows_stay_with_their_tokens(uw):
         assert torch.equal(got[keep], want[keep])
 
 
-@pytest.mark.parametrize("slices,width", [(1, 1), (4, 2), (8, 0), (3, 1)])
+@pytest.mark.parametrize("kernel,bn,kw", [(3, 1, dict(width=1)), (3, 4, dict(width=2)), (3, 8, {}), (3, 3, dict(width=1)),
+                                          (2, 128, dict(rows=32)), (2, 256, dict(rows=128, sort=1))])
 @pytest.mark.parametrize("k", [256, 1152])
-def test_compressed_equals_plain_bit_for_bit(uw, slices, width, k):
+def test_compressed_equals_plain_bit_for_bit(uw, kernel, bn, kw, k):
     from decode_gemm_exponent_b200 import synth
     t, e, n = 23, 6, 192
-    plan = uw.make_expert_plan(uw.KERNEL_MMA, slices, width=width)
+    plan = uw.make_expert_plan(kernel, bn, **kw)
     ws = [[synth.weights_bf16(n, k, 0.01 + 0.004 * i, 0.004, 1.0, seed=100 * j + i) for i in range(e)] for j in range(2)]
     sets = [uw.ExpertSet([uw.Matrix(uw.encode(w)) for w in row]) for row in ws]
     plain = [torch.from_numpy(np.stack(row).view(np.int16)).cuda() for row in ws]
@@ -280,8 +281,9 @@ def test_refusals(uw):
     from decode_gemm_exponent_b200 import synth
     mats = [uw.Matrix(uw.encode(synth.weights_bf16(64, 128, 0.02, 0.0, 1.0, seed=i))) for i in range(4)]
     s = uw.ExpertSet(mats)
-    with pytest.raises(uw.UwError):            # tcgen05 plans take plain weights
-        uw.expert_matmul(x, s, r, gather=True, plan=P(uw.KERNEL_TC, 128))
+    with pytest.raises(uw.UwError) as err:     # rebuilt weights need a workspace
+        uw.expert_matmul(x, s, r, gather=True, plan=P(uw.KERNEL_TC, 128), ws=torch.empty(512, device="cuda").byte())
+    assert err.value.status == uw.ERR_WORKSPACE
     with pytest.raises(uw.UwError) as err:     # the sorted rows need a workspace
         uw.expert_matmul(x, w, r, gather=True, plan=P(uw.KERNEL_TC, 128, sort=1), ws=torch.empty(512, device="cuda").byte())
     assert err.value.status == uw.ERR_WORKSPACE

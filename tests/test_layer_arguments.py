@@ -127,12 +127,16 @@ def test_expert_calls(uw):
         assert run(plan=plan) == uw.ERR_INVALID_ARG
     assert run(w=wset(k=192, stride=64 * 192), r=rows(xs=192), plan=P(uw.KERNEL_MMA, 4, width=2)) == uw.ERR_INVALID_ARG
     tc = P(uw.KERNEL_TC, 256)
-    assert run(w=wset(w=None, table=FAKE), plan=tc) == uw.ERR_INVALID_ARG
+    assert run(w=wset(w=None, table=FAKE), plan=tc) == uw.ERR_WORKSPACE       # rebuilt weights need one
     assert run(w=wset(stride=1 << 39), plan=tc) == uw.ERR_UNSUPPORTED_SHAPE
     sort, size = P(uw.KERNEL_TC, 256, sort=1), ctypes.c_size_t()
     for r, want in ((rows(), 16 * 128 * 2), (rows(order=None), 0)):
-        assert L.uw_expert_workspace_size(ctypes.byref(r), ctypes.byref(wset()), ctypes.byref(sort), ctypes.byref(size)) == 0
+        assert L.uw_expert_workspace_size(ctypes.byref(r), ctypes.byref(wset()), 1, ctypes.byref(sort), ctypes.byref(size)) == 0
         assert size.value == want
+        compressed = wset(w=None, table=FAKE)
+        for gated in (0, 1):
+            assert L.uw_expert_workspace_size(ctypes.byref(r), ctypes.byref(compressed), gated, ctypes.byref(sort), ctypes.byref(size)) == 0
+            assert size.value == want + (1 + gated) * 4 * 64 * 128 * 2
     for ws, nbytes in ((None, 0), (FAKE, 4095), (FAKE + 16, 1 << 20)):
         assert run(plan=sort, ws=ws, nbytes=nbytes) == uw.ERR_WORKSPACE
 
@@ -146,11 +150,11 @@ def test_expert_calls(uw):
 
     p = uw.ExpertPlan()
     for w, places, gated, kernel in ((wset(), 4, 0, uw.KERNEL_MMA), (wset(), 100000, 0, uw.KERNEL_TC), (wset(), 100, 1, uw.KERNEL_TC),
-                                     (wset(w=None, table=FAKE), 100000, 0, uw.KERNEL_MMA), (wset(k=192, stride=64 * 192), 1, 1, uw.KERNEL_MMA)):
+                                     (wset(w=None, table=FAKE), 64, 0, uw.KERNEL_MMA), (wset(w=None, table=FAKE), 65, 0, uw.KERNEL_TC), (wset(k=192, stride=64 * 192), 1, 1, uw.KERNEL_MMA)):
         assert L.uw_expert_plan_default(ctypes.byref(w), places, gated, ctypes.byref(p)) == 0 and p.kernel == kernel
         # every default is a valid plan
         size = ctypes.c_size_t()
-        assert L.uw_expert_workspace_size(ctypes.byref(rows(places=places)), ctypes.byref(w), ctypes.byref(p), ctypes.byref(size)) == 0
+        assert L.uw_expert_workspace_size(ctypes.byref(rows(places=places)), ctypes.byref(w), gated, ctypes.byref(p), ctypes.byref(size)) == 0
     assert L.uw_expert_plan_default(ctypes.byref(wset()), -1, 0, ctypes.byref(p)) == uw.ERR_INVALID_ARG
     assert L.uw_expert_plan_default(ctypes.byref(wset()), 1, 0, None) == uw.ERR_INVALID_ARG
 
