@@ -36,7 +36,8 @@ uw_status check_groups(int64_t rows, int32_t per_row, int32_t groups) {
 
 uw_status check_adapters(const uw_adapters *a, int64_t t) {
     if (!a || t < 0 || a->n <= 0 || a->k <= 0) return UW_ERR_INVALID_ARG;
-    if (a->n % 64 || a->k % 64 || a->n > kMaxItems || a->k > kMaxItems) return UW_ERR_UNSUPPORTED_SHAPE;
+    // column blocks of at least 128 are a grid dimension
+    if (a->n % 64 || a->k % 64 || a->n > 65535 * 128 || a->k > kMaxItems) return UW_ERR_UNSUPPORTED_SHAPE;
     if (a->count < 1 || a->count > UW_MAX_GROUPS) return UW_ERR_INVALID_ARG;
     if (a->max_rank < 8 || a->max_rank > 256 || a->max_rank % 8) return UW_ERR_INVALID_ARG;
     if (t > kMaxItems) return UW_ERR_UNSUPPORTED_SHAPE;

@@ -45,7 +45,10 @@
  *     previous libuw kernel on the stream is still draining; X is read, and
  *     Y and the workspace are written, only after that kernel has completed.
  *     Kernels of other libraries on the stream end before it starts, as
- *     usual.  The library never writes a blob's device copy.
+ *     usual.  The library never writes a blob's device copy.  The operators
+ *     around the matmuls (routing, grouping, expert products, adapters) are
+ *     launched the same way, but read nothing before the previous kernel has
+ *     completed.
  */
 #ifndef UW_H
 #define UW_H
@@ -612,7 +615,8 @@ uw_status uw_expert_gate_up(const uw_expert_rows *rows, const uw_expert_set *gat
 /* out[i] = (base[i] +) sum over s < top_k of weights[i, s] * y[slot[i, s]], in that
  * order; slots of -1 add nothing.  y: float [t * top_k, n] in expert order; base_dev
  * (float [t, n], may be NULL, may be out_dev) is for a shared expert's output or a
- * residual.  n a multiple of 4, strides >= n and multiples of 4, 16-byte aligned.   */
+ * residual.  n a multiple of 4, strides >= n and multiples of 4, 16-byte aligned.
+ * out must not overlap y.                                                          */
 uw_status uw_expert_combine(const float *y_dev, int64_t y_stride, const int32_t *slot_dev, const float *weights_dev,
                             int64_t t, int32_t top_k, int64_t n, const float *base_dev, int64_t base_stride,
                             float *out_dev, int64_t out_stride, void *stream);
@@ -622,7 +626,7 @@ uw_status uw_expert_combine(const float *y_dev, int64_t y_stride, const int32_t 
 
 /* The adapters of one projection, in slots of equal size. */
 typedef struct uw_adapters {
-    int64_t n, k;             /* the projection's sizes, multiples of 64              */
+    int64_t n, k;             /* the projection's sizes, multiples of 64, n <= 65535 * 128 */
     int32_t count;            /* 1..UW_MAX_GROUPS slots                               */
     int32_t max_rank;         /* ranks per slot, a multiple of 8, 8..256              */
     const uint16_t *a_dev;    /* BF16 [count, max_rank, k], 16-byte aligned           */

@@ -73,7 +73,7 @@ def test_lora(uw):
 
     for kw, status in ((dict(n=0), 1), (dict(k=-64), 1), (dict(n=100), 2), (dict(k=100), 2), (dict(count=0), 1),
                        (dict(count=1025), 1), (dict(rank=0), 1), (dict(rank=12), 1), (dict(rank=264), 1),
-                       (dict(k=1 << 40), 2)):
+                       (dict(k=1 << 40), 2), (dict(n=1 << 24), 2)):
         assert L.uw_lora_workspace_size(8, ctypes.byref(adapters(**kw)), ctypes.byref(size)) == status, kw
     assert L.uw_lora_workspace_size(-1, ctypes.byref(adapters()), ctypes.byref(size)) == 1
     assert L.uw_lora_workspace_size(0, ctypes.byref(adapters()), ctypes.byref(size)) == 0 and size.value == 0
