@@ -148,11 +148,13 @@ struct LoraWorkspace {
     uint64_t order_off, sort_off, v_off, bytes;
 };
 LoraWorkspace lora_workspace(int64_t t, const uw_adapters *a) {
-    LoraWorkspace w;
+    LoraWorkspace w{};
+    const LoraGeometry g = lora_geometry(t, a->k, a->count, a->max_rank);
+    if (g.few && t <= kLoraUngrouped) return w;
     w.order_off = up256(uint64_t(a->count + 1) * 4);
     w.sort_off = w.order_off + up256(uint64_t(t) * 4);
     w.v_off = w.sort_off + group_geometry(t, 1, a->count).bytes;
-    w.bytes = w.v_off + lora_geometry(t, a->k, a->count, a->max_rank).v_bytes;
+    w.bytes = w.v_off + g.v_bytes;
     return w;
 }
 
@@ -265,7 +267,7 @@ extern "C" uw_status uw_lora_add(const uint16_t *x_dev, int64_t x_stride, int64_
         if (!apart && !columns) return UW_ERR_INVALID_ARG;
     }
     const LoraWorkspace w = lora_workspace(t, adapters);
-    if (!ws || ws_bytes < w.bytes || !aligned(ws, 256)) return UW_ERR_WORKSPACE;
+    if (w.bytes && (!ws || ws_bytes < w.bytes || !aligned(ws, 256))) return UW_ERR_WORKSPACE;
     uint8_t *base = static_cast<uint8_t *>(ws);
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     const bool ungrouped = ids_dev && t <= kLoraUngrouped;
@@ -302,7 +304,7 @@ extern "C" uw_status uw_lora_add(const uint16_t *x_dev, int64_t x_stride, int64_
     p.y_stride = y_stride;
     p.out = out_dev;
     p.out_stride = out_stride;
-    p.v = reinterpret_cast<float *>(base + w.v_off);
+    p.v = w.bytes ? reinterpret_cast<float *>(base + w.v_off) : nullptr;
     return cuda_status(launch_lora(p, s));
 }
 

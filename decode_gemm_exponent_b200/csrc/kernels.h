@@ -253,7 +253,9 @@ cudaError_t launch_route(const RouteLaunch &p, cudaStream_t stream);
 // Low-rank adapters beside a projection (lora.cu): out = y + scale * B (A x)
 // per row of an adapter's group.  v: [splits][t][max_rank] floats.
 constexpr int64_t kLoraUngrouped = 32;   // up to so many rows a warp groups for itself
+constexpr int64_t kLoraFew = 32;         // up to so many rows one launch does it all
 struct LoraGeometry {
+    bool few = false;          // one launch: a cluster of `splits` CTAs per row tile, no workspace
     int splits = 1;            // slices of K
     int token_tiles = 1;       // 8-token tiles of the first product's tile: 1 or 4
     int rank_tiles = 1;        // 16-rank tiles per CTA of the first product: 1 or 2

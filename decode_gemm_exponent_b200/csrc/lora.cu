@@ -5,8 +5,9 @@
 // through.
 //
 // Rows come grouped by adapter (offsets and order of a stable counting sort),
-// so a tile of rows reads one adapter's matrices.  Two launches: the inner
-// product over all of K must be complete before the outer one starts.
+// so a tile of rows reads one adapter's matrices.  The inner product over all of K
+// must be complete before the outer one starts: two launches, or, for few rows, the
+// barrier of a cluster.
 //
 // First product, V = A x: warp-level MMA (m16n8k16) with the ranks as M and the
 // tokens as N.  Both operands are K-contiguous, so every lane loads 32
@@ -63,6 +64,7 @@ struct LoraArgs {
     int wide;                  // rows of out are 32-byte aligned
     int copy_rest;             // rows without an adapter are copied (out is not y)
     int steps;                 // second product: 32-column steps per warp
+    int cols;                  // few rows: clusters per row tile
 };
 
 struct Tile {
@@ -265,46 +267,46 @@ __device__ __forceinline__ void split3(float v, uint32_t (&p)[3]) {
     p[2] = bf16_bits((v - h) - __uint_as_float(p[1] << 16));
 }
 
-// C: 16-rank chunks whose B loads are in flight together; MT: 16-row parts of a
-// tile, which share the loads of B.  Fragments of V: [part][chunk][piece][lane].
-template <int C, int MT>
-__global__ void __launch_bounds__(kExpandWarps * 32, C == 4 ? 3 : 4) k_lora_expand(const LoraArgs a) {
-    // dynamic shared memory: y on its way, then the fragments of V
-    extern __shared__ uint4 s_dyn[];
-    __shared__ Tile s_tile;
-    __shared__ int32_t s_row[16 * MT];       // rows of the tile, -1: none
-    // y on its way, a ring of units (16 rows of 128 bytes) per warp: eight lanes copy
-    // a row, so that every request is a whole line; the 16-byte pieces of odd rows
-    // are swapped in pairs to keep the reads free of bank conflicts
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
-    uint8_t *s_y = reinterpret_cast<uint8_t *>(s_dyn) + warp * kAhead * kUnit;
-    uint4 *s_frag = s_dyn + kExpandSmem / 16;
-    if (warp == 0) {
-        const Tile f = find_tile(a, 16 * MT, blockIdx.x, a.copy_rest != 0, s_row);
-        if (lane == 0) s_tile = f;
-    }
-    __syncthreads();
-    const Tile tile = s_tile;
-    const int rank = tile.group < 0 ? 0 : rank_of(a, tile.group);
-    if (tile.group < 0 || (rank == 0 && !a.copy_rest)) {
-        pdl_wait();   // no CTA ends before the kernels that this one stands behind
-        return;
-    }
-    const int chunks = (rank + 15) / 16;
+// One warp's share of the second product: columns n0 + 32 W s for its steps s, of a
+// tile of MT parts of 16 rows, whose loads of B the parts share; C: 16-rank chunks
+// whose B loads are in flight together; W: warps that take neighbouring columns.
+template <int W, int C, int MT>
+struct Expand {
+    static constexpr int kStride = W * 32;
+    const LoraArgs &a;
+    const int32_t *s_row;      // the tile's rows, -1: none
+    const uint4 *s_frag;       // fragments of V: [part][chunk][piece][lane]
+    // y on its way, a ring of units (16 rows of 128 bytes): eight lanes copy a row, so
+    // that every request is a whole line; the 16-byte pieces of odd rows are swapped
+    // in pairs to keep the reads free of bank conflicts
+    uint8_t *s_y;
+    int rank, chunks, steps, parts;
+    int64_t n0;
+    const uint16_t *pb;
+    int fetch_part = 0, fetch_slot = 0, left, slot = 0;
+    int64_t fetch_n;
+    uint2 w[C][4];
 
-    // the CTA's warps take neighbouring columns, kStride of them per step
-    constexpr int kStride = kExpandWarps * 32;
-    const int64_t n0 = int64_t(blockIdx.y) * a.steps * kStride + warp * 32;
-    const int steps = int(max(int64_t(0), min(int64_t(a.steps), (a.n - n0 + kStride - 32) / kStride)));
-    const int parts = (tile.rows + 15) / 16;           // of this tile, <= MT
-    const int units = steps * parts;
-    // column tile q, MMA column j is output column 8 (j / 2) + 2 q + j % 2 of the step's
-    // 32: a thread owns eight consecutive columns, a row's four lanes a whole line
-    const uint16_t *pb = a.b + (int64_t(min(tile.group, a.groups - 1)) * a.n + n0 + 8 * (g >> 1) + (g & 1)) * a.max_rank + 4 * c;
+    __device__ __forceinline__ Expand(const LoraArgs &args, const Tile &tile, int tile_rank, int64_t block, uint8_t *ring,
+                                      const uint4 *frag, const int32_t *rows)
+        : a(args), s_row(rows), s_frag(frag), rank(tile_rank) {
+        const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+        s_y = ring + warp * kAhead * kUnit;
+        chunks = (rank + 15) / 16;
+        n0 = block * a.steps * kStride + warp * 32;
+        steps = int(max(int64_t(0), min(int64_t(a.steps), (a.n - n0 + kStride - 32) / kStride)));
+        parts = (tile.rows + 15) / 16;
+        left = steps * parts;
+        fetch_n = n0 + 4 * (lane & 7);
+        // column tile q, MMA column j is output column 8 (j / 2) + 2 q + j % 2 of the step's
+        // 32: a thread owns eight consecutive columns, a row's four lanes a whole line
+        pb = a.b + (int64_t(min(tile.group, a.groups - 1)) * a.n + n0 + 8 * (g >> 1) + (g & 1)) * a.max_rank + 4 * c;
+    }
 
     // B of chunks [j0, j0 + C) for the step at column offset `n`; ranks past the
     // adapter's are zeroed, whatever its storage holds there
-    auto load_b = [&](uint2 (&w)[C][4], int64_t n, int j0) {
+    __device__ __forceinline__ void load_b(int64_t n, int j0) {
+        const int c = threadIdx.x & 3;
 #pragma unroll
         for (int j = 0; j < C; j++) {
             const int r = 16 * (j0 + j) + 4 * c;
@@ -314,19 +316,19 @@ __global__ void __launch_bounds__(kExpandWarps * 32, C == 4 ? 3 : 4) k_lora_expa
                 if (r < rank) {
                     w[j][q] = __ldg(reinterpret_cast<const uint2 *>(pb + (n + 2 * q) * a.max_rank + 16 * (j0 + j)));
                     if (r + 4 > rank) {
-                        const int left = rank - r;     // 1, 2 or 3 ranks
-                        if (left < 2) w[j][q].x &= 0xFFFFu;
-                        w[j][q].y = left < 3 ? 0u : w[j][q].y & 0xFFFFu;
+                        const int some = rank - r;     // 1, 2 or 3 ranks
+                        if (some < 2) w[j][q].x &= 0xFFFFu;
+                        w[j][q].y = some < 3 ? 0u : w[j][q].y & 0xFFFFu;
                     }
                 }
             }
         }
-    };
-    // units of 16 rows x 32 columns, the parts of a step one after the other
-    int fetch_part = 0, fetch_slot = 0, fetched = 0;
-    int64_t fetch_n = n0 + 4 * (lane & 7);
-    auto fetch_y = [&]() {
-        if (fetched < units) {
+    }
+
+    // the next unit of y, the parts of a step one after the other
+    __device__ __forceinline__ void fetch_y() {
+        const int lane = threadIdx.x & 31;
+        if (left > 0) {
 #pragma unroll
             for (int i = 0; i < 4; i++) {
                 const int row = 4 * i + (lane >> 3);
@@ -335,7 +337,7 @@ __global__ void __launch_bounds__(kExpandWarps * 32, C == 4 ? 3 : 4) k_lora_expa
                     cp_async16(s_y + fetch_slot * kUnit + row * 128 + (((lane & 7) ^ (row & 1)) << 4),
                                a.y + r * a.y_stride + fetch_n);
             }
-            fetched++;
+            left--;
             fetch_slot = fetch_slot + 1 == kAhead ? 0 : fetch_slot + 1;
             if (++fetch_part == parts) {
                 fetch_part = 0;
@@ -343,54 +345,18 @@ __global__ void __launch_bounds__(kExpandWarps * 32, C == 4 ? 3 : 4) k_lora_expa
             }
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
-    };
-    uint2 w[C][4];
-    if (steps > 0) load_b(w, 0, 0);
-#pragma unroll
-    for (int s = 0; s < kAhead - 1; s++) fetch_y();
-
-    pdl_wait();   // V is the previous kernel's; everything read so far is older
-    // fragments: lane (g, c) holds ranks 16 j + 4 c .. + 3 of rows g and g + 8 of a part
-    const float scale = a.scales && rank ? __ldg(a.scales + tile.group) : 1.f;
-    for (int u = threadIdx.x; u < parts * chunks * 32; u += kExpandWarps * 32) {
-        const int l = u & 31, j = (u >> 5) % chunks, part = (u >> 5) / chunks, r = 16 * j + 4 * (l & 3);
-        uint32_t piece[3][4];
-#pragma unroll
-        for (int h = 0; h < 2; h++) {
-            const int m = 16 * part + (l >> 2) + 8 * h;
-            float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (m < tile.rows && r < rank) {
-                const float *pv = a.v + int64_t(tile.pos + m) * a.max_rank + r;
-                s = __ldcg(reinterpret_cast<const float4 *>(pv));
-#pragma unroll 4
-                for (int z = 1; z < a.splits; z++) {
-                    const float4 o = __ldcg(reinterpret_cast<const float4 *>(pv + int64_t(z) * a.t * a.max_rank));
-                    s.x += o.x;
-                    s.y += o.y;
-                    s.z += o.z;
-                    s.w += o.w;
-                }
-            }
-            const float v[4] = {s.x * scale, r + 1 < rank ? s.y * scale : 0.f, r + 2 < rank ? s.z * scale : 0.f,
-                                r + 3 < rank ? s.w * scale : 0.f};
-            uint32_t p[4][3];
-#pragma unroll
-            for (int i = 0; i < 4; i++) split3(v[i], p[i]);
-#pragma unroll
-            for (int z = 0; z < 3; z++) {
-                piece[z][h] = p[0][z] | p[1][z] << 16;          // K slots 2 c, 2 c + 1
-                piece[z][2 + h] = p[2][z] | p[3][z] << 16;      // K slots 2 c + 8, 2 c + 9
-            }
-        }
-#pragma unroll
-        for (int z = 0; z < 3; z++)
-            s_frag[((part * chunks + j) * 3 + z) * 32 + l] = make_uint4(piece[z][0], piece[z][1], piece[z][2], piece[z][3]);
     }
-    __syncthreads();
 
-    int slot = 0;
+    // the first loads of B and y
+    __device__ __forceinline__ void prefetch() {
+        if (steps > 0) load_b(0, 0);
+#pragma unroll
+        for (int s = 0; s < kAhead - 1; s++) fetch_y();
+    }
+
     // adds unit (n, part)'s y and stores it
-    auto finish = [&](const float (&d)[4][4], int64_t n, int part) {
+    __device__ __forceinline__ void finish(const float (&d)[4][4], int64_t n, int part) {
+        const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
         fetch_y();
         asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory");
         __syncwarp();
@@ -414,53 +380,253 @@ __global__ void __launch_bounds__(kExpandWarps * 32, C == 4 ? 3 : 4) k_lora_expa
         }
         __syncwarp();   // the slot is written again by a later fetch
         slot = slot + 1 == kAhead ? 0 : slot + 1;
-    };
-    for (int s = 0; s < steps; s++) {
-        const int64_t n = int64_t(s) * kStride;
-        if (chunks <= C) {
-            // all ranks' B in registers: it serves every part, and the next step's
-            // comes in meanwhile
-            uint2 cur[C][4];
+    }
+
+    __device__ __forceinline__ void chunk(float (&d)[4][4], const uint2 (&b)[4], int part, int j) const {
 #pragma unroll
-            for (int j = 0; j < C; j++)
+        for (int z = 2; z >= 0; z--) {     // smallest piece first
+            const uint4 f = s_frag[((part * chunks + j) * 3 + z) * 32 + (threadIdx.x & 31)];
 #pragma unroll
-                for (int q = 0; q < 4; q++) cur[j][q] = w[j][q];
-            if (s + 1 < steps) load_b(w, n + kStride, 0);
-            for (int part = 0; part < parts; part++) {
-                float d[4][4] = {};
-#pragma unroll
-                for (int j = 0; j < C; j++) {
-                    if (j >= chunks) break;
-#pragma unroll
-                    for (int z = 2; z >= 0; z--) {     // smallest piece first
-                        const uint4 f = s_frag[((part * chunks + j) * 3 + z) * 32 + lane];
-#pragma unroll
-                        for (int q = 0; q < 4; q++) mma_16816(d[q], f.x, f.y, f.z, f.w, cur[j][q].x, cur[j][q].y);
-                    }
-                }
-                finish(d, n, part);
-            }
-        } else {
-            for (int part = 0; part < parts; part++) {
-                float d[4][4] = {};
-                for (int j0 = 0; j0 < chunks; j0 += C) {
-                    load_b(w, n, j0);
-#pragma unroll
-                    for (int j = 0; j < C; j++) {
-                        if (j0 + j >= chunks) break;
-#pragma unroll
-                        for (int z = 2; z >= 0; z--) {
-                            const uint4 f = s_frag[((part * chunks + j0 + j) * 3 + z) * 32 + lane];
-#pragma unroll
-                            for (int q = 0; q < 4; q++) mma_16816(d[q], f.x, f.y, f.z, f.w, w[j][q].x, w[j][q].y);
-                        }
-                    }
-                }
-                finish(d, n, part);
-            }
+            for (int q = 0; q < 4; q++) mma_16816(d[q], f.x, f.y, f.z, f.w, b[q].x, b[q].y);
         }
     }
-    asm volatile("cp.async.wait_all;" ::: "memory");
+
+    __device__ __forceinline__ void run() {
+        for (int s = 0; s < steps; s++) {
+            const int64_t n = int64_t(s) * kStride;
+            if (chunks <= C) {
+                // all ranks' B in registers: it serves every part, and the next step's
+                // comes in meanwhile
+                uint2 cur[C][4];
+#pragma unroll
+                for (int j = 0; j < C; j++)
+#pragma unroll
+                    for (int q = 0; q < 4; q++) cur[j][q] = w[j][q];
+                if (s + 1 < steps) load_b(n + kStride, 0);
+                for (int part = 0; part < parts; part++) {
+                    float d[4][4] = {};
+#pragma unroll
+                    for (int j = 0; j < C; j++) {
+                        if (j >= chunks) break;
+                        chunk(d, cur[j], part, j);
+                    }
+                    finish(d, n, part);
+                }
+            } else {
+                for (int part = 0; part < parts; part++) {
+                    float d[4][4] = {};
+                    for (int j0 = 0; j0 < chunks; j0 += C) {
+                        load_b(n, j0);
+#pragma unroll
+                        for (int j = 0; j < C; j++) {
+                            if (j0 + j >= chunks) break;
+                            chunk(d, w[j], part, j0 + j);
+                        }
+                    }
+                    finish(d, n, part);
+                }
+            }
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+    }
+};
+
+// The fragments of one lane's V: ranks r .. r + 3 (those below `rank`) of two rows.
+__device__ __forceinline__ void put_fragment(uint4 *frag, const float4 (&v)[2], float scale, int r, int rank) {
+    uint32_t piece[3][4];
+#pragma unroll
+    for (int h = 0; h < 2; h++) {
+        const float x[4] = {r < rank ? v[h].x * scale : 0.f, r + 1 < rank ? v[h].y * scale : 0.f,
+                            r + 2 < rank ? v[h].z * scale : 0.f, r + 3 < rank ? v[h].w * scale : 0.f};
+        uint32_t p[4][3];
+#pragma unroll
+        for (int i = 0; i < 4; i++) split3(x[i], p[i]);
+#pragma unroll
+        for (int z = 0; z < 3; z++) {
+            piece[z][h] = p[0][z] | p[1][z] << 16;          // K slots 2 c, 2 c + 1
+            piece[z][2 + h] = p[2][z] | p[3][z] << 16;      // K slots 2 c + 8, 2 c + 9
+        }
+    }
+#pragma unroll
+    for (int z = 0; z < 3; z++) frag[z * 32] = make_uint4(piece[z][0], piece[z][1], piece[z][2], piece[z][3]);
+}
+
+__device__ __forceinline__ void add4(float4 &s, const float4 &o) {
+    s.x += o.x;
+    s.y += o.y;
+    s.z += o.z;
+    s.w += o.w;
+}
+
+template <int C, int MT>
+__global__ void __launch_bounds__(kExpandWarps * 32, C == 4 ? 3 : 4) k_lora_expand(const LoraArgs a) {
+    // dynamic shared memory: y on its way, then the fragments of V
+    extern __shared__ uint4 s_dyn[];
+    __shared__ Tile s_tile;
+    __shared__ int32_t s_row[16 * MT];
+    uint4 *s_frag = s_dyn + kExpandSmem / 16;
+    if (threadIdx.x < 32) {
+        const Tile f = find_tile(a, 16 * MT, blockIdx.x, a.copy_rest != 0, s_row);
+        if (threadIdx.x == 0) s_tile = f;
+    }
+    __syncthreads();
+    const Tile tile = s_tile;
+    const int rank = tile.group < 0 ? 0 : rank_of(a, tile.group);
+    if (tile.group < 0 || (rank == 0 && !a.copy_rest)) {
+        pdl_wait();   // no CTA ends before the kernels that this one stands behind
+        return;
+    }
+    Expand<kExpandWarps, C, MT> e(a, tile, rank, blockIdx.y, reinterpret_cast<uint8_t *>(s_dyn), s_frag, s_row);
+    e.prefetch();
+
+    pdl_wait();   // V is the previous kernel's; everything read so far is older
+    // fragments: lane (g, c) holds ranks 16 j + 4 c .. + 3 of rows g and g + 8 of a part
+    const float scale = a.scales && rank ? __ldg(a.scales + tile.group) : 1.f;
+    for (int u = threadIdx.x; u < e.parts * e.chunks * 32; u += kExpandWarps * 32) {
+        const int l = u & 31, j = (u >> 5) % e.chunks, part = (u >> 5) / e.chunks, r = 16 * j + 4 * (l & 3);
+        float4 v[2];
+#pragma unroll
+        for (int h = 0; h < 2; h++) {
+            const int m = 16 * part + (l >> 2) + 8 * h;
+            v[h] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (m < tile.rows && r < rank) {
+                const float *pv = a.v + int64_t(tile.pos + m) * a.max_rank + r;
+                v[h] = __ldcg(reinterpret_cast<const float4 *>(pv));
+#pragma unroll 4
+                for (int z = 1; z < a.splits; z++)
+                    add4(v[h], __ldcg(reinterpret_cast<const float4 *>(pv + int64_t(z) * a.t * a.max_rank)));
+            }
+        }
+        put_fragment(s_frag + (part * e.chunks + j) * 96 + l, v, scale, r, rank);
+    }
+    __syncthreads();
+    e.run();
+}
+
+// ---------------------------------------------------------------- few rows: both products in one launch
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+
+// 16 bytes of another CTA's shared memory, at the address that `p` has in this one
+__device__ __forceinline__ float4 peer_load(const float4 *p, uint32_t cta) {
+    float4 v;
+    asm volatile(
+        "{ .reg .b32 q; mapa.shared::cluster.u32 q, %4, %5; ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [q]; }"
+        : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+        : "r"(smem_addr(p)), "r"(cta)
+        : "memory");
+    return v;
+}
+
+// Up to kLoraFew rows: a cluster of CTAs per tile of eight rows of one adapter.  The
+// CTAs split K for the first product (every warp a slice of its own), add their
+// pieces of V through distributed shared memory in CTA order, and split the columns
+// for the second.  B and y are on their way while the first product runs.  Bound by
+// latency: one launch, and one trip to memory for A and x.
+constexpr int kFewWarps = 8;
+template <int C>
+__global__ void __launch_bounds__(kFewWarps * 32, C == 4 ? 1 : 2) k_lora_few(const LoraArgs a) {
+    extern __shared__ uint4 s_dyn[];
+    __shared__ Tile s_tile;
+    __shared__ int32_t s_row[16];
+    __shared__ float s_red[kFewWarps * C * 128];       // C rank tiles of every warp
+    uint8_t *ring = reinterpret_cast<uint8_t *>(s_dyn);
+    const int width = (a.max_rank + 15) / 16 * 16;
+    float *s_v = reinterpret_cast<float *>(ring + size_t(kFewWarps) * kAhead * kUnit);   // [8][width], this CTA's piece
+    uint4 *s_frag = reinterpret_cast<uint4 *>(s_v + 8 * width);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+    const uint32_t ctas = uint32_t(a.splits), cta = cluster_rank();
+    pdl_trigger();
+    pdl_wait();
+    if (warp == 0) {
+        const Tile f = find_tile(a, 8, blockIdx.x / (ctas * uint32_t(a.cols)), a.copy_rest != 0, s_row);
+        if (lane == 0) s_tile = f;
+        if (lane >= 8 && lane < 16) s_row[lane] = -1;
+    }
+    __syncthreads();
+    const Tile tile = s_tile;
+    const int rank = tile.group < 0 ? 0 : rank_of(a, tile.group);
+    if (tile.group < 0 || (rank == 0 && !a.copy_rest)) return;     // the whole cluster alike
+    Expand<kFewWarps, C, 1> e(a, tile, rank, blockIdx.x % (ctas * uint32_t(a.cols)), ring, s_frag, s_row);
+
+    if (rank > 0) {
+        const int64_t steps = a.k / 64, slices = int64_t(ctas) * kFewWarps, mine = int64_t(cta) * kFewWarps + warp;
+        const int64_t k0 = steps * mine / slices, k1 = steps * (mine + 1) / slices;
+        const uint16_t *px = a.x + int64_t(max(s_row[min(g, tile.rows - 1)], 0)) * a.x_stride + 16 * c;
+        const uint16_t *pa = a.a + int64_t(tile.group) * a.max_rank * a.k + 16 * c;
+        for (int i0 = 0; i0 < e.chunks; i0 += C) {
+            float d[C][4] = {};
+#pragma unroll 1
+            for (int64_t s = k0; s < k1; s++) {
+                uint4 xv[2], wa[C][2][2];
+#pragma unroll
+                for (int h = 0; h < 2; h++) xv[h] = __ldg(reinterpret_cast<const uint4 *>(px + s * 64) + h);
+#pragma unroll
+                for (int i = 0; i < C; i++)
+#pragma unroll
+                    for (int m = 0; m < 2; m++) {
+                        // ranks past the slot's storage repeat its last (not used)
+                        const int r = min(16 * (i0 + i) + 8 * m + g, a.max_rank - 1);
+                        if (i0 + i < e.chunks) {
+                            const uint4 *p = reinterpret_cast<const uint4 *>(pa + int64_t(r) * a.k + s * 64);
+                            wa[i][m][0] = __ldg(p);
+                            wa[i][m][1] = __ldg(p + 1);
+                        }
+                    }
+                if (i0 == 0 && s == k0) e.prefetch();     // behind the first loads of A and x
+#pragma unroll
+                for (int i = 0; i < C; i++)
+                    if (i0 + i < e.chunks) {
+#pragma unroll
+                        for (int h = 0; h < 2; h++) {
+                            mma_16816(d[i], wa[i][0][h].x, wa[i][1][h].x, wa[i][0][h].y, wa[i][1][h].y, xv[h].x, xv[h].y);
+                            mma_16816(d[i], wa[i][0][h].z, wa[i][1][h].z, wa[i][0][h].w, wa[i][1][h].w, xv[h].z, xv[h].w);
+                        }
+                    }
+            }
+            if (i0 == 0 && k0 >= k1) e.prefetch();
+#pragma unroll
+            for (int i = 0; i < C; i++)
+#pragma unroll
+                for (int q = 0; q < 4; q++) s_red[((warp * C + i) * 4 + q) * 32 + lane] = d[i][q];
+            __syncthreads();
+            for (int u = threadIdx.x; u < C * 128; u += kFewWarps * 32) {
+                const int l = u & 31, q = (u >> 5) & 3, i = u >> 7;
+                if (i0 + i >= e.chunks) continue;
+                float sum = s_red[u];
+#pragma unroll
+                for (int w = 1; w < kFewWarps; w++) sum += s_red[w * C * 128 + u];
+                s_v[(2 * (l & 3) + (q & 1)) * width + 16 * (i0 + i) + (l >> 2) + (q >= 2 ? 8 : 0)] = sum;
+            }
+            __syncthreads();
+        }
+        cluster_arrive();
+        cluster_wait();
+        const float scale = a.scales ? __ldg(a.scales + tile.group) : 1.f;
+        for (int u = threadIdx.x; u < e.chunks * 32; u += kFewWarps * 32) {
+            const int l = u & 31, j = u >> 5, r = 16 * j + 4 * (l & 3);
+            float4 v[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
+            if ((l >> 2) < tile.rows && r < rank) {
+                const float4 *pv = reinterpret_cast<const float4 *>(s_v + (l >> 2) * width + r);
+                v[0] = peer_load(pv, 0);
+#pragma unroll 8
+                for (uint32_t z = 1; z < ctas; z++) add4(v[0], peer_load(pv, z));
+            }
+            put_fragment(s_frag + j * 96 + l, v, scale, r, rank);
+        }
+        cluster_arrive();    // this CTA has read the others' pieces
+        __syncthreads();
+    } else {
+        e.prefetch();
+    }
+    e.run();
+    if (rank > 0) cluster_wait();   // none ends while another may still read its piece
 }
 
 // most tiles of `size` rows that t rows in at most `groups` groups can make
@@ -468,10 +634,40 @@ int64_t most_tiles(int64_t t, int64_t groups, int64_t size) {
     return (t + (size - 1) * std::min(groups, t)) / size;
 }
 
+template <int C>
+cudaError_t launch_few(const LoraArgs &a, const LoraGeometry &geo, size_t smem, cudaStream_t stream) {
+    static std::atomic<uint64_t> allowed{0};
+    cudaError_t err = allow_smem(k_lora_few<C>, size_t(kFewWarps) * kAhead * kUnit + 16 * (8 * 16 * 4 + 3 * 32 * 16), allowed);
+    if (err != cudaSuccess) return err;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(unsigned(geo.expand_tiles * a.cols * geo.splits));
+    cfg.blockDim = dim3(kFewWarps * 32);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = unsigned(geo.splits);
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    err = cudaLaunchKernelEx(&cfg, k_lora_few<C>, a);
+    return err != cudaSuccess ? err : cudaGetLastError();
+}
+
 }  // namespace
 
 LoraGeometry lora_geometry(int64_t t, int64_t k, int groups, int max_rank) {
     LoraGeometry g;
+    // One launch for few rows; chains of at most 512 of K in its 8 x 8 slices or more.
+    if (t <= kLoraFew && k <= 512 * 64) {
+        g.few = true;
+        g.shrink_tiles = g.expand_tiles = most_tiles(t, groups + 1, 8);
+        g.splits = 8;
+        return g;
+    }
     // tiles of 32 tokens reuse A's fragments four times where rows per adapter
     // are many; single tokens would only repeat themselves in them
     g.token_tiles = t >= 16 * int64_t(groups) && t >= 64 ? 4 : 1;
@@ -514,6 +710,18 @@ cudaError_t launch_lora(const LoraLaunch &p, cudaStream_t stream) {
     a.out = p.out;
     a.out_stride = p.out_stride;
     a.copy_rest = p.out != p.y;
+    if (geo.few) {
+        const int64_t units = (p.n + kFewWarps * 32 - 1) / (kFewWarps * 32);
+        // several clusters per tile, each with the whole first product, where one would
+        // leave SMs idle and its CTAs a long stretch of columns
+        const int64_t clusters = std::max<int64_t>(1, std::min(2 * 148 / (geo.expand_tiles * geo.splits), (units + geo.splits - 1) / geo.splits));
+        a.cols = int(clusters);
+        a.steps = int((units + geo.splits * clusters - 1) / (geo.splits * clusters));
+        const int ranks = (p.max_rank + 15) / 16;
+        const size_t smem = size_t(kFewWarps) * kAhead * kUnit + size_t(ranks) * (8 * 16 * 4 + 3 * 32 * 16);
+        return ranks == 1 ? launch_few<1>(a, geo, smem, stream)
+                          : ranks == 2 ? launch_few<2>(a, geo, smem, stream) : launch_few<4>(a, geo, smem, stream);
+    }
     a.wide = ((reinterpret_cast<uintptr_t>(p.out) | uintptr_t(p.out_stride) * 4) & 31u) == 0;
     const int rt = (p.max_rank + 15) / 16;
     const dim3 grid1(unsigned(geo.shrink_tiles), unsigned(geo.splits), unsigned((rt + geo.rank_tiles - 1) / geo.rank_tiles));

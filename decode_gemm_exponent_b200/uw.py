@@ -853,10 +853,13 @@ def lora_add(x, a, b, ids, y, *, ranks=None, scales=None, groups: Optional[Group
     if out is None:
         out = torch.empty(t, n, dtype=torch.float32, device=x.device)
     if ws is None:
-        ws = torch.empty(max(lora_workspace_size(t, k, n, count, rank), 1), dtype=torch.uint8, device=x.device)
+        nbytes = lora_workspace_size(t, k, n, count, rank)
+        if nbytes:
+            ws = torch.empty(nbytes, dtype=torch.uint8, device=x.device)
     check(lib().uw_lora_add(_need(x, "x", (t, k), bf16, dev, True), _stride(x), t, d, ids, offsets, order,
                             _need(y, "y", (t, n), f32, dev, True), _stride(y), _need(out, "out", (t, n), f32, dev, True),
-                            _stride(out), ws.data_ptr(), ws.numel(), _handle(dev)), "uw_lora_add")
+                            _stride(out), None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel(),
+                            _handle(dev)), "uw_lora_add")
     return out
 
 

@@ -648,7 +648,8 @@ typedef struct uw_adapters {
  * itself) or, with ids_dev NULL, by offsets_dev and order_dev as uw_group_rows wrote
  * them for per_row = 1 and groups = count, so that the projections of a step share
  * one grouping.  The inner product is summed and kept in 32 bits.
- * ws: >= uw_lora_workspace_size bytes, 256-byte aligned; its contents do not matter.
+ * ws: >= uw_lora_workspace_size bytes (0 for few rows), 256-byte aligned; its
+ * contents do not matter.
  * t >= 0; t = 0 launches nothing.                                                  */
 uw_status uw_lora_workspace_size(int64_t t, const uw_adapters *adapters, size_t *bytes);
 uw_status uw_lora_add(const uint16_t *x_dev, int64_t x_stride, int64_t t, const uw_adapters *adapters,

@@ -65,7 +65,7 @@ def check(got, want, bound):
 
 
 @pytest.mark.parametrize("t,k,n,count,rank", [
-    (1, 64, 64, 1, 8), (1, 4096, 1024, 8, 64), (2, 128, 192, 3, 16), (17, 512, 320, 40, 24), (32, 4096, 512, 48, 16),
+    (1, 64, 64, 1, 8), (1, 4096, 1024, 8, 64), (1, 4096, 14336, 3, 256), (3, 65536, 128, 2, 16), (31, 640, 2048, 1, 72), (32, 192, 320, 40, 8), (2, 128, 192, 3, 16), (17, 512, 320, 40, 24), (32, 4096, 512, 48, 16),
     (64, 1024, 256, 2, 8), (65, 1024, 256, 3, 32), (333, 2048, 448, 5, 40), (130, 14336, 128, 4, 64), (300, 192, 640, 1, 256),
     (1000, 256, 64, 1000, 8)])
 def test_against_float64(uw, t, k, n, count, rank):
@@ -179,7 +179,7 @@ def test_beside_a_compressed_projection(uw):
     plan = uw.make_plan(uw.PIPE_DIRECT_PALETTE, uw.KERNEL_MMA, 4)
     groups = uw.group_rows(ids, 5)
     y = torch.empty(m, n, device="cuda")
-    ws = uw.new_workspace(uw.lora_workspace_size(m, k, n, 5, 16), "cuda")
+    ws = uw.new_workspace(uw.lora_workspace_size(m, k, n, 5, 16), "cuda")     # None: few rows need none
     base = mat.matmul(x.view(torch.int16), plan)
     want, bound = plain(x, a, b, ids, base, ranks, scales)
     for _ in range(20):
@@ -190,7 +190,7 @@ def test_beside_a_compressed_projection(uw):
 
 
 def test_refusals(uw):
-    x, a, b, ids, y, ranks, scales = make(8, 128, 128, 2, 16, 2)
+    x, a, b, ids, y, ranks, scales = make(48, 128, 128, 2, 16, 2)
     for args, kw in (((x.float(), a, b, ids, y), {}), ((x, a[:, :, :64], b, ids, y), {}), ((x, a, b[:1], ids, y), {}),
                      ((x, a, b, ids.long(), y), {}), ((x, a, b, ids[:4], y), {}), ((x, a, b, ids, y.double()), {}),
                      ((x, a, b, ids, y), dict(ranks=ranks.long())), ((x, a, b, ids, y), dict(scales=scales.cpu())),
@@ -206,6 +206,6 @@ def test_refusals(uw):
     with pytest.raises(uw.UwError) as e:
         uw.lora_add(x, a, b, ids, y, ws=torch.empty(256, dtype=torch.uint8, device="cuda"))
     assert e.value.status == uw.ERR_WORKSPACE
-    wide = torch.zeros(8, 256, device="cuda")
+    wide = torch.zeros(48, 256, device="cuda")
     with pytest.raises(uw.UwError):            # result overlaps the input
         uw.lora_add(x, a, b, ids, wide[:, :128], out=wide[:, 64:192])

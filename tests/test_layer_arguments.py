@@ -77,9 +77,11 @@ def test_lora(uw):
         assert L.uw_lora_workspace_size(8, ctypes.byref(adapters(**kw)), ctypes.byref(size)) == status, kw
     assert L.uw_lora_workspace_size(-1, ctypes.byref(adapters()), ctypes.byref(size)) == 1
     assert L.uw_lora_workspace_size(0, ctypes.byref(adapters()), ctypes.byref(size)) == 0 and size.value == 0
-    assert L.uw_lora_workspace_size(8, ctypes.byref(adapters()), ctypes.byref(size)) == 0 and size.value > 0
+    assert L.uw_lora_workspace_size(8, ctypes.byref(adapters()), ctypes.byref(size)) == 0 and size.value == 0    # one launch
+    assert L.uw_lora_workspace_size(8, ctypes.byref(adapters(k=65536)), ctypes.byref(size)) == 0 and size.value > 0
+    assert L.uw_lora_workspace_size(80, ctypes.byref(adapters()), ctypes.byref(size)) == 0 and size.value > 0
 
-    def run(d=None, x=FAKE, xs=256, t=8, ids=FAKE, off=None, order=None, y=FAKE, ys=128, out=FAKE, os_=128, ws=FAKE,
+    def run(d=None, x=FAKE, xs=256, t=80, ids=FAKE, off=None, order=None, y=FAKE, ys=128, out=FAKE, os_=128, ws=FAKE,
             nbytes=1 << 30):
         d = d or adapters()
         return L.uw_lora_add(x, xs, t, ctypes.byref(d), ids, off, order, y, ys, out, os_, ws, nbytes, None)
