@@ -249,22 +249,26 @@ __global__ void __launch_bounds__(kShrinkWarps * 32, 2) k_lora_shrink(const Lora
 
 // ---------------------------------------------------------------- out = y + V B^T
 
-__device__ __forceinline__ uint32_t bf16_bits(float f) {   // round to nearest even; f is finite or inf
+__device__ __forceinline__ uint32_t bf16_bits(float f) {   // round to nearest even; f is finite
     uint32_t o;
     asm("{ .reg .b16 h; cvt.rn.bf16.f32 h, %1; cvt.u32.u16 %0, h; }" : "=r"(o) : "f"(f));
     return o;
 }
 
-// v = p[0] + p[1] + p[2] up to 2^-24 of v, each a BF16
+// v = p[0] + p[1] + p[2], each a BF16.  The first is cut off, not rounded, so that it
+// never exceeds a finite v; 16 bits are left, of which the second rounds to eight,
+// and the third holds the rest.
 __device__ __forceinline__ void split3(float v, uint32_t (&p)[3]) {
-    p[0] = bf16_bits(v);
-    const float h = __uint_as_float(p[0] << 16);
-    if (!(fabsf(h) <= 3.402823466e38f)) {     // inf or NaN: there is no remainder
-        p[1] = p[2] = 0u;
+    const uint32_t bits = __float_as_uint(v);
+    p[0] = bits >> 16;
+    p[1] = p[2] = 0u;
+    if ((bits & 0x7F800000u) == 0x7F800000u) {      // inf or NaN: no remainder; a NaN stays one
+        if (bits & 0x007FFFFFu) p[0] |= 1u;
         return;
     }
-    p[1] = bf16_bits(v - h);
-    p[2] = bf16_bits((v - h) - __uint_as_float(p[1] << 16));
+    const float rest = v - __uint_as_float(p[0] << 16);
+    p[1] = bf16_bits(rest);
+    p[2] = bf16_bits(rest - __uint_as_float(p[1] << 16));
 }
 
 // One warp's share of the second product: columns n0 + 32 W s for its steps s, of a
@@ -710,6 +714,7 @@ cudaError_t launch_lora(const LoraLaunch &p, cudaStream_t stream) {
     a.out = p.out;
     a.out_stride = p.out_stride;
     a.copy_rest = p.out != p.y;
+    a.wide = ((reinterpret_cast<uintptr_t>(p.out) | uintptr_t(p.out_stride) * 4) & 31u) == 0;
     if (geo.few) {
         const int64_t units = (p.n + kFewWarps * 32 - 1) / (kFewWarps * 32);
         // several clusters per tile, each with the whole first product, where one would
@@ -722,7 +727,6 @@ cudaError_t launch_lora(const LoraLaunch &p, cudaStream_t stream) {
         return ranks == 1 ? launch_few<1>(a, geo, smem, stream)
                           : ranks == 2 ? launch_few<2>(a, geo, smem, stream) : launch_few<4>(a, geo, smem, stream);
     }
-    a.wide = ((reinterpret_cast<uintptr_t>(p.out) | uintptr_t(p.out_stride) * 4) & 31u) == 0;
     const int rt = (p.max_rank + 15) / 16;
     const dim3 grid1(unsigned(geo.shrink_tiles), unsigned(geo.splits), unsigned((rt + geo.rank_tiles - 1) / geo.rank_tiles));
     const dim3 block1(kShrinkWarps * 32);

@@ -541,6 +541,15 @@ def _need(t, name, shape, dtypes, dev, rows=False):
     raise ValueError("%s: on %s, expected cuda:%d" % (name, t.device, dev))
 
 
+def _workspace(ws, dev):
+    """Address and bytes of a workspace tensor (or None)."""
+    if ws is None:
+        return None, 0
+    if ws.get_device() != dev or not ws.is_contiguous():
+        raise ValueError("ws: a contiguous tensor on cuda:%d" % dev)
+    return ws.data_ptr(), ws.numel() * ws.element_size()
+
+
 @functools.lru_cache(maxsize=None)
 def _types():
     torch = _torch()
@@ -770,7 +779,7 @@ def _expert_call(fn, name, x, sets, routing, gather, plan, out, dtypes, status, 
     if ws is None and plan.kernel == KERNEL_TC and (plan.sort or a.w_dev is None):
         ws = torch.empty(max(1, _expert_bytes(r, a, len(sets) == 2, plan)), dtype=torch.uint8, device=x.device)
     check(fn(r, *sets, _need(out, "out", (places, n), dtypes, dev, True), out.stride(0) if places > 1 else n, plan,
-             None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel(), status, _handle(dev)), name)
+             *_workspace(ws, dev), status, _handle(dev)), name)
     return out
 
 
@@ -845,6 +854,8 @@ def lora_add(x, a, b, ids, y, *, ranks=None, scales=None, groups: Optional[Group
                  None if ranks is None else _need(ranks, "ranks", (count,), i32, dev),
                  None if scales is None else _need(scales, "scales", (count,), f32, dev))
     if groups is None:
+        if ids is None:
+            raise ValueError("ids or groups must be given")
         ids, offsets, order = _need(ids, "ids", (t,), i32, dev), None, None
     else:
         ids = None
@@ -858,8 +869,7 @@ def lora_add(x, a, b, ids, y, *, ranks=None, scales=None, groups: Optional[Group
             ws = torch.empty(nbytes, dtype=torch.uint8, device=x.device)
     check(lib().uw_lora_add(_need(x, "x", (t, k), bf16, dev, True), _stride(x), t, d, ids, offsets, order,
                             _need(y, "y", (t, n), f32, dev, True), _stride(y), _need(out, "out", (t, n), f32, dev, True),
-                            _stride(out), None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel(),
-                            _handle(dev)), "uw_lora_add")
+                            _stride(out), *_workspace(ws, dev), _handle(dev)), "uw_lora_add")
     return out
 
 

@@ -287,6 +287,9 @@ def test_refusals(uw):
     with pytest.raises(uw.UwError) as err:     # the sorted rows need a workspace
         uw.expert_matmul(x, w, r, gather=True, plan=P(uw.KERNEL_TC, 128, sort=1), ws=torch.empty(512, device="cuda").byte())
     assert err.value.status == uw.ERR_WORKSPACE
+    for ws in (torch.empty(1 << 20, dtype=torch.uint8), torch.empty(1 << 21, dtype=torch.uint8, device="cuda")[::2]):
+        with pytest.raises(ValueError):        # a workspace that the kernel could not use
+            uw.expert_matmul(x, w, r, gather=True, plan=P(uw.KERNEL_TC, 128, sort=1), ws=ws)
     with pytest.raises(uw.UwError):            # one form for both
         uw.expert_gate_up(x, s, w, r)
     other = uw.Matrix(uw.encode(synth.weights_bf16(128, 128, 0.02, 0.0, 1.0, seed=9)))

@@ -67,7 +67,7 @@ def check(got, want, bound):
 @pytest.mark.parametrize("t,k,n,count,rank", [
     (1, 64, 64, 1, 8), (1, 4096, 1024, 8, 64), (1, 4096, 14336, 3, 256), (3, 65536, 128, 2, 16), (31, 640, 2048, 1, 72), (32, 192, 320, 40, 8), (2, 128, 192, 3, 16), (17, 512, 320, 40, 24), (32, 4096, 512, 48, 16),
     (64, 1024, 256, 2, 8), (65, 1024, 256, 3, 32), (333, 2048, 448, 5, 40), (130, 14336, 128, 4, 64), (300, 192, 640, 1, 256),
-    (1000, 256, 64, 1000, 8)])
+    (1000, 256, 64, 1000, 8), (1024, 128, 128, 1024, 8), (1025, 128, 128, 7, 16), (900, 192, 64, 1, 24), (33, 4096, 512, 64, 16)])
 def test_against_float64(uw, t, k, n, count, rank):
     x, a, b, ids, y, ranks, scales = make(t, k, n, count, rank, t + k + n)
     want, bound = plain(x, a, b, ids, y, ranks, scales)
@@ -146,6 +146,21 @@ def test_infinite_activations_reach_their_row_only(uw):
     assert not bool(got[7].isfinite().any()) and bool(got[9].isnan().all())
 
 
+@pytest.mark.parametrize("t", [3, 100])
+def test_inner_products_near_the_largest_float(uw, t):
+    """A x just above the largest BF16, which rounding to BF16 would make infinite."""
+    x, a, b, _, y, _, _ = make(t, 128, 64, 1, 8, 13)
+    ids = torch.zeros(t, dtype=torch.int32, device="cuda")
+    top = torch.finfo(torch.bfloat16).max                     # (2 - 2^-7) 2^127
+    x.zero_(), a.zero_(), y.zero_(), b.zero_()
+    x[:, 0], x[:, 1] = top, 2.0 ** 119                        # the sum is half way to 2^128
+    a[0, 0, :2] = 1.0
+    b[0, :, 0] = 2.0 ** -100
+    got = uw.lora_add(x, a, b, ids, y)
+    want = (top + 2.0 ** 119) * 2.0 ** -100                   # every sum and piece is exact
+    assert bool((got.double() == want).all())
+
+
 def test_another_stream_and_a_replayed_graph(uw):
     x, a, b, ids, y, ranks, scales = make(100, 256, 192, 6, 16, 77)
     want = uw.lora_add(x, a, b, ids, y, ranks=ranks, scales=scales)
@@ -194,7 +209,8 @@ def test_refusals(uw):
     for args, kw in (((x.float(), a, b, ids, y), {}), ((x, a[:, :, :64], b, ids, y), {}), ((x, a, b[:1], ids, y), {}),
                      ((x, a, b, ids.long(), y), {}), ((x, a, b, ids[:4], y), {}), ((x, a, b, ids, y.double()), {}),
                      ((x, a, b, ids, y), dict(ranks=ranks.long())), ((x, a, b, ids, y), dict(scales=scales.cpu())),
-                     ((x, a, b, ids, y.T.contiguous().T), {}), ((x, a, b, ids, y), dict(out=y[:4]))):
+                     ((x, a, b, ids, y.T.contiguous().T), {}), ((x, a, b, ids, y), dict(out=y[:4])),
+                     ((x, a, b, None, y), {}), ((x, a, b, ids, y), dict(ws=torch.empty(1 << 20, dtype=torch.uint8)))):
         with pytest.raises(ValueError):
             uw.lora_add(*args, **kw)
     with pytest.raises(uw.UwError) as e:       # ranks in eights
