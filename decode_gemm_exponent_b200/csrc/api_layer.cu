@@ -65,7 +65,8 @@ uw_status check_expert_plan(const uw_expert_plan *p, const uw_expert_set *w) {
         if (w->table_dev && w->k > 131072) return UW_ERR_UNSUPPORTED_SHAPE;
     } else if (p->kernel == UW_KERNEL_TC) {
         if ((p->bn != 128 && p->bn != 256) || p->width) return UW_ERR_INVALID_ARG;
-        if (p->rows != 32 && p->rows != 64 && p->rows != 128) return UW_ERR_INVALID_ARG;
+        if (p->rows != 32 && p->rows != 64 && p->rows != 128 && p->rows != 256) return UW_ERR_INVALID_ARG;
+        if (p->rows == 256 && p->bn != 256) return UW_ERR_INVALID_ARG;
         // a tensor map's largest stride
         if ((w->w_dev ? w->stride : w->n * w->k) >= int64_t(1) << 39) return UW_ERR_UNSUPPORTED_SHAPE;
     } else {
@@ -96,6 +97,7 @@ uw_status check_expert_call(const uw_expert_rows *r, const uw_expert_set *a, con
     st = check_expert_plan(p, a);
     if (st == UW_OK && b) st = check_expert_plan(p, b);
     if (st != UW_OK) return st;
+    if (!b && p->rows == 256 && r && r->order_dev && !p->sort) return UW_ERR_INVALID_ARG;
     if (!r || r->places < 0 || r->per_row < 1) return UW_ERR_INVALID_ARG;
     if (r->places > kMaxItems || r->x_rows > kMaxItems) return UW_ERR_UNSUPPORTED_SHAPE;
     if (out_stride < a->n || out_stride % out_unit) return UW_ERR_INVALID_ARG;

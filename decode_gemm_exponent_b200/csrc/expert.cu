@@ -326,6 +326,14 @@ __device__ __forceinline__ void tma_gather4(void *dst, const CUtensorMap *map, i
         : "memory");
 }
 
+__device__ __forceinline__ void tma_gather4_pair(void *dst, const CUtensorMap *map, int32_t x, const int32_t (&row)[4], uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, %3, %4, %5, "
+        "%6}], [%7];" ::"r"(smem_addr(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(row[0]), "r"(row[1]), "r"(row[2]), "r"(row[3]), "r"(bar)
+        : "memory");
+}
+
 // Place in the ring and its phase, as counters: a division per K-step (64-bit,
 // in one thread) took as long as the copies it stands between, 0.4 us.
 struct Slot {
@@ -340,6 +348,34 @@ struct Slot {
         }
     }
 };
+
+// By one warp: place[e] = places before expert e, first[e] = sum of tiles(rows) of the
+// experts before it, for e in [0, experts]; offsets are clamped, so that none lead out of
+// bounds.
+template <class F>
+__device__ __forceinline__ void tile_table(const int32_t *offsets, int experts, int most, int32_t *first, int32_t *place, F of) {
+    const int lane = threadIdx.x & 31;
+    int run = 0;
+    for (int e0 = 0; e0 < experts; e0 += 32) {
+        int tiles = 0;
+        if (e0 + lane < experts) {
+            const int lo = min(max(__ldg(offsets + e0 + lane), 0), most);
+            const int hi = min(max(__ldg(offsets + e0 + lane + 1), 0), most);
+            tiles = of(max(hi - lo, 0));
+            place[e0 + lane] = lo;
+            if (e0 + lane + 1 == experts) place[experts] = hi;
+        }
+        int incl = tiles;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int u = __shfl_up_sync(kAll, incl, d);
+            if (lane >= d) incl += u;
+        }
+        if (e0 + lane < experts) first[e0 + lane] = run + incl - tiles;
+        run += __shfl_sync(kAll, incl, 31);
+    }
+    if (lane == 0) first[experts] = run;
+}
 
 // BN: weight rows per tile (gate_up: half of them of G, half of U)
 template <int BN, bool GATED>
@@ -386,28 +422,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         tmem_relinquish();
     }
     pdl_wait();   // offsets, order, x and (a decode's output) the weights are older kernels'
-    if (warp == 2) {
-        int run = 0;
-        for (int e0 = 0; e0 < a.experts; e0 += 32) {
-            int tiles = 0;
-            if (e0 + lane < a.experts) {
-                const int lo = min(max(__ldg(a.offsets + e0 + lane), 0), most);
-                const int hi = min(max(__ldg(a.offsets + e0 + lane + 1), 0), most);
-                tiles = (max(hi - lo, 0) + a.bm - 1) / a.bm;
-                place[e0 + lane] = lo;
-                if (e0 + lane + 1 == a.experts) place[a.experts] = hi;
-            }
-            int incl = tiles;
-#pragma unroll
-            for (int d = 1; d < 32; d <<= 1) {
-                const int u = __shfl_up_sync(kAll, incl, d);
-                if (lane >= d) incl += u;
-            }
-            if (e0 + lane < a.experts) first[e0 + lane] = run + incl - tiles;
-            run += __shfl_sync(kAll, incl, 31);
-        }
-        if (lane == 0) first[a.experts] = run;
-    }
+    if (warp == 2) tile_table(a.offsets, a.experts, most, first, place, [&](int rows) { return (rows + a.bm - 1) / a.bm; });
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -635,6 +650,314 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     }
 }
 
+// ---------------------------------------------------------------- tcgen05, two SMs per tile
+
+// Many rows per expert: weights are the MMA's M (256, 128 of them in each CTA of a
+// pair), the places of a tile its N, which follows the tile's rows in steps of 32: the
+// last tile of an expert costs what its rows cost, not a whole tile.  A pair moves
+// 2 x 32 KB per K-step for 256 x 256 products where two CTAs on tiles of 128 rows x 256
+// weights move 2 x 48 KB, and at 1450 MHz under the power cap such copies cost as much
+// as the products.  A TMEM lane is a weight row: a warp stores 32 neighbouring outputs of
+// one place; gate and up values meet through shared memory, each of the two warps
+// finishing half of the places.
+//
+// Rows of x (gate_up): gathered where they are, four to a copy, so that neither a sorted
+// copy of x (134 MB written and read for 4096 tokens x 8) nor its launch is needed.  One
+// warp issues such a copy in about 80 cycles, so eight warps share them: 4096 tokens 330
+// with sorted rows in 128-row tiles, 310 sorted in pairs, 288 gathered (four warps: 344).
+//
+// An expert's tiles are made about equal and taken in turns.  Measured and not better: one
+// run of neighbouring tiles per pair (x leaves L2 between its uses: twice the time), tiles
+// drawn from a counter, and tiles given to the least loaded pair (the power cap, not the
+// busiest pair, sets the time).
+constexpr int kPairRows = 256;        // places per tile
+constexpr int kGather = 8;            // warps that gather rows of x
+constexpr int kPairW = 128 * kBK * 2, kPairStage = 2 * kPairW;   // weights and places of one CTA
+constexpr int kPairSwap = 4 * 2 * 2 * 8 * 32 * 4;                // gate_up: [pair of warps][buffer][half][place][lane]
+
+struct PairArgs {
+    int experts, ksteps, stages;
+    int64_t places, n;
+    const int32_t *offsets;
+    void *y;
+    int64_t y_stride;
+    uint64_t timeout_ns;
+    uint32_t *status;
+    const int32_t *order;      // gathered rows of x
+    int64_t x_rows;
+    int per_row;
+};
+
+template <bool GATED, bool GATHER>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads + (GATHER ? 32 * kGather : 0), 1)
+    k_expert_pair(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmX32,
+                  const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, const PairArgs a) {
+    constexpr int kCols = GATED ? 128 : 256, kMine = kCols / 2;      // output columns of the pair, of a CTA
+    extern __shared__ uint8_t smem_dyn[];
+    uint8_t *ring = smem_dyn + ((1024u - (smem_addr(smem_dyn) & 1023u)) & 1023u);
+    const int S = a.stages;
+    float *swap = reinterpret_cast<float *>(ring + size_t(S) * kPairStage);
+    uint64_t *full = reinterpret_cast<uint64_t *>(ring + size_t(S) * kPairStage + (GATED ? kPairSwap : 0));
+    uint64_t *empty = full + S, *accf = empty + S, *acce = accf + 2;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(acce + 2);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+    int32_t *first = reinterpret_cast<int32_t *>(tmem_slot + 2);     // [experts + 1] row tiles before each expert
+    int32_t *place = first + a.experts + 1;                          // [experts + 1] places before each expert
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t cta = cluster_rank();
+    const uint64_t T = a.timeout_ns;
+    pdl_trigger();
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < S; s++) {
+            mbar_init(&full[s], 1);        // the first CTA's; both CTAs' copies count on it
+            mbar_init(&empty[s], 1);
+        }
+        for (int b = 0; b < 2; b++) {
+            mbar_init(&accf[b], 1);
+            mbar_init(&acce[b], 16);       // the first CTA's: the epilogue warps of both
+        }
+        *abort_flag = 0;
+        fence_mbar_init();
+        prefetch_tensormap(&tmX);
+        prefetch_tensormap(&tmX32);
+        prefetch_tensormap(&tmA);
+        if (GATED) prefetch_tensormap(&tmB);
+    }
+    if (warp == 1) tmem_alloc_pair(tmem_slot, 512);
+    pdl_wait();
+    if (warp == 2) 
+        tile_table(a.offsets, a.experts, int(a.places), first, place,
+                   [](int rows) { return (rows + kPairRows - 1) / kPairRows; });
+    tc_fence_before();
+    __syncthreads();
+    cluster_arrive();
+    cluster_wait();                        // the other CTA's barriers are ready too
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    const int ntn = int((a.n + kCols - 1) / kCols);
+    const int tiles = first[a.experts] * ntn, step = int(gridDim.x >> 1);        // tiles: below 2^31, checked by the launch
+
+    // row tile mt -> expert (the last one with first[e] <= mt that has tiles), places
+    auto locate = [&](int mt) {
+        int lo = 0, hi = a.experts;          // first[lo] <= mt < first[hi]
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (first[mid] <= mt) lo = mid;
+            else hi = mid;
+        }
+        const int rows = place[lo + 1] - place[lo], count = first[lo + 1] - first[lo];
+        const int size = ((rows + count - 1) / count + 31) / 32 * 32, skip = (mt - first[lo]) * size;
+        return Span{lo, place[lo] + skip, min(size, rows - skip)};
+    };
+
+    // places per CTA of a tile: N is a multiple of 32
+    auto half_of = [](int rows) { return max((rows + 31) / 32 * 16, GATHER ? 32 : 16); };
+
+    // waits for what the last S uses of the ring have still under way on `bar`
+    auto drain = [&](uint64_t *bar, const Slot &r) {
+        for (int s = 0; s < S; s++)
+            if (s < r.at) mbar_wait(&bar[s], r.phase, T);
+            else if (r.wrapped) mbar_wait(&bar[s], r.phase ^ 1u, T);
+    };
+    auto give_up = [&]() {
+        if (!*abort_flag) flag_error(a.status, UW_DEVERR_TIMEOUT);
+        *abort_flag = 1;
+    };
+
+    if (warp == 0 || (warp == 3 && !GATHER)) {
+        // ------------------------------------------------ copies, each CTA its own half:
+        // the weights, and the places (an issue takes about 80 cycles of its thread)
+        if (lane == 0) {
+            Slot r;
+            bool ok = true;
+            for (int tile = blockIdx.x >> 1; tile < tiles && ok; tile += step) {
+                const int mt = tile / ntn, n0 = (tile - mt * ntn) * kCols + int(cta) * kMine;
+                const Span t = locate(mt);
+                const int half = half_of(t.rows);                           // places per CTA
+                const int small = half > 96 ? 0 : (half + 31) / 32;         // boxes of 32 places, or one of 128
+                const uint32_t bytes = kPairW + (GATHER ? half * (kBK * 2) : small ? small * (32 * kBK * 2) : kPairW);
+                const int row = t.pos + int(cta) * half;
+                for (int ks = 0; ks < a.ksteps; ks++, r.next(S)) {
+                    const int s = r.at;
+                    ok = mbar_wait_or_abort(&empty[s], r.phase ^ 1u, T, abort_flag) && !*abort_flag;
+                    if (!ok) break;
+                    uint8_t *st = ring + size_t(s) * kPairStage;
+                    const uint32_t bar = peer_addr(&full[s], 0);
+                    if (warp == 0) {
+                        if (cta == 0) mbar_arrive_expect_tx(&full[s], 2 * bytes);
+                        tma_load_3d_pair(st, &tmA, ks * kBK, n0, t.expert, bar);
+                        if (GATED) tma_load_3d_pair(st + kPairW / 2, &tmB, ks * kBK, n0, t.expert, bar);
+                    } else if (small == 0) {
+                        tma_load_2d_pair(st + kPairW, &tmX, ks * kBK, row, bar);
+                    } else {
+                        for (int i = 0; i < small; i++)
+                            tma_load_2d_pair(st + kPairW + i * (32 * kBK * 2), &tmX32, ks * kBK, row + 32 * i, bar);
+                    }
+                }
+            }
+            if (!ok) give_up();
+            if (cta == 0) drain(full, r);      // all copies of both have landed
+            drain(empty, r);                   // no arrival for this CTA is under way
+        }
+        __syncwarp();
+    } else if (GATHER && warp >= 12) {
+        // ------------------------------------------------ rows of x, gathered, four to a copy.
+        // Every warp has a copy in every K-step (half >= 32): one that had none could be
+        // lapped by the ring and wait for a phase that is over.
+        Slot r;
+        bool ok = true;
+        const int copy = (warp - 12) + lane * kGather;
+        for (int tile = blockIdx.x >> 1; tile < tiles && ok; tile += step) {
+            const Span t = locate(tile / ntn);
+            const int half = half_of(t.rows);
+            const bool mine = 4 * copy < half;
+            int32_t row[4];
+#pragma unroll
+            for (int i = 0; i < 4; i++)
+                row[i] = int32_t(source_row(a.order, a.per_row, a.x_rows, t.pos + min(int(cta) * half + 4 * copy + i, t.rows - 1)));
+            for (int ks = 0; ks < a.ksteps; ks++, r.next(S)) {
+                const int s = r.at;
+                ok = mbar_wait_or_abort(&empty[s], r.phase ^ 1u, T, abort_flag);
+                ok = __all_sync(kAll, ok && !*abort_flag);
+                if (!ok) break;
+                if (mine)
+                    tma_gather4_pair(ring + size_t(s) * kPairStage + kPairW + copy * (4 * kBK * 2), &tmX, ks * kBK, row,
+                                     peer_addr(&full[s], 0));
+            }
+        }
+        if (!ok && lane == 0) give_up();
+        __syncwarp();
+    } else if (warp == 1 && cta == 0) {
+        // ------------------------------------------------ MMA
+        if (lane == 0) {
+            const int chunk = GATED ? a.ksteps : kSumSteps;
+            Slot r;
+            uint32_t acc = 0;
+            bool ok = true;
+            for (int tile = blockIdx.x >> 1; tile < tiles && ok; tile += step) {
+                const Span t = locate(tile / ntn);
+                const uint32_t idesc = idesc_bf16_f32(256, 2 * half_of(t.rows));
+                for (int k0 = 0; k0 < a.ksteps && ok; k0 += chunk, acc++) {
+                    const uint32_t b = acc & 1u;
+                    if (acc >= 2) ok = mbar_wait_or_abort(&acce[b], ((acc >> 1) & 1u) ^ 1u, T, abort_flag);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const int k1 = min(a.ksteps, k0 + chunk);
+                    for (int ks = k0; ks < k1; ks++, r.next(S)) {
+                        const int s = r.at;
+                        ok = mbar_wait_or_abort(&full[s], r.phase, T, abort_flag);
+                        if (!ok) break;
+                        tc_fence_after();
+                        const uint32_t sw = smem_addr(ring + size_t(s) * kPairStage), sx = sw + kPairW;
+#pragma unroll
+                        for (int kk = 0; kk < kBK / 16; kk++)
+                            tc_mma_bf16_pair(tmem + b * 256, smem_desc_k128(sw + 32 * kk), smem_desc_k128(sx + 32 * kk), idesc,
+                                             (ks != k0 || kk) ? 1u : 0u);
+                        tc_commit_pair(&empty[s]);
+                    }
+                    if (ok) tc_commit_pair(&accf[b]);
+                }
+            }
+            if (!ok) {
+                give_up();
+                // what was issued must end before TMEM is freed and shared memory goes away
+                tc_commit_pair(&accf[acc & 1u]);
+                mbar_wait(&accf[acc & 1u], (acc >> 1) & 1u, T);
+            }
+        }
+        __syncwarp();
+    } else if (warp >= 4 && warp < 12) {
+        // ------------------------------------------------ epilogue: lane = weight row
+        const int q = warp & 3, h = (warp - 4) >> 2;       // lanes 32 q ..; half of the tile's places
+        const uint32_t lane_base = tmem + (uint32_t(q * 32) << 16);
+        uint32_t acc = 0;
+        bool ok = true;
+        for (int tile = blockIdx.x >> 1; tile < tiles; tile += step) {
+            const int mt = tile / ntn;
+            const Span t = locate(mt);
+            const int half = half_of(t.rows), c0 = h * half;
+            const int left = min(half, t.rows - c0);        // places of this half
+            if constexpr (GATED) {
+                // the CTA's rows 0..63 are gates, 64..127 the same rows' up values
+                const int me = q >> 1, pair = 2 * h + (q & 1);
+                const int64_t col = int64_t(tile - mt * ntn) * kCols + cta * kMine + (q & 1) * 32 + lane;
+                const uint32_t b = acc & 1u;
+                ok = mbar_wait_or_abort(&accf[b], (acc >> 1) & 1u, T, abort_flag) && !*abort_flag;
+                ok = !named_bar_any(1 + pair, 64, !ok);     // both warps of the pair alike
+                if (!ok) break;
+                tc_fence_after();
+                uint16_t *out = static_cast<uint16_t *>(a.y) + int64_t(t.pos + c0) * a.y_stride + col;
+                float *mine = swap + (pair * 4 + me) * 256 + lane, *other = swap + (pair * 4 + (me ^ 1)) * 256 + lane;
+#pragma unroll 1
+                for (int c = 0; c < half; c += 16) {
+                    uint32_t v[16];
+                    tmem_ld16(lane_base + b * 256 + c0 + c, v);
+                    tmem_ld_wait();
+                    const int buf = (c & 16) * 32;          // two in turn
+#pragma unroll
+                    for (int i = 0; i < 8; i++) mine[buf + i * 32] = __uint_as_float(me ? v[i] : v[8 + i]);
+                    named_bar_sync(1 + pair, 64);
+#pragma unroll
+                    for (int i = 0; i < 8; i++) {
+                        const float o = other[buf + i * 32], w = __uint_as_float(me ? v[8 + i] : v[i]);
+                        const int p = c + 8 * me + i;
+                        if (p < left && col < a.n)
+                            out[p * a.y_stride] = __bfloat16_as_ushort(__float2bfloat16_rn(me ? silu(o) * w : silu(w) * o));
+                    }
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster_relaxed(peer_addr(&acce[b], 0));
+                acc++;
+            } else {
+                float sum[kPairRows / 2];
+#pragma unroll
+                for (int i = 0; i < kPairRows / 2; i++) sum[i] = 0.f;
+                for (int k0 = 0; k0 < a.ksteps; k0 += kSumSteps, acc++) {
+                    const uint32_t b = acc & 1u;
+                    ok = mbar_wait_or_abort(&accf[b], (acc >> 1) & 1u, T, abort_flag) && !*abort_flag;
+                    ok = __all_sync(kAll, ok);
+                    if (!ok) break;
+                    tc_fence_after();
+#pragma unroll
+                    for (int c = 0; c < kPairRows / 2; c += 16) {
+                        if (c >= half) break;
+                        uint32_t v[16];
+                        tmem_ld16(lane_base + b * 256 + c0 + c, v);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int i = 0; i < 16; i++) sum[c + i] += __uint_as_float(v[i]);
+                    }
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_cluster_relaxed(peer_addr(&acce[b], 0));
+                }
+                if (!ok) break;
+                const int64_t col = int64_t(tile - mt * ntn) * kCols + cta * kMine + q * 32 + lane;
+                float *out = static_cast<float *>(a.y) + int64_t(t.pos + c0) * a.y_stride + col;
+                if (col < a.n) {
+#pragma unroll
+                    for (int p = 0; p < kPairRows / 2; p++) {
+                        if (p % 16 == 0 && p >= left) break;
+                        if (p < left) *out = sum[p];
+                        out += a.y_stride;
+                    }
+                }
+            }
+        }
+        if (!ok && lane == 0) give_up();
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_arrive();
+    cluster_wait();                        // neither CTA's memory goes while the other may use it
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc_pair(tmem, 512);
+    }
+}
+
 // ---------------------------------------------------------------- join
 
 struct CombineArgs {
@@ -650,28 +973,58 @@ struct CombineArgs {
     int64_t out_stride;
 };
 
-// One token's columns in 16-byte pieces; the slots in order, so that the sum
-// does not vary.  The bytes of y bound it.
-__global__ void __launch_bounds__(256) k_expert_combine(const CombineArgs a) {
+// One token's columns, two 16-byte pieces per thread; four slots' loads in flight
+// together, added in slot order, so that the sum does not vary.  The bytes of y, base
+// and out bound it.
+constexpr int kCombineThreads = 128, kCombineCols = 8 * kCombineThreads;
+
+__global__ void __launch_bounds__(kCombineThreads) k_expert_combine(const CombineArgs a) {
     pdl_trigger();
     pdl_wait();
     const int64_t t = blockIdx.x;
-    const int64_t c = (int64_t(blockIdx.y) * blockDim.x + threadIdx.x) * 4;
-    if (c >= a.n) return;
-    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (a.base) s = *reinterpret_cast<const float4 *>(a.base + t * a.base_stride + c);
-#pragma unroll 8
-    for (int i = 0; i < a.top_k; i++) {
-        const int32_t p = __ldg(a.slot + t * a.top_k + i);
-        if (p < 0 || p >= a.places) continue;
-        const float w = __ldg(a.weights + t * a.top_k + i);
-        const float4 v = __ldcs(reinterpret_cast<const float4 *>(a.y + int64_t(p) * a.y_stride + c));
-        s.x = fmaf(w, v.x, s.x);
-        s.y = fmaf(w, v.y, s.y);
-        s.z = fmaf(w, v.z, s.z);
-        s.w = fmaf(w, v.w, s.w);
+    const int64_t c0 = int64_t(blockIdx.y) * kCombineCols + threadIdx.x * 4;
+    float4 s[2];
+#pragma unroll
+    for (int h = 0; h < 2; h++) {
+        const int64_t c = c0 + h * (kCombineCols / 2);
+        s[h] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (a.base && c < a.n) s[h] = *reinterpret_cast<const float4 *>(a.base + t * a.base_stride + c);
     }
-    *reinterpret_cast<float4 *>(a.out + t * a.out_stride + c) = s;
+    for (int i0 = 0; i0 < a.top_k; i0 += 4) {
+        int32_t p[4];
+        float w[4];
+        float4 v[4][2];
+#pragma unroll
+        for (int j = 0; j < 4; j++) {
+            const int64_t at = t * a.top_k + min(i0 + j, a.top_k - 1);
+            p[j] = __ldg(a.slot + at);
+            w[j] = __ldg(a.weights + at);
+            if (i0 + j >= a.top_k || p[j] >= a.places) p[j] = -1;
+        }
+#pragma unroll
+        for (int j = 0; j < 4; j++)
+#pragma unroll
+            for (int h = 0; h < 2; h++) {
+                const int64_t c = c0 + h * (kCombineCols / 2);
+                if (p[j] >= 0 && c < a.n) v[j][h] = __ldcs(reinterpret_cast<const float4 *>(a.y + p[j] * a.y_stride + c));
+            }
+#pragma unroll
+        for (int j = 0; j < 4; j++) {
+            if (p[j] < 0) continue;
+#pragma unroll
+            for (int h = 0; h < 2; h++) {
+                s[h].x = fmaf(w[j], v[j][h].x, s[h].x);
+                s[h].y = fmaf(w[j], v[j][h].y, s[h].y);
+                s[h].z = fmaf(w[j], v[j][h].z, s[h].z);
+                s[h].w = fmaf(w[j], v[j][h].w, s[h].w);
+            }
+        }
+    }
+#pragma unroll
+    for (int h = 0; h < 2; h++) {
+        const int64_t c = c0 + h * (kCombineCols / 2);
+        if (c < a.n) *reinterpret_cast<float4 *>(a.out + t * a.out_stride + c) = s[h];
+    }
 }
 
 // ---------------------------------------------------------------- host side
@@ -739,6 +1092,34 @@ cudaError_t launch_tc(const ExpertLaunch &p, cudaStream_t stream) {
     return err != cudaSuccess ? err : cudaGetLastError();
 }
 
+template <bool GATED, bool GATHER>
+cudaError_t launch_pair(const ExpertLaunch &p, cudaStream_t stream) {
+    constexpr int kMaxSmem = 232448;
+    const int tail = 1024 + 64 + 2 * (p.experts + 2) * 4 + (GATED ? kPairSwap : 0);
+    const int stages = std::min(12, (kMaxSmem - tail) / (kPairStage + 16));       // (and two barriers each)
+    const size_t smem = size_t(stages) * (kPairStage + 16) + tail;
+    CUtensorMap mx, mx32, ma, mb;
+    const cuuint64_t xd[2] = {cuuint64_t(p.k), cuuint64_t(p.x_rows)};
+    const cuuint64_t xs[1] = {cuuint64_t(p.x_stride) * 2};
+    const cuuint32_t box[2] = {kBK, GATHER ? 1 : 128}, box32[2] = {kBK, 32};
+    const int rows = GATED ? 64 : 128;
+    if (!make_map(&mx, p.x, 2, xd, xs, box) || !make_map(&mx32, p.x, 2, xd, xs, box32) ||
+        !weight_map(&ma, p.a, p.experts, p.n, p.k, rows))
+        return cudaErrorInvalidValue;
+    mb = ma;
+    if (GATED && !weight_map(&mb, p.b, p.experts, p.n, p.k, rows)) return cudaErrorInvalidValue;
+    static std::atomic<uint64_t> allowed{0};
+    cudaError_t err = allow_smem(k_expert_pair<GATED, GATHER>, kMaxSmem, allowed);
+    if (err != cudaSuccess) return err;
+    PairArgs a{p.experts, int(p.k / kBK), stages, p.places, p.n, p.offsets, p.y, p.y_stride, p.timeout_ns, p.status, p.order, p.x_rows, p.per_row};
+    const int64_t cols = GATED ? 128 : 256;
+    const int64_t tiles = (p.places + (kPairRows - 1) * std::min<int64_t>(p.experts, p.places)) / kPairRows * ((p.n + cols - 1) / cols);
+    if (tiles >= (int64_t(1) << 31) - 4096) return cudaErrorInvalidValue;
+    const unsigned grid = 2 * unsigned(std::min<int64_t>(sm_count() / 2, tiles));
+    err = launch_pdl(true, k_expert_pair<GATED, GATHER>, dim3(grid), dim3(kTcThreads + (GATHER ? 32 * kGather : 0)), smem, stream, mx, mx32, ma, mb, a);
+    return err != cudaSuccess ? err : cudaGetLastError();
+}
+
 template <bool PAL, bool GATED>
 cudaError_t launch_mma(const ExpertLaunch &p, cudaStream_t stream) {
     MmaExpertArgs a{};
@@ -801,8 +1182,9 @@ uw_expert_plan expert_plan(bool plain, bool gated, int experts, int64_t n, int64
     p.kernel = UW_KERNEL_TC;
     const int64_t cols = gated ? 128 : 256;
     p.bn = active * ((n + cols - 1) / cols) < 148 ? 128 : 256;
-    p.rows = places <= 48 * int64_t(experts) ? 64 : 128;
-    p.sort = places > 24 * int64_t(experts);
+    p.rows = places <= 48 * int64_t(experts) ? 64 : places <= 96 * int64_t(experts) ? 128 : 256;
+    if (p.rows == 256) p.bn = 256;
+    p.sort = places > 24 * int64_t(experts) && !(gated && p.rows == 256);
     return p;
 }
 
@@ -893,14 +1275,18 @@ cudaError_t launch_expert(const ExpertLaunch &given, cudaStream_t stream) {
         if (p.a.table) return p.gated ? launch_mma<true, true>(p, stream) : launch_mma<true, false>(p, stream);
         return p.gated ? launch_mma<false, true>(p, stream) : launch_mma<false, false>(p, stream);
     }
+    if (p.bm == kPairRows) {
+        if (p.order) return p.gated ? launch_pair<true, true>(p, stream) : cudaErrorInvalidValue;      // (refused before)
+        return p.gated ? launch_pair<true, false>(p, stream) : launch_pair<false, false>(p, stream);
+    }
     if (p.bn == 128) return p.gated ? launch_tc<128, true>(p, stream) : launch_tc<128, false>(p, stream);
     return p.gated ? launch_tc<256, true>(p, stream) : launch_tc<256, false>(p, stream);
 }
 
 cudaError_t launch_expert_combine(const CombineLaunch &p, cudaStream_t stream) {
     CombineArgs a{p.y, p.y_stride, p.slot, p.weights, p.t, p.t * p.top_k, p.n, p.top_k, p.base, p.base_stride, p.out, p.out_stride};
-    const dim3 grid(unsigned(p.t), unsigned((p.n / 4 + 255) / 256));
-    const cudaError_t err = launch_pdl(true, k_expert_combine, grid, dim3(256), 0, stream, a);
+    const dim3 grid(unsigned(p.t), unsigned((p.n + kCombineCols - 1) / kCombineCols));
+    const cudaError_t err = launch_pdl(true, k_expert_combine, grid, dim3(kCombineThreads), 0, stream, a);
     return err != cudaSuccess ? err : cudaGetLastError();
 }
 

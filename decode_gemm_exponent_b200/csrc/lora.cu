@@ -509,22 +509,13 @@ __global__ void __launch_bounds__(kExpandWarps * 32, C == 4 ? 3 : 4) k_lora_expa
 
 // ---------------------------------------------------------------- few rows: both products in one launch
 
-__device__ __forceinline__ uint32_t cluster_rank() {
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
-__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
-__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
-
 // 16 bytes of another CTA's shared memory, at the address that `p` has in this one
 __device__ __forceinline__ float4 peer_load(const float4 *p, uint32_t cta) {
     float4 v;
-    asm volatile(
-        "{ .reg .b32 q; mapa.shared::cluster.u32 q, %4, %5; ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [q]; }"
-        : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-        : "r"(smem_addr(p)), "r"(cta)
-        : "memory");
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(peer_addr(p, cta))
+                 : "memory");
     return v;
 }
 

@@ -568,9 +568,11 @@ typedef struct uw_expert_plan {
                             tile, 128 or 256 (gate_up: half of each matrix)             */
     int32_t width;       /* MMA: 16 (1) or 32 (2, k a multiple of 128) weights per lane and
                             row per step, 0 = 32 where k allows; TC: must be 0          */
-    int32_t rows;        /* TC: places per tile, 32, 64 or 128; MMA: must be 0          */
+    int32_t rows;        /* TC: places per tile, 32, 64, 128 or (two SMs per tile, bn 256)
+                            256; MMA: must be 0                                         */
     int32_t sort;        /* TC: non-zero = copy the rows of x into expert order first (into
-                            the workspace; no effect without order_dev); MMA: must be 0 */
+                            the workspace; no effect without order_dev); uw_expert_matmul
+                            with 256 places per tile needs that; MMA: must be 0         */
     int64_t timeout_ns;  /* TC: spin-wait limit (0 = 2 s)                               */
 } uw_expert_plan;
 

@@ -49,7 +49,7 @@ def normal(seed, *shape, std=1.0):
 def plans(uw):
     P = uw.make_expert_plan
     return [P(uw.KERNEL_MMA, 4), P(uw.KERNEL_MMA, 1, width=1), P(uw.KERNEL_TC, 128, 128), P(uw.KERNEL_TC, 256, 32),
-            P(uw.KERNEL_TC, 256, 64, sort=1), P(uw.KERNEL_TC, 128, 128, sort=1), None]
+            P(uw.KERNEL_TC, 256, 64, sort=1), P(uw.KERNEL_TC, 128, 128, sort=1), P(uw.KERNEL_TC, 256, 256, sort=1), None]
 
 
 def product(x, w, routing, gather, k_per_chain):
@@ -79,10 +79,10 @@ def check(got, want, bound):
 
 
 SHAPES = [(1, 4, 64, 64, 2), (3, 8, 192, 128, 3), (40, 16, 320, 256, 4), (33, 2, 64, 576, 1), (200, 5, 448, 192, 2),
-          (700, 8, 256, 1024, 2), (300, 130, 64, 128, 8)]
+          (700, 8, 256, 1024, 2), (300, 130, 64, 128, 8), (900, 2, 192, 640, 1), (520, 1, 320, 2112, 1)]
 
 
-@pytest.mark.parametrize("which", range(7))
+@pytest.mark.parametrize("which", range(8))
 @pytest.mark.parametrize("t,e,n,k,top_k", SHAPES)
 def test_matmul(uw, which, t, e, n, k, top_k):
     plan = plans(uw)[which]
@@ -94,7 +94,7 @@ def test_matmul(uw, which, t, e, n, k, top_k):
     check(uw.expert_matmul(xs, w, r, plan=plan), want, bound)
 
 
-@pytest.mark.parametrize("which", range(7))
+@pytest.mark.parametrize("which", range(8))
 @pytest.mark.parametrize("t,e,n,k,top_k", SHAPES)
 def test_gate_up(uw, which, t, e, n, k, top_k):
     plan = plans(uw)[which]
@@ -111,9 +111,42 @@ def test_gate_up(uw, which, t, e, n, k, top_k):
     status = torch.zeros(1, dtype=torch.int32, device="cuda")
     again = uw.expert_gate_up(x.view(torch.int16), w[:, :n], w[:, n:], r, plan=plan, status=status)
     assert torch.equal(again.view(torch.int16), got.view(torch.int16)) and int(status) == 0
+    if plan is not None and plan.rows == 256:             # gathered rows of x: the same products
+        plan = uw.make_expert_plan(uw.KERNEL_TC, 256, 256)
+        again = uw.expert_gate_up(x, w[:, :n], w[:, n:], r, plan=plan, status=status)
+        check(again, want, bound)
+        assert int(status) == 0
 
 
-@pytest.mark.parametrize("which", range(7))
+@pytest.mark.parametrize("k", [64, 832])
+def test_uneven_experts_over_many_tiles(uw, k):
+    """From one row to several tiles per expert, more tiles than SMs, so that every
+    stage and queue of the kernels is used again with another number of rows."""
+    g = torch.Generator().manual_seed(k)
+    counts = torch.cat([torch.randint(1, 40, (60,), generator=g), torch.randint(40, 700, (30,), generator=g)])
+    counts = counts[torch.randperm(90, generator=g)]
+    ids = torch.repeat_interleave(torch.arange(90), counts)
+    ids = ids[torch.randperm(len(ids), generator=g)].int().cuda()[:, None].contiguous()
+    r = uw.group_rows(ids, 90)
+    w, x = normal(1, 90, 2 * 192, k, std=0.05), normal(2, len(ids), k)
+    gate, dg = product(x, w[:, :192], r, True, max(512, k))
+    up, du = product(x, w[:, 192:], r, True, max(512, k))
+    s = gate * torch.sigmoid(gate)
+    want = s * up
+    bound = 1.1 * dg * (up.abs() + du) + s.abs() * du + (8 + 2 * gate.abs()) * U * want.abs()
+    bound = bound + torch.finfo(torch.bfloat16).eps / 2 * (want.abs() + bound) + 1e-38
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    for rows in (64, 256):
+        plan = uw.make_expert_plan(uw.KERNEL_TC, 256, rows)
+        for _ in range(3):
+            check(uw.expert_gate_up(x, w[:, :192], w[:, 192:], r, plan=plan, status=status), want, bound)
+    y, dy = product(x, w, r, True, 512)
+    xs = x[r.order.long()].contiguous()
+    check(uw.expert_matmul(xs, w, r, plan=uw.make_expert_plan(uw.KERNEL_TC, 256, 256), status=status), y, dy)
+    assert int(status) == 0
+
+
+@pytest.mark.parametrize("which", range(8))
 def test_crowded_and_empty_experts_and_dropped_slots(uw, which):
     plan = plans(uw)[which]
     t, e, n, k = 150, 40, 128, 192
@@ -127,7 +160,7 @@ def test_crowded_and_empty_experts_and_dropped_slots(uw, which):
     assert last < 2 * t and bool((y[last:] == 7.0).all())      # rows behind the last expert are left as they were
 
 
-@pytest.mark.parametrize("which", range(7))
+@pytest.mark.parametrize("which", range(8))
 def test_no_slot_has_an_expert_and_no_tokens(uw, which):
     plan = plans(uw)[which]
     r = routed(uw, 20, 6, 2, 3, drop=1.1)
@@ -140,7 +173,7 @@ def test_no_slot_has_an_expert_and_no_tokens(uw, which):
     assert uw.expert_combine(torch.empty(0, 64, device="cuda"), none).shape == (0, 64)
 
 
-@pytest.mark.parametrize("which", [0, 2, 3, 4])
+@pytest.mark.parametrize("which", [0, 2, 3, 4, 6])
 def test_strides_and_guard_rows(uw, which):
     plan = plans(uw)[which]
     t, e, n, k = 90, 3, 128, 128
@@ -278,6 +311,9 @@ def test_refusals(uw):
         with pytest.raises(uw.UwError) as err:
             uw.expert_matmul(x, w, r, gather=True, plan=plan)
         assert err.value.status == uw.ERR_INVALID_ARG
+    with pytest.raises(uw.UwError) as err:     # 256 places per tile take rows in expert order
+        uw.expert_matmul(x, w, r, gather=True, plan=P(uw.KERNEL_TC, 256, 256))
+    assert err.value.status == uw.ERR_INVALID_ARG
     from decode_gemm_exponent_b200 import synth
     mats = [uw.Matrix(uw.encode(synth.weights_bf16(64, 128, 0.02, 0.0, 1.0, seed=i))) for i in range(4)]
     s = uw.ExpertSet(mats)
