@@ -1162,8 +1162,10 @@ cudaError_t launch_mma(const ExpertLaunch &p, cudaStream_t stream) {
 //   but FP32 chains of at most 512 of K.
 //   tcgen05: 256 weight rows per tile (64 tokens: 110 against 116 with 128) unless
 //   that leaves SMs without a tile; 64 places per tile up to 48 rows per expert on
-//   average, then 128 (1024 tokens: 167 / 156); a sorted copy of x pays from 24
-//   rows per expert (256 tokens 131 without, 134 with; 512 tokens 164 / 139).
+//   average (gate_up: 32 up to 16, 256 tokens: 132 / 140), then 128 (1024 tokens:
+//   167 / 156); 256 on pairs of SMs above 128 rows (96 rows: 168 with 128, 170; 256 rows:
+//   330, 290).  A sorted copy of x pays from 24 rows per expert (256 tokens 131 without,
+//   134 with; 512 tokens 164 / 139), but gate_up's pairs gather.
 //   Compressed sets (32 experts of 768 x 2048, gate_up): a pass of the warp-MMA
 //   kernel per 16 rows, until rebuilding the weights once costs less.
 uw_expert_plan expert_plan(bool plain, bool gated, int experts, int64_t n, int64_t k, int64_t places) {
@@ -1182,9 +1184,10 @@ uw_expert_plan expert_plan(bool plain, bool gated, int experts, int64_t n, int64
     p.kernel = UW_KERNEL_TC;
     const int64_t cols = gated ? 128 : 256;
     p.bn = active * ((n + cols - 1) / cols) < 148 ? 128 : 256;
-    p.rows = places <= 48 * int64_t(experts) ? 64 : places <= 96 * int64_t(experts) ? 128 : 256;
+    const int64_t mean = places / experts;      // rows per expert
+    p.rows = gated && mean < 16 ? 32 : mean < 48 ? 64 : mean < 128 ? 128 : 256;
     if (p.rows == 256) p.bn = 256;
-    p.sort = places > 24 * int64_t(experts) && !(gated && p.rows == 256);
+    p.sort = mean >= 24 && !(gated && p.rows == 256);
     return p;
 }
 
