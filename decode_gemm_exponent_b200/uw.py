@@ -14,6 +14,7 @@ import ctypes
 import functools
 import json
 import os
+import struct
 import sys
 from typing import Optional, Sequence
 
@@ -178,16 +179,14 @@ def lib() -> ctypes.CDLL:
         "uw_group_workspace_size": (ctypes.c_int, [I64, I32, I32, ctypes.POINTER(SZ)]),
         "uw_group_rows": (ctypes.c_int, [P, I64, I32, I32, P, P, P, P, SZ, P]),
         "uw_lora_workspace_size": (ctypes.c_int, [I64, ctypes.POINTER(Adapters), ctypes.POINTER(SZ)]),
-        "uw_lora_add": (ctypes.c_int, [P, I64, I64, ctypes.POINTER(Adapters), P, P, P, P, I64, P, I64, P, SZ, P]),
+        "uw_lora_add": (ctypes.c_int, [P, I64, I64, P, P, P, P, P, I64, P, I64, P, SZ, P]),
         "uw_expert_table": (ctypes.c_int, [ctypes.POINTER(ctypes.POINTER(DMat)), I32, P, SZ]),
         "uw_expert_plan_default": (ctypes.c_int, [ctypes.POINTER(ExpertSetArgs), I64, ctypes.c_int,
                                                   ctypes.POINTER(ExpertPlan)]),
-        "uw_expert_workspace_size": (ctypes.c_int, [ctypes.POINTER(ExpertRows), ctypes.POINTER(ExpertSetArgs), ctypes.c_int,
-                                                    ctypes.POINTER(ExpertPlan), ctypes.POINTER(SZ)]),
-        "uw_expert_matmul": (ctypes.c_int, [ctypes.POINTER(ExpertRows), ctypes.POINTER(ExpertSetArgs), P, I64,
-                                            ctypes.POINTER(ExpertPlan), P, SZ, P, P]),
-        "uw_expert_gate_up": (ctypes.c_int, [ctypes.POINTER(ExpertRows), ctypes.POINTER(ExpertSetArgs),
-                                             ctypes.POINTER(ExpertSetArgs), P, I64, ctypes.POINTER(ExpertPlan), P, SZ, P, P]),
+        # rows, sets and adapters as void pointers: a call passes them packed
+        "uw_expert_workspace_size": (ctypes.c_int, [P, P, ctypes.c_int, ctypes.POINTER(ExpertPlan), ctypes.POINTER(SZ)]),
+        "uw_expert_matmul": (ctypes.c_int, [P, P, P, I64, ctypes.POINTER(ExpertPlan), P, SZ, P, P]),
+        "uw_expert_gate_up": (ctypes.c_int, [P, P, P, P, I64, ctypes.POINTER(ExpertPlan), P, SZ, P, P]),
         "uw_expert_combine": (ctypes.c_int, [P, I64, P, P, I64, I32, I64, P, I64, P, I64, P]),
         "uw_sm_split_create": (ctypes.c_int, [ctypes.c_int, ctypes.c_int, ctypes.POINTER(P)]),
         "uw_sm_split_get": (ctypes.c_int, [P, ctypes.POINTER(P), ctypes.POINTER(P), ctypes.POINTER(ctypes.c_int),
@@ -517,20 +516,19 @@ def _enter(t, stream):
     return torch.cuda.stream(stream)
 
 
-def _handle(dev):
-    """The current stream of device `dev`, as the C ABI takes it."""
-    return _torch()._C._cuda_getCurrentRawStream(dev)
-
-
-def _elsewhere(t, stream):
-    """Whether a call on `t` has to switch the device or the stream first."""
-    return stream is not None or t.get_device() != _torch()._C._cuda_getDevice()
+@functools.lru_cache(maxsize=None)
+def _api():
+    """What every call looks up: the current device, a device's current stream as
+    the C ABI takes it, and the accepted types of indices, sums and weights."""
+    torch = _torch()
+    return (torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream, (torch.int32,), (torch.float32,),
+            (torch.bfloat16, torch.int16))
 
 
 def _need(t, name, shape, dtypes, dev, rows=False):
     """Check a tensor argument: shape, type, device index, and contiguity
     (rows=True: only of each row).  Returns its address."""
-    if t.shape == shape and t.dtype in dtypes and t.get_device() == dev:
+    if t.dtype in dtypes and t.shape == shape and t.get_device() == dev:
         if t.is_contiguous() or (rows and t.dim() == 2 and t.stride(1) == 1):
             return t.data_ptr()
         raise ValueError("%s: not contiguous" % name)
@@ -548,17 +546,6 @@ def _workspace(ws, dev):
     if ws.get_device() != dev or not ws.is_contiguous():
         raise ValueError("ws: a contiguous tensor on cuda:%d" % dev)
     return ws.data_ptr(), ws.numel() * ws.element_size()
-
-
-@functools.lru_cache(maxsize=None)
-def _types():
-    torch = _torch()
-    return (torch.int32,), (torch.float32,), (torch.bfloat16, torch.int16)
-
-
-def _stride(t):
-    """Elements between the rows of a [rows, n] tensor (n where there is one row)."""
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
 
 
 class Grouping:
@@ -614,30 +601,31 @@ def route_experts(logits, top_k: int, *, score: str = "softmax", bias=None, n_gr
     """uw_route_experts: logits [t, experts] (float32 or bfloat16; rows may be
     strided) -> Routing.  `out`: a Routing of the same sizes to write into
     (its workspace is kept with it)."""
-    torch = _torch()
-    if _elsewhere(logits, stream):
+    current, handle_of, i32, f32, _ = _api()
+    dev = logits.get_device()
+    if stream is not None or dev != current():
         with _enter(logits, stream):
             return route_experts(logits, top_k, score=score, bias=bias, n_groups=n_groups, top_groups=top_groups,
                                  group_score=group_score, renormalize=renormalize, scale=scale, out=out)
-    i32, f32, _ = _types()
-    if logits.dim() != 2 or logits.dtype not in (torch.float32, torch.bfloat16):
+    torch = _torch()
+    bf16 = logits.dtype == torch.bfloat16
+    if logits.dim() != 2 or not (bf16 or logits.dtype == torch.float32):
         raise ValueError("logits: a [t, experts] tensor of float32 or bfloat16")
     if score not in SCORES or group_score not in GROUP_SCORES:
         raise ValueError("unknown score %r or group score %r" % (score, group_score))
     t, e = logits.shape
-    dev = logits.get_device()
     stride = e
     if not logits.is_contiguous():
         if (e > 1 and logits.stride(1) != 1) or (t > 1 and logits.stride(0) < e):
             raise ValueError("logits: rows must be contiguous and must not overlap")
         stride = logits.stride(0) if t > 1 else e
     fields = (e, top_k, n_groups, top_groups, SCORES[score], GROUP_SCORES[group_score], 1 if renormalize else 0,
-              TYPE_BF16 if logits.dtype == torch.bfloat16 else TYPE_F32, scale)
+              TYPE_BF16 if bf16 else TYPE_F32, scale)
     router, nbytes = _router(t, fields)
     if out is None:
         new = lambda *shape, d=torch.int32: torch.empty(shape, dtype=d, device=logits.device)
         out = Routing(new(t, top_k), new(t, top_k, d=torch.float32), new(e + 1), new(t * top_k), new(t, top_k))
-    handle = _handle(dev)
+    handle = handle_of(dev)
     check(lib().uw_route_experts(logits.data_ptr(), t, stride, None if bias is None else _need(bias, "bias", (e,), f32, dev),
                                  router, _need(out.ids, "out.ids", (t, top_k), i32, dev),
                                  _need(out.weights, "out.weights", (t, top_k), f32, dev),
@@ -651,19 +639,20 @@ def route_experts(logits, top_k: int, *, score: str = "softmax", bias=None, n_gr
 def group_rows(ids, groups: int, out: Optional[Grouping] = None, stream=None) -> Grouping:
     """uw_group_rows: int32 ids [rows] or [rows, per_row] -> Grouping of their
     items by id; ids outside [0, groups) belong to no group."""
-    torch = _torch()
-    if _elsewhere(ids, stream):
+    current, handle_of, i32, _, _ = _api()
+    dev = ids.get_device()
+    if stream is not None or dev != current():
         with _enter(ids, stream):
             return group_rows(ids, groups, out)
-    i32 = _types()[0]
+    torch = _torch()
     if ids.dim() not in (1, 2) or ids.dtype != torch.int32 or not ids.is_contiguous():
         raise ValueError("ids: a contiguous int32 tensor [rows] or [rows, per_row]")
-    rows, per_row, dev = ids.shape[0], ids.shape[1] if ids.dim() == 2 else 1, ids.get_device()
+    rows, per_row = ids.shape[0], ids.shape[1] if ids.dim() == 2 else 1
     nbytes = _group_bytes(rows, per_row, groups)
     if out is None:
         new = lambda *shape: torch.empty(shape, dtype=torch.int32, device=ids.device)
         out = Grouping(new(groups + 1), new(ids.numel()), new(*ids.shape))
-    handle = _handle(dev)
+    handle = handle_of(dev)
     check(lib().uw_group_rows(ids.data_ptr(), rows, per_row, groups,
                               _need(out.offsets, "out.offsets", (groups + 1,), i32, dev),
                               _need(out.order, "out.order", (ids.numel(),), i32, dev),
@@ -687,42 +676,28 @@ class ExpertSet:
             raise ValueError("the experts' matrices are on different devices")
         self.table = torch.from_numpy(host).to(device)
         self.experts, self.n, self.k, self.device = len(mats), mats[0].n, mats[0].k, device
-        self.args = ExpertSetArgs(self.n, self.k, self.experts, None, 0, self.table.data_ptr())
+        self.packed = _SET.pack(self.n, self.k, self.experts, 0, 0, self.table.data_ptr())
 
 
-def _expert_set(w, name, dev) -> ExpertSetArgs:
+# The C structs of a call, packed: a third of the time that a ctypes.Structure takes.
+_SET, _ROWS, _ADAPTERS = (struct.Struct(f) for f in ("@qqiPqP", "@qiPPPqq", "@qqiiPPPP"))
+
+
+def _expert_set(w, name, dev):
+    """(n, k, experts, plain, the packed struct) of an ExpertSet or a BF16 tensor."""
     if isinstance(w, ExpertSet):
         if w.table.get_device() != dev:
             raise ValueError("%s: on %s, expected cuda:%d" % (name, w.device, dev))
-        return w.args
-    if w.dim() != 3 or w.dtype not in _types()[2]:
+        return w.n, w.k, w.experts, False, w.packed
+    if w.dim() != 3 or w.dtype not in _api()[4]:
         raise ValueError("%s: an ExpertSet or BF16 [experts, n, k]" % name)
-    e, n, k = w.shape
     if w.get_device() != dev:
         raise ValueError("%s: on %s, expected cuda:%d" % (name, w.device, dev))
+    e, n, k = w.shape
     step, row, one = w.stride()
     if one != 1 or row != k or (e > 1 and step < n * k):
         raise ValueError("%s: each expert's matrix must be contiguous" % name)
-    return ExpertSetArgs(n, k, e, w.data_ptr(), step if e > 1 else n * k, None)
-
-
-def _expert_rows(x, grouping: Grouping, set_: ExpertSetArgs, gather: bool, dev: int) -> ExpertRows:
-    i32, _, bf16 = _types()
-    places = grouping.order.numel()
-    if x.dim() != 2:
-        raise ValueError("x: [rows, k]")
-    rows, k = x.shape[0], set_.k
-    per_row = 1
-    if gather:
-        if (rows == 0) != (places == 0) or (rows and places % rows):
-            raise ValueError("x: %d rows do not share %d routed slots evenly" % (rows, places))
-        per_row = places // rows if rows else 1
-    elif rows != places:
-        raise ValueError("x: %d rows in expert order, expected %d" % (rows, places))
-    order = _need(grouping.order, "order", (places,), i32, dev)
-    return ExpertRows(places, per_row, _need(grouping.offsets, "offsets", (set_.experts + 1,), i32, dev),
-                      order if gather else None, _need(x, "x", (rows, k), bf16, dev, True), rows,
-                      x.stride(0) if rows > 1 else k)
+    return n, k, e, True, _SET.pack(n, k, e, w.data_ptr(), step if e > 1 else n * k, 0)
 
 
 def make_expert_plan(kernel=KERNEL_TC, bn=256, rows=None, sort=0, width=0, timeout_ns=0) -> ExpertPlan:
@@ -742,44 +717,64 @@ def _default_plan(plain: bool, experts: int, n: int, k: int, places: int, gated:
 
 def expert_plan_default(w, places: int, gated: bool = False) -> ExpertPlan:
     """uw_expert_plan_default for an ExpertSet or a BF16 [experts, n, k] tensor."""
-    a = _expert_set(w, "w", w.device.index if isinstance(w, ExpertSet) else w.get_device())
-    return ExpertPlan.from_buffer_copy(_default_plan(a.w_dev is not None, a.experts, a.n, a.k, places, bool(gated)))
+    n, k, e, plain, _ = _expert_set(w, "w", w.device.index if isinstance(w, ExpertSet) else w.get_device())
+    return ExpertPlan.from_buffer_copy(_default_plan(plain, e, n, k, places, bool(gated)))
 
 
-def _expert_bytes(r: ExpertRows, a: ExpertSetArgs, gated: bool, plan: ExpertPlan) -> int:
+def _expert_bytes(rows: bytes, set_: bytes, gated: bool, plan: ExpertPlan) -> int:
     size = ctypes.c_size_t()
-    check(lib().uw_expert_workspace_size(r, a, int(gated), plan, ctypes.byref(size)), "uw_expert_workspace_size")
+    check(lib().uw_expert_workspace_size(rows, set_, int(gated), plan, ctypes.byref(size)), "uw_expert_workspace_size")
     return int(size.value)
 
 
 def expert_workspace_size(places: int, w, plan: ExpertPlan, gated: bool = False, gather: bool = True) -> int:
     """uw_expert_workspace_size for `places` routed slots."""
-    a = _expert_set(w, "w", w.device.index if isinstance(w, ExpertSet) else w.get_device())
-    return _expert_bytes(ExpertRows(places, 1, None, 1 if gather else None, None, 0, 0), a, gated, plan)
+    set_ = _expert_set(w, "w", w.device.index if isinstance(w, ExpertSet) else w.get_device())[4]
+    return _expert_bytes(_ROWS.pack(places, 1, 0, 1 if gather else 0, 0, 0, 0), set_, gated, plan)
 
 
-def _expert_call(fn, name, x, sets, routing, gather, plan, out, dtypes, status, ws, stream):
-    torch = _torch()
-    if _elsewhere(x, stream):
-        with _enter(x, stream):
-            return _expert_call(fn, name, x, sets, routing, gather, plan, out, dtypes, status, ws, None)
+def _expert_call(x, w, up, grouping, gather, plan, out, status, ws, stream):
+    """expert_matmul (up is None) or expert_gate_up."""
+    current, handle_of, i32, f32, bf16 = _api()
     dev = x.get_device()
-    sets = [_expert_set(w, what, dev) for what, w in sets]
-    a = sets[0]
-    if len(sets) == 2 and (a.n, a.k, a.experts) != (sets[1].n, sets[1].k, sets[1].experts):
-        raise ValueError("gate and up have different sizes")
-    r = _expert_rows(x, routing, a, gather, dev)
-    places, n = r.places, a.n
+    if stream is not None or dev != current():
+        with _enter(x, stream):
+            return _expert_call(x, w, up, grouping, gather, plan, out, status, ws, None)
+    gated = up is not None
+    n, k, e, plain, set_ = _expert_set(w, "gate" if gated else "w", dev)
+    if gated:
+        n2, k2, e2, _, up_set = _expert_set(up, "up", dev)
+        if n2 != n or k2 != k or e2 != e:
+            raise ValueError("gate and up have different sizes")
+    if x.dim() != 2:
+        raise ValueError("x: [rows, k]")
+    order, rows = grouping.order, x.shape[0]
+    places = order.numel()
+    per_row = 1
+    if gather:
+        if (rows == 0) != (places == 0) or (rows and places % rows):
+            raise ValueError("x: %d rows do not share %d routed slots evenly" % (rows, places))
+        per_row = places // rows if rows else 1
+    elif rows != places:
+        raise ValueError("x: %d rows in expert order, expected %d" % (rows, places))
+    order = _need(order, "order", (places,), i32, dev)
+    r = _ROWS.pack(places, per_row, _need(grouping.offsets, "offsets", (e + 1,), i32, dev), order if gather else 0,
+                   _need(x, "x", (rows, k), bf16, dev, True), rows, x.stride(0) if rows > 1 else k)
     if out is None:
-        out = torch.empty(places, n, dtype=dtypes[0], device=x.device)
+        out = _torch().empty(places, n, dtype=bf16[0] if gated else f32[0], device=x.device)
     if status is not None:
-        status = _need(status, "status", status.shape, _types()[0], dev)
+        status = _need(status, "status", status.shape, i32, dev)
     if plan is None:
-        plan = _default_plan(a.w_dev is not None, a.experts, n, a.k, places, len(sets) == 2)
-    if ws is None and plan.kernel == KERNEL_TC and (plan.sort or a.w_dev is None):
-        ws = torch.empty(max(1, _expert_bytes(r, a, len(sets) == 2, plan)), dtype=torch.uint8, device=x.device)
-    check(fn(r, *sets, _need(out, "out", (places, n), dtypes, dev, True), out.stride(0) if places > 1 else n, plan,
-             *_workspace(ws, dev), status, _handle(dev)), name)
+        plan = _default_plan(plain, e, n, k, places, gated)
+    if ws is None and plan.kernel == KERNEL_TC and (plan.sort or not plain):
+        ws = _torch().empty(max(1, _expert_bytes(r, set_, gated, plan)), dtype=_torch().uint8, device=x.device)
+    ws, ws_bytes = _workspace(ws, dev)
+    y, stride = _need(out, "out", (places, n), bf16 if gated else f32, dev, True), out.stride(0) if places > 1 else n
+    if gated:
+        check(lib().uw_expert_gate_up(r, set_, up_set, y, stride, plan, ws, ws_bytes, status, handle_of(dev)),
+              "uw_expert_gate_up")
+    else:
+        check(lib().uw_expert_matmul(r, set_, y, stride, plan, ws, ws_bytes, status, handle_of(dev)), "uw_expert_matmul")
     return out
 
 
@@ -788,38 +783,40 @@ def expert_matmul(x, w, routing: Grouping, *, gather: bool = False, plan: Option
     """uw_expert_matmul: float32 [places, n] in expert order.  w: an ExpertSet or
     BF16 [experts, n, k].  x: rows in expert order, or with gather=True one row
     per token (the routed slots of a token share its row)."""
-    return _expert_call(lib().uw_expert_matmul, "uw_expert_matmul", x, (("w", w),), routing, gather, plan, out, _types()[1],
-                        status, ws, stream)
+    return _expert_call(x, w, None, routing, gather, plan, out, status, ws, stream)
 
 
 def expert_gate_up(x, gate, up, routing: Grouping, *, gather: bool = True, plan: Optional[ExpertPlan] = None, out=None,
                    status=None, ws=None, stream=None):
     """uw_expert_gate_up: bfloat16 [places, n] in expert order, the routed
     experts' silu(gate x) * (up x); gate and up as expert_matmul's w."""
-    return _expert_call(lib().uw_expert_gate_up, "uw_expert_gate_up", x, (("gate", gate), ("up", up)), routing, gather, plan,
-                        out, _types()[2], status, ws, stream)
+    if up is None:
+        raise ValueError("up: an ExpertSet or BF16 [experts, n, k]")
+    return _expert_call(x, gate, up, routing, gather, plan, out, status, ws, stream)
 
 
 def expert_combine(y, routing: Routing, *, base=None, out=None, stream=None):
     """uw_expert_combine: float32 [t, n], each token's weighted sum of its
     slots' rows of y (float32 [places, n] in expert order), plus base."""
-    torch = _torch()
-    if _elsewhere(y, stream):
+    current, handle_of, i32, f32, _ = _api()
+    dev = y.get_device()
+    if stream is not None or dev != current():
         with _enter(y, stream):
             return expert_combine(y, routing, base=base, out=out)
-    i32, f32, _ = _types()
-    t, top_k = routing.slot.shape
+    slot = routing.slot
+    t, top_k = slot.shape
     if y.dim() != 2:
         raise ValueError("y: [places, n]")
-    n, dev = y.shape[1], y.get_device()
+    places, n = t * top_k, y.shape[1]
     if out is None:
-        out = torch.empty(t, n, dtype=torch.float32, device=y.device)
-    check(lib().uw_expert_combine(_need(y, "y", (t * top_k, n), f32, dev, True), _stride(y),
-                                  _need(routing.slot, "slot", (t, top_k), i32, dev),
+        out = _torch().empty(t, n, dtype=f32[0], device=y.device)
+    check(lib().uw_expert_combine(_need(y, "y", (places, n), f32, dev, True), y.stride(0) if places > 1 else n,
+                                  _need(slot, "slot", (t, top_k), i32, dev),
                                   _need(routing.weights, "weights", (t, top_k), f32, dev), t, top_k, n,
                                   None if base is None else _need(base, "base", (t, n), f32, dev, True),
-                                  0 if base is None else _stride(base), _need(out, "out", (t, n), f32, dev, True),
-                                  _stride(out), _handle(dev)), "uw_expert_combine")
+                                  0 if base is None else base.stride(0) if t > 1 else n,
+                                  _need(out, "out", (t, n), f32, dev, True), out.stride(0) if t > 1 else n, handle_of(dev)),
+          "uw_expert_combine")
     return out
 
 
@@ -840,19 +837,20 @@ def lora_add(x, a, b, ids, y, *, ranks=None, scales=None, groups: Optional[Group
     each row's slot (outside: none), or `groups` holds the rows' grouping
     (group_rows(ids, adapters), then ids may be None).  out: where the result
     goes (y itself for an update in place)."""
-    torch = _torch()
-    if _elsewhere(x, stream):
+    current, handle_of, i32, f32, bf16 = _api()
+    dev = x.get_device()
+    if stream is not None or dev != current():
         with _enter(x, stream):
             return lora_add(x, a, b, ids, y, ranks=ranks, scales=scales, groups=groups, out=out, ws=ws)
-    i32, f32, bf16 = _types()
     if x.dim() != 2 or a.dim() != 3 or b.dim() != 3 or y.dim() != 2:
         raise ValueError("x [t, k], a [adapters, max_rank, k], b [adapters, n, max_rank], y [t, n]")
     t, k = x.shape
     count, rank, _ = a.shape
-    n, dev = y.shape[1], x.get_device()
-    d = Adapters(n, k, count, rank, _need(a, "a", (count, rank, k), bf16, dev), _need(b, "b", (count, n, rank), bf16, dev),
-                 None if ranks is None else _need(ranks, "ranks", (count,), i32, dev),
-                 None if scales is None else _need(scales, "scales", (count,), f32, dev))
+    n = y.shape[1]
+    d = _ADAPTERS.pack(n, k, count, rank, _need(a, "a", (count, rank, k), bf16, dev),
+                       _need(b, "b", (count, n, rank), bf16, dev),
+                       0 if ranks is None else _need(ranks, "ranks", (count,), i32, dev),
+                       0 if scales is None else _need(scales, "scales", (count,), f32, dev))
     if groups is None:
         if ids is None:
             raise ValueError("ids or groups must be given")
@@ -862,47 +860,15 @@ def lora_add(x, a, b, ids, y, *, ranks=None, scales=None, groups: Optional[Group
         offsets = _need(groups.offsets, "groups.offsets", (count + 1,), i32, dev)
         order = _need(groups.order, "groups.order", (t,), i32, dev)
     if out is None:
-        out = torch.empty(t, n, dtype=torch.float32, device=x.device)
+        out = _torch().empty(t, n, dtype=f32[0], device=x.device)
     if ws is None:
         nbytes = lora_workspace_size(t, k, n, count, rank)
         if nbytes:
-            ws = torch.empty(nbytes, dtype=torch.uint8, device=x.device)
-    check(lib().uw_lora_add(_need(x, "x", (t, k), bf16, dev, True), _stride(x), t, d, ids, offsets, order,
-                            _need(y, "y", (t, n), f32, dev, True), _stride(y), _need(out, "out", (t, n), f32, dev, True),
-                            _stride(out), *_workspace(ws, dev), _handle(dev)), "uw_lora_add")
+            ws = _torch().empty(nbytes, dtype=_torch().uint8, device=x.device)
+    ws, ws_bytes = _workspace(ws, dev)
+    many = t > 1
+    check(lib().uw_lora_add(_need(x, "x", (t, k), bf16, dev, True), x.stride(0) if many else k, t, d, ids, offsets, order,
+                            _need(y, "y", (t, n), f32, dev, True), y.stride(0) if many else n,
+                            _need(out, "out", (t, n), f32, dev, True), out.stride(0) if many else n, ws, ws_bytes,
+                            handle_of(dev)), "uw_lora_add")
     return out
-
-
-PIPELINE_NAMES = {PIPE_DECODE_GEMM: "decode_gemm", PIPE_DECODE_EXP_FUSED: "decode_exp_fused",
-                  PIPE_TRANSCODE_FUSED: "transcode_fused", PIPE_DIRECT_PALETTE: "direct_palette",
-                  PIPE_HUFFMAN_FUSED: "huffman_fused"}
-KERNEL_NAMES = {KERNEL_FMA: "fma", KERNEL_TC: "tc", KERNEL_MMA: "mma", KERNEL_TC_SK: "tc_sk",
-                KERNEL_MMA_SK: "mma_sk"}
-
-
-def plans_from_json(text: str, ms: Sequence[int]):
-    """Reload a plan file written by uw_plan_autotune (the per-model plan of
-    Unweight page §九): plans[i][j] for matrix i and batch size ms[j].  Raises
-    ValueError when the file lacks a (matrix, m) pair or names an unknown
-    pipeline or kernel."""
-    doc = json.loads(text)
-    pipes = {v: k for k, v in PIPELINE_NAMES.items()}
-    kerns = {v: k for k, v in KERNEL_NAMES.items()}
-    ms = list(ms)
-    n_mats = 1 + max((e["matrix"] for e in doc["plans"]), default=-1)
-    plans = [[None] * len(ms) for _ in range(n_mats)]
-    for e in doc["plans"]:
-        if e["m"] not in ms:
-            continue
-        b = e["best"]
-        if b["pipeline"] not in pipes or b["kernel"] not in kerns:
-            raise ValueError("plan file: unknown pipeline or kernel in %r" % (b,))
-        plans[e["matrix"]][ms.index(e["m"])] = make_plan(pipes[b["pipeline"]], kerns[b["kernel"]], b["bn"],
-                                                         b["split_k"], b.get("stages", 0))
-    missing = [(i, ms[j]) for i in range(n_mats) for j in range(len(ms)) if plans[i][j] is None]
-    if missing:
-        raise ValueError("plan file has no plan for (matrix, m) %s" % missing[:4])
-    return plans
-
-
-lib()   # fail loudly at import when the library is missing

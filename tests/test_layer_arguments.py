@@ -194,3 +194,14 @@ def test_expert_combine(uw):
         assert run(**kw) == uw.ERR_INVALID_ARG, kw
     assert run(n=66, ys=68, os_=68) == uw.ERR_UNSUPPORTED_SHAPE
     assert run(t=1 << 31) == uw.ERR_UNSUPPORTED_SHAPE
+
+
+def test_packed_structs_equal_the_declared_ones(uw):
+    for packed, declared, values in ((uw._SET, uw.ExpertSetArgs, (64, 128, 5, FAKE, 64 * 128, FAKE + 16)),
+                                     (uw._ROWS, uw.ExpertRows, (70, 7, FAKE, FAKE + 4, FAKE + 16, 10, 128)),
+                                     (uw._ADAPTERS, uw.Adapters, (64, 128, 3, 16, FAKE, FAKE + 16, FAKE + 32, FAKE + 48))):
+        s = declared(*values)
+        got = declared.from_buffer_copy(packed.pack(*values))
+        assert packed.size == ctypes.sizeof(declared)
+        for name, _ in declared._fields_:
+            assert getattr(got, name) == getattr(s, name), name
