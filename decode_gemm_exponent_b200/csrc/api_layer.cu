@@ -1,6 +1,7 @@
 // api_layer.cu -- C ABI of the operators around the matmuls (declared in
 // include/uw.h): routing, grouping of rows, expert products, low-rank adapters.
 // Checks of the arguments; the kernels are in route.cu, expert.cu and lora.cu.
+#include <algorithm>
 #include <cmath>
 
 #include "kernels.h"
@@ -251,6 +252,8 @@ extern "C" uw_status uw_lora_add(const uint16_t *x_dev, int64_t x_stride, int64_
     if (x_stride < d.k || x_stride % 8 || y_stride < d.n || y_stride % 4 || out_stride < d.n || out_stride % 4)
         return UW_ERR_INVALID_ARG;
     if (t == 0) return UW_OK;
+    // rows of y and out are found by 32-bit counts of 16 bytes
+    if (t > 1 && std::max(y_stride, out_stride) / 4 >= (int64_t(1) << 32) / t) return UW_ERR_UNSUPPORTED_SHAPE;
     if (!x_dev || !y_dev || !out_dev || !d.a_dev || !d.b_dev) return UW_ERR_INVALID_ARG;
     if (!ids_dev && (!offsets_dev || !order_dev)) return UW_ERR_INVALID_ARG;
     if (!aligned(x_dev, 16) || !aligned(y_dev, 16) || !aligned(out_dev, 16) || !aligned(d.a_dev, 16) ||

@@ -271,6 +271,13 @@ __device__ __forceinline__ void split3(float v, uint32_t (&p)[3]) {
     p[2] = bf16_bits(rest - __uint_as_float(p[1] << 16));
 }
 
+constexpr uint32_t kNone = 0xFFFFFFFFu;
+// where a row of y and of out starts, in 16 bytes (32 bits: checked by the call): a
+// 64-bit product per row and unit cost the loop a tenth of its time
+__device__ __forceinline__ uint2 row_start(const LoraArgs &a, int32_t row) {
+    return row < 0 ? make_uint2(kNone, kNone) : make_uint2(uint32_t(row * a.y_stride / 4), uint32_t(row * a.out_stride / 4));
+}
+
 // One warp's share of the second product: columns n0 + 32 W s for its steps s, of a
 // tile of MT parts of 16 rows, whose loads of B the parts share; C: 16-rank chunks
 // whose B loads are in flight together; W: warps that take neighbouring columns.
@@ -278,7 +285,7 @@ template <int W, int C, int MT>
 struct Expand {
     static constexpr int kStride = W * 32;
     const LoraArgs &a;
-    const int32_t *s_row;      // the tile's rows, -1: none
+    const uint2 *s_at;         // where the tile's rows of y and out start, in 16 bytes; kNone: no row
     const uint4 *s_frag;       // fragments of V: [part][chunk][piece][lane]
     // y on its way, a ring of units (16 rows of 128 bytes): eight lanes copy a row, so
     // that every request is a whole line; the 16-byte pieces of odd rows are swapped
@@ -287,13 +294,14 @@ struct Expand {
     int rank, chunks, steps, parts;
     int64_t n0;
     const uint16_t *pb;
+    float *out0;
     int fetch_part = 0, fetch_slot = 0, left, slot = 0;
-    int64_t fetch_n;
+    const float *fetch_y0;
     uint2 w[C][4];
 
     __device__ __forceinline__ Expand(const LoraArgs &args, const Tile &tile, int tile_rank, int64_t block, uint8_t *ring,
-                                      const uint4 *frag, const int32_t *rows)
-        : a(args), s_row(rows), s_frag(frag), rank(tile_rank) {
+                                      const uint4 *frag, const uint2 *at)
+        : a(args), s_at(at), s_frag(frag), rank(tile_rank) {
         const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
         s_y = ring + warp * kAhead * kUnit;
         chunks = (rank + 15) / 16;
@@ -301,31 +309,36 @@ struct Expand {
         steps = int(max(int64_t(0), min(int64_t(a.steps), (a.n - n0 + kStride - 32) / kStride)));
         parts = (tile.rows + 15) / 16;
         left = steps * parts;
-        fetch_n = n0 + 4 * (lane & 7);
+        fetch_y0 = a.y + n0 + 4 * (lane & 7);
+        out0 = a.out + n0 + 8 * c;
         // column tile q, MMA column j is output column 8 (j / 2) + 2 q + j % 2 of the step's
         // 32: a thread owns eight consecutive columns, a row's four lanes a whole line
         pb = a.b + (int64_t(min(tile.group, a.groups - 1)) * a.n + n0 + 8 * (g >> 1) + (g & 1)) * a.max_rank + 4 * c;
     }
 
-    // B of chunks [j0, j0 + C) for the step at column offset `n`; ranks past the
-    // adapter's are zeroed, whatever its storage holds there
+    // B of chunks [j0, j0 + C) for the step at column offset `n`, as stored: masking it
+    // here would wait for it
     __device__ __forceinline__ void load_b(int64_t n, int j0) {
         const int c = threadIdx.x & 3;
 #pragma unroll
-        for (int j = 0; j < C; j++) {
-            const int r = 16 * (j0 + j) + 4 * c;
+        for (int j = 0; j < C; j++)
 #pragma unroll
             for (int q = 0; q < 4; q++) {
                 w[j][q] = make_uint2(0u, 0u);
-                if (r < rank) {
+                if (16 * (j0 + j) + 4 * c < rank)
                     w[j][q] = __ldg(reinterpret_cast<const uint2 *>(pb + (n + 2 * q) * a.max_rank + 16 * (j0 + j)));
-                    if (r + 4 > rank) {
-                        const int some = rank - r;     // 1, 2 or 3 ranks
-                        if (some < 2) w[j][q].x &= 0xFFFFu;
-                        w[j][q].y = some < 3 ? 0u : w[j][q].y & 0xFFFFu;
-                    }
-                }
             }
+    }
+
+    // ranks past the adapter's (in its last chunk) zeroed, whatever its storage holds there
+    __device__ __forceinline__ void mask_b(uint2 (&b)[4], int j) const {
+        const int left = rank - 16 * j - 4 * int(threadIdx.x & 3);      // ranks that this lane holds
+        if (16 * j + 16 <= rank) return;
+        const uint32_t m0 = left >= 2 ? ~0u : left == 1 ? 0xFFFFu : 0u, m1 = left >= 4 ? ~0u : left == 3 ? 0xFFFFu : 0u;
+#pragma unroll
+        for (int q = 0; q < 4; q++) {
+            b[q].x &= m0;
+            b[q].y &= m1;
         }
     }
 
@@ -336,16 +349,16 @@ struct Expand {
 #pragma unroll
             for (int i = 0; i < 4; i++) {
                 const int row = 4 * i + (lane >> 3);
-                const int32_t r = s_row[16 * fetch_part + row];
-                if (r >= 0)
+                const uint32_t at = s_at[16 * fetch_part + row].x;
+                if (at != kNone)
                     cp_async16(s_y + fetch_slot * kUnit + row * 128 + (((lane & 7) ^ (row & 1)) << 4),
-                               a.y + r * a.y_stride + fetch_n);
+                               fetch_y0 + uint64_t(at) * 4);
             }
             left--;
             fetch_slot = fetch_slot + 1 == kAhead ? 0 : fetch_slot + 1;
             if (++fetch_part == parts) {
                 fetch_part = 0;
-                fetch_n += kStride;
+                fetch_y0 += kStride;
             }
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
@@ -367,14 +380,14 @@ struct Expand {
 #pragma unroll
         for (int h = 0; h < 2; h++) {
             const int row = 8 * h + g;
-            const int32_t r = s_row[16 * part + row];
-            if (r < 0) continue;
+            const uint32_t start = s_at[16 * part + row].y;
+            if (start == kNone) continue;
             const uint8_t *at = s_y + slot * kUnit + row * 128;
             const float4 y0 = *reinterpret_cast<const float4 *>(at + (((2 * c) ^ (row & 1)) << 4));
             const float4 y1 = *reinterpret_cast<const float4 *>(at + (((2 * c + 1) ^ (row & 1)) << 4));
             const float v[8] = {y0.x + d[0][2 * h], y0.y + d[0][2 * h + 1], y0.z + d[1][2 * h], y0.w + d[1][2 * h + 1],
                                 y1.x + d[2][2 * h], y1.y + d[2][2 * h + 1], y1.z + d[3][2 * h], y1.w + d[3][2 * h + 1]};
-            float *o = a.out + r * a.out_stride + n0 + n + 8 * c;
+            float *o = out0 + n + uint64_t(start) * 4;
             if (a.wide) {
                 store32(o, v);
             } else {
@@ -403,9 +416,11 @@ struct Expand {
                 // comes in meanwhile
                 uint2 cur[C][4];
 #pragma unroll
-                for (int j = 0; j < C; j++)
+                for (int j = 0; j < C; j++) {
 #pragma unroll
                     for (int q = 0; q < 4; q++) cur[j][q] = w[j][q];
+                    mask_b(cur[j], j);
+                }
                 if (s + 1 < steps) load_b(n + kStride, 0);
                 for (int part = 0; part < parts; part++) {
                     float d[4][4] = {};
@@ -424,6 +439,7 @@ struct Expand {
 #pragma unroll
                         for (int j = 0; j < C; j++) {
                             if (j0 + j >= chunks) break;
+                            mask_b(w[j], j0 + j);
                             chunk(d, w[j], part, j0 + j);
                         }
                     }
@@ -468,10 +484,14 @@ __global__ void __launch_bounds__(kExpandWarps * 32, C == 4 ? 3 : 4) k_lora_expa
     extern __shared__ uint4 s_dyn[];
     __shared__ Tile s_tile;
     __shared__ int32_t s_row[16 * MT];
+    __shared__ uint2 s_at[16 * MT];
     uint4 *s_frag = s_dyn + kExpandSmem / 16;
     if (threadIdx.x < 32) {
         const Tile f = find_tile(a, 16 * MT, blockIdx.x, a.copy_rest != 0, s_row);
         if (threadIdx.x == 0) s_tile = f;
+        __syncwarp();
+        if (f.group >= 0)
+            for (int i = threadIdx.x; i < 16 * MT; i += 32) s_at[i] = row_start(a, s_row[i]);
     }
     __syncthreads();
     const Tile tile = s_tile;
@@ -480,7 +500,7 @@ __global__ void __launch_bounds__(kExpandWarps * 32, C == 4 ? 3 : 4) k_lora_expa
         pdl_wait();   // no CTA ends before the kernels that this one stands behind
         return;
     }
-    Expand<kExpandWarps, C, MT> e(a, tile, rank, blockIdx.y, reinterpret_cast<uint8_t *>(s_dyn), s_frag, s_row);
+    Expand<kExpandWarps, C, MT> e(a, tile, rank, blockIdx.y, reinterpret_cast<uint8_t *>(s_dyn), s_frag, s_at);
     e.prefetch();
 
     pdl_wait();   // V is the previous kernel's; everything read so far is older
@@ -488,18 +508,24 @@ __global__ void __launch_bounds__(kExpandWarps * 32, C == 4 ? 3 : 4) k_lora_expa
     const float scale = a.scales && rank ? __ldg(a.scales + tile.group) : 1.f;
     for (int u = threadIdx.x; u < e.parts * e.chunks * 32; u += kExpandWarps * 32) {
         const int l = u & 31, j = (u >> 5) % e.chunks, part = (u >> 5) / e.chunks, r = 16 * j + 4 * (l & 3);
-        float4 v[2];
+        float4 v[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
+        const int m = 16 * part + (l >> 2);
+        const float *pv = a.v + int64_t(tile.pos + m) * a.max_rank + r;
+        // the slices in order, four slices' loads together
+        for (int z0 = 0; z0 < a.splits; z0 += 4) {
+            float4 t[4][2];
 #pragma unroll
-        for (int h = 0; h < 2; h++) {
-            const int m = 16 * part + (l >> 2) + 8 * h;
-            v[h] = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (m < tile.rows && r < rank) {
-                const float *pv = a.v + int64_t(tile.pos + m) * a.max_rank + r;
-                v[h] = __ldcg(reinterpret_cast<const float4 *>(pv));
-#pragma unroll 4
-                for (int z = 1; z < a.splits; z++)
-                    add4(v[h], __ldcg(reinterpret_cast<const float4 *>(pv + int64_t(z) * a.t * a.max_rank)));
-            }
+            for (int z = 0; z < 4; z++)
+#pragma unroll
+                for (int h = 0; h < 2; h++) {
+                    t[z][h] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (z0 + z < a.splits && m + 8 * h < tile.rows && r < rank)
+                        t[z][h] = __ldcg(reinterpret_cast<const float4 *>(pv + (int64_t(z0 + z) * a.t + 8 * h) * a.max_rank));
+                }
+#pragma unroll
+            for (int z = 0; z < 4; z++)
+#pragma unroll
+                for (int h = 0; h < 2; h++) add4(v[h], t[z][h]);
         }
         put_fragment(s_frag + (part * e.chunks + j) * 96 + l, v, scale, r, rank);
     }
@@ -529,7 +555,8 @@ template <int C>
 __global__ void __launch_bounds__(kFewWarps * 32, C == 4 ? 1 : 2) k_lora_few(const LoraArgs a) {
     extern __shared__ uint4 s_dyn[];
     __shared__ Tile s_tile;
-    __shared__ int32_t s_row[16];
+    __shared__ int32_t s_row[8];
+    __shared__ uint2 s_at[16];
     __shared__ float s_red[kFewWarps * C * 128];       // C rank tiles of every warp
     uint8_t *ring = reinterpret_cast<uint8_t *>(s_dyn);
     const int width = (a.max_rank + 15) / 16 * 16;
@@ -542,13 +569,14 @@ __global__ void __launch_bounds__(kFewWarps * 32, C == 4 ? 1 : 2) k_lora_few(con
     if (warp == 0) {
         const Tile f = find_tile(a, 8, blockIdx.x / (ctas * uint32_t(a.cols)), a.copy_rest != 0, s_row);
         if (lane == 0) s_tile = f;
-        if (lane >= 8 && lane < 16) s_row[lane] = -1;
+        __syncwarp();
+        if (lane < 16) s_at[lane] = row_start(a, f.group >= 0 && lane < 8 ? s_row[lane] : -1);
     }
     __syncthreads();
     const Tile tile = s_tile;
     const int rank = tile.group < 0 ? 0 : rank_of(a, tile.group);
     if (tile.group < 0 || (rank == 0 && !a.copy_rest)) return;     // the whole cluster alike
-    Expand<kFewWarps, C, 1> e(a, tile, rank, blockIdx.x % (ctas * uint32_t(a.cols)), ring, s_frag, s_row);
+    Expand<kFewWarps, C, 1> e(a, tile, rank, blockIdx.x % (ctas * uint32_t(a.cols)), ring, s_frag, s_at);
 
     if (rank > 0) {
         const int64_t steps = a.k / 64, slices = int64_t(ctas) * kFewWarps, mine = int64_t(cta) * kFewWarps + warp;

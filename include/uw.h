@@ -645,8 +645,8 @@ typedef struct uw_adapters {
  * y_dev, out_dev: float [t, n]; out_dev may be y_dev (then with the same stride:
  * the update is in place and rows without an adapter are not touched) but may not
  * overlap it otherwise, and out may not overlap x.  Strides are elements between rows: x_stride >= k and a
- * multiple of 8, y_stride and out_stride >= n and multiples of 4; x, y and out are
- * 16-byte aligned.
+ * multiple of 8, y_stride and out_stride >= n and multiples of 4, t times either
+ * below 2^34 (64 GB); x, y and out are 16-byte aligned.
  * The rows' adapters are given either by ids_dev (int32[t]; the call groups them
  * itself) or, with ids_dev NULL, by offsets_dev and order_dev as uw_group_rows wrote
  * them for per_row = 1 and groups = count, so that the projections of a step share

@@ -94,6 +94,8 @@ def test_lora(uw):
     for kw in (dict(ws=None), dict(ws=FAKE + 16), dict(nbytes=size.value - 1)):
         assert run(**kw) == uw.ERR_WORKSPACE, kw
     assert run(t=0, x=None, ids=None, y=None, out=None, ws=None, nbytes=0) == uw.UW_OK    # nothing to launch
+    for kw in (dict(ys=1 << 28, os_=1 << 28), dict(os_=1 << 28, out=FAKE << 4), dict(t=4096, ys=1 << 22, os_=1 << 22)):
+        assert run(**kw) == uw.ERR_UNSUPPORTED_SHAPE, kw          # more than 64 GB
 
 
 def test_expert_calls(uw):
