@@ -59,7 +59,7 @@ struct GroupArgs {
     int64_t items;
     int groups;
     int64_t per_block;      // items per block (the same chunks as `counts`)
-    const int32_t *counts;  // [blocks][groups + 1]; null: one block, which counts itself
+    const int32_t *counts;  // [blocks][count_row(groups)]; null: one block, which counts itself
     int blocks;
     int warps;              // warps that rank (groups + 1 counters each)
     int32_t *offsets, *order, *slot;
@@ -75,10 +75,13 @@ struct RouteArgs {
     int32_t *ids;
     float *weights;
     int64_t rows_per_block;
-    int32_t *counts;        // [blocks][experts + 1]; null: one block, which also orders
+    int32_t *counts;        // [blocks][count_row(experts)]; null: one block, which also orders
     int scratch_at, scratch_words;   // per-warp keys in shared memory (with groups): words before, words each
     GroupArgs group;
 };
+
+// a block's counts in memory: one per group and one for no group, in whole 16 bytes
+__host__ __device__ constexpr int count_row(int groups) { return (groups + 4) / 4 * 4; }
 
 __device__ __forceinline__ int group_of(int32_t id, int groups) { return uint32_t(id) < uint32_t(groups) ? id : groups; }
 
@@ -132,25 +135,29 @@ __device__ __forceinline__ void order_block(const GroupArgs &a, int64_t block, i
     __syncthreads();
     // base: where this block's first item of each group goes
     if (a.counts) {
-        // part p of the columns' threads sums blocks p, p + parts, ...
-        const int cols = (g1 + 31) / 32 * 32;
-        const int parts = max(1, int(blockDim.x) / cols);
+        // part p of the threads of four columns sums blocks p, p + parts, ...
+        const int quads = count_row(a.groups) / 4;
+        const int parts = max(1, int(blockDim.x) / quads);
         int32_t *before = cell + a.warps * g1;
         for (int i = threadIdx.x; i < g1; i += blockDim.x) before[i] = 0;
         __syncthreads();
-        for (int c0 = threadIdx.x; c0 < cols * parts; c0 += blockDim.x) {
-            const int c = c0 % cols, p = c0 / cols;
-            if (c < g1) {
-                int32_t sum = 0, bef = 0;
+        for (int c0 = threadIdx.x; c0 < quads * parts; c0 += blockDim.x) {
+            const int c = c0 % quads, p = c0 / quads;
+            int4 sum = make_int4(0, 0, 0, 0), bef = sum;
 #pragma unroll 8
-                for (int b = p; b < a.blocks; b += parts) {
-                    const int32_t v = a.counts[int64_t(b) * g1 + c];
-                    sum += v;
-                    bef += b < block ? v : 0;
-                }
-                atomicAdd(&base[c], sum);
-                atomicAdd(&before[c], bef);
+            for (int b = p; b < a.blocks; b += parts) {
+                const int4 v = *reinterpret_cast<const int4 *>(a.counts + (int64_t(b) * quads + c) * 4);
+                const int m = b < block ? -1 : 0;
+                sum.x += v.x, sum.y += v.y, sum.z += v.z, sum.w += v.w;
+                bef.x += v.x & m, bef.y += v.y & m, bef.z += v.z & m, bef.w += v.w & m;
             }
+            const int s4[4] = {sum.x, sum.y, sum.z, sum.w}, b4[4] = {bef.x, bef.y, bef.z, bef.w};
+#pragma unroll
+            for (int q = 0; q < 4; q++)
+                if (4 * c + q < g1) {
+                    atomicAdd(&base[4 * c + q], s4[q]);
+                    atomicAdd(&before[4 * c + q], b4[q]);
+                }
         }
         __syncthreads();
         if (warp == 0) warp_exclusive_scan(base, g1);
@@ -231,7 +238,7 @@ __global__ void __launch_bounds__(1024) k_group_count(const int32_t *ids, int64_
     for (int64_t i = begin + threadIdx.x; i < end; i += blockDim.x)
         atomicAdd(&smem_route[group_of(ids[i], groups)], 1);
     __syncthreads();
-    for (int i = threadIdx.x; i < g1; i += blockDim.x) counts[int64_t(blockIdx.x) * g1 + i] = smem_route[i];
+    for (int i = threadIdx.x; i < g1; i += blockDim.x) counts[int64_t(blockIdx.x) * count_row(groups) + i] = smem_route[i];
 }
 
 // ---------------------------------------------------------------- keys
@@ -620,7 +627,7 @@ __global__ void __launch_bounds__(route_threads<NV>()) k_route(const __grid_cons
     __syncthreads();
     if (count) {
         for (int i = threadIdx.x; i <= a.experts; i += blockDim.x)
-            a.counts[int64_t(blockIdx.x) * (a.experts + 1) + i] = count[i];
+            a.counts[int64_t(blockIdx.x) * count_row(a.experts) + i] = count[i];
     } else {
         order_block(a.group, 0, smem_route, smem_route + a.experts + 1);
     }
@@ -651,7 +658,7 @@ GroupGeometry group_geometry(int64_t rows, int per_row, int groups) {
     // at least 256 items per block
     g.rows_per_block = std::max<int64_t>(g.rows_per_block, (256 + per_row - 1) / per_row);
     g.blocks = int((rows + g.rows_per_block - 1) / g.rows_per_block);
-    g.bytes = (uint64_t(g.blocks) * uint64_t(groups + 1) * 4 + 255) / 256 * 256;
+    g.bytes = (uint64_t(g.blocks) * uint64_t(count_row(groups)) * 4 + 255) / 256 * 256;
     return g;
 }
 
@@ -663,7 +670,7 @@ GroupGeometry route_geometry(int64_t t, int top_k, int experts) {
     const int64_t most = 148;
     g.rows_per_block = std::max<int64_t>((t + most - 1) / most, 32);
     g.blocks = int((t + g.rows_per_block - 1) / g.rows_per_block);
-    g.bytes = (uint64_t(g.blocks) * uint64_t(experts + 1) * 4 + 255) / 256 * 256;
+    g.bytes = (uint64_t(g.blocks) * uint64_t(count_row(experts)) * 4 + 255) / 256 * 256;
     return g;
 }
 
