@@ -318,13 +318,22 @@ __device__ __forceinline__ bool route_row(const RouteArgs &a, int64_t row, int32
     Key *scratch = static_cast<Key *>(warp_scratch);
     float l[NV];
     float m = -INFINITY;
+    // (what is the same for all of a row's experts is asked outside the loops over them:
+    // a branch per expert was a seventh of the instructions)
+    if (a.bf16) {
+        const uint16_t *at = static_cast<const uint16_t *>(a.logits) + row * a.stride + lane;
+#pragma unroll
+        for (int i = 0; i < NV; i++)
+            l[i] = 32 * i + lane < a.experts ? __uint_as_float(uint32_t(__ldg(at + 32 * i)) << 16) : -INFINITY;
+    } else {
+        const float *at = static_cast<const float *>(a.logits) + row * a.stride + lane;
+#pragma unroll
+        for (int i = 0; i < NV; i++) l[i] = 32 * i + lane < a.experts ? __ldg(at + 32 * i) : -INFINITY;
+    }
 #pragma unroll
     for (int i = 0; i < NV; i++) {
-        const int e = 32 * i + lane;
-        float v = e < a.experts ? load_logit(a, row, e) : -INFINITY;
-        v = v > -INFINITY ? fminf(v, kMaxFloat) : -INFINITY;   // NaN, -inf: not there
-        l[i] = v;
-        m = fmaxf(m, v);
+        l[i] = l[i] > -INFINITY ? fminf(l[i], kMaxFloat) : -INFINITY;   // NaN, -inf: not there
+        m = fmaxf(m, l[i]);
     }
     double sum = 1.0;
     float inv_sum = 1.f;
@@ -349,22 +358,38 @@ __device__ __forceinline__ bool route_row(const RouteArgs &a, int64_t row, int32
         }
     }
     Key key[NV];
+    if (MODE == kLogits || !a.bias) {
 #pragma unroll
-    for (int i = 0; i < NV; i++) {
-        key[i] = 0;
-        if (l[i] >= -kMaxFloat) {
-            if (MODE == kLogits || !a.bias) {
-                if constexpr (MODE == kExact) key[i] = key_of(double(l[i]));
-                else key[i] = key_of(l[i]);
-            } else {
-                const float bias = __ldg(a.bias + 32 * i + lane);      // -inf or NaN: never chosen
-                if constexpr (MODE == kExact) {
-                    const double c = score_of(a, l[i], m, sum) + double(bias);
-                    key[i] = c > -INFINITY ? key_of(c) : 0;
-                } else {
-                    const float c = fast_score(a, l[i], m, inv_sum) + bias;
-                    key[i] = c > -INFINITY ? key_of(c) : 0;
+        for (int i = 0; i < NV; i++) {
+            if constexpr (MODE == kExact) key[i] = l[i] >= -kMaxFloat ? key_of(double(l[i])) : 0;
+            else key[i] = l[i] >= -kMaxFloat ? key_of(l[i]) : 0;
+        }
+    } else {
+        float bias[NV];                  // -inf or NaN: never chosen
+#pragma unroll
+        for (int i = 0; i < NV; i++) bias[i] = 32 * i + lane < a.experts ? __ldg(a.bias + 32 * i + lane) : 0.f;
+        if constexpr (MODE == kExact) {
+#pragma unroll
+            for (int i = 0; i < NV; i++) {
+                key[i] = 0;
+                if (l[i] >= -kMaxFloat) {
+                    const double c = score_of(a, l[i], m, sum) + double(bias[i]);
+                    if (c > -INFINITY) key[i] = key_of(c);
                 }
+            }
+        } else {
+            float c[NV];
+            if (a.softmax) {
+#pragma unroll
+                for (int i = 0; i < NV; i++) c[i] = expf(l[i] - m) * inv_sum;
+            } else {
+#pragma unroll
+                for (int i = 0; i < NV; i++) c[i] = __frcp_rn(1.f + expf(-l[i]));
+            }
+#pragma unroll
+            for (int i = 0; i < NV; i++) {
+                c[i] += bias[i];
+                key[i] = l[i] >= -kMaxFloat && c[i] > -INFINITY ? key_of(c[i]) : 0;
             }
         }
     }
