@@ -819,14 +819,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads + (GATHER
             for (int ks = 0; ks < a.ksteps; ks++, r.next(S)) {
                 const int s = r.at;
                 ok = mbar_wait_or_abort(&empty[s], r.phase ^ 1u, T, abort_flag);
-                ok = __all_sync(kAll, ok && !*abort_flag);
                 if (!ok) break;
                 if (mine)
                     tma_gather4_pair(ring + size_t(s) * kPairStage + kPairW + copy * (4 * kBK * 2), &tmX, ks * kBK, row,
                                      peer_addr(&full[s], 0));
             }
         }
-        if (!ok && lane == 0) give_up();
+        if (!ok) give_up();
         __syncwarp();
     } else if (warp == 1 && cta == 0) {
         // ------------------------------------------------ MMA
@@ -887,7 +886,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads + (GATHER
                 ok = !named_bar_any(1 + pair, 64, !ok);     // both warps of the pair alike
                 if (!ok) break;
                 tc_fence_after();
-                uint16_t *out = static_cast<uint16_t *>(a.y) + int64_t(t.pos + c0) * a.y_stride + col;
+                uint16_t *out = static_cast<uint16_t *>(a.y) + int64_t(t.pos + c0 + 8 * me) * a.y_stride + col;
                 float *mine = swap + (pair * 4 + me) * 256 + lane, *other = swap + (pair * 4 + (me ^ 1)) * 256 + lane;
 #pragma unroll 1
                 for (int c = 0; c < half; c += 16) {
@@ -901,10 +900,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads + (GATHER
 #pragma unroll
                     for (int i = 0; i < 8; i++) {
                         const float o = other[buf + i * 32], w = __uint_as_float(me ? v[8 + i] : v[i]);
-                        const int p = c + 8 * me + i;
-                        if (p < left && col < a.n)
-                            out[p * a.y_stride] = __bfloat16_as_ushort(__float2bfloat16_rn(me ? silu(o) * w : silu(w) * o));
+                        if (c + 8 * me + i < left && col < a.n)
+                            *out = __bfloat16_as_ushort(__float2bfloat16_rn(silu(me ? o : w) * (me ? w : o)));
+                        out += a.y_stride;
                     }
+                    out += 8 * a.y_stride;
                 }
                 tc_fence_before();
                 __syncwarp();
