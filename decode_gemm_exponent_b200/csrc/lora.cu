@@ -478,6 +478,8 @@ __device__ __forceinline__ void add4(float4 &s, const float4 &o) {
     s.w += o.w;
 }
 
+// 4096 rows, 8 slots of rank 32, 14336 columns: 85 us of the call's 109, 5.5 TB/s of y and
+// sum.  More CTAs per SM with fewer registers (5 or 6 instead of 4): 114 and 125.
 template <int C, int MT>
 __global__ void __launch_bounds__(kExpandWarps * 32, C == 4 ? 3 : 4) k_lora_expand(const LoraArgs a) {
     // dynamic shared memory: y on its way, then the fragments of V
