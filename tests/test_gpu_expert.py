@@ -201,10 +201,14 @@ def test_nan_rows_stay_with_their_tokens(uw):
         assert bool(got[at].isnan().all())
         keep = torch.arange(60, device="cuda") != at
         assert torch.equal(got[keep], want[keep])
+    for plan in plans(uw) + [uw.make_expert_plan(uw.KERNEL_TC, 256, 256)]:
+        want = uw.expert_gate_up(x, w, w, r, plan=plan)
+        got = uw.expert_gate_up(bad, w, w, r, plan=plan)
+        assert bool(got[at].isnan().all()) and torch.equal(got[keep], want[keep])
 
 
 @pytest.mark.parametrize("kernel,bn,kw", [(3, 1, dict(width=1)), (3, 4, dict(width=2)), (3, 8, {}), (3, 3, dict(width=1)),
-                                          (2, 128, dict(rows=32)), (2, 256, dict(rows=128, sort=1))])
+                                          (2, 128, dict(rows=32)), (2, 256, dict(rows=128, sort=1)), (2, 256, dict(rows=256, sort=1))])
 @pytest.mark.parametrize("k", [256, 1152])
 def test_compressed_equals_plain_bit_for_bit(uw, kernel, bn, kw, k):
     from decode_gemm_exponent_b200 import synth
@@ -244,7 +248,7 @@ def test_combine(uw, t, top_k, n, based):
         assert torch.equal(uw.expert_combine(y, r, base=place, out=place), got)
 
 
-@pytest.mark.parametrize("t", [1, 6, 500])
+@pytest.mark.parametrize("t", [1, 6, 500, 1500])
 @pytest.mark.parametrize("compressed", [False, True])
 def test_a_layer_from_the_logits_to_the_output(uw, t, compressed):
     """Router, experts and join in one run, captured into a graph and replayed

@@ -40,7 +40,7 @@ def test_route_beyond_32_bits_of_logits(uw):
     assert torch.equal(r.slot.reshape(-1)[r.order.long()], torch.arange(t * top_k, device="cuda", dtype=torch.int32))
 
 
-@pytest.mark.parametrize("kernel,bn,rows", [(2, 256, 128), (2, 128, 64), (3, 4, 0)])
+@pytest.mark.parametrize("kernel,bn,rows", [(2, 256, 128), (2, 128, 64), (2, 256, 256), (3, 4, 0)])
 def test_expert_products_beyond_32_bits_of_outputs(uw, kernel, bn, rows):
     e, n, k = 3, 4096, 64
     t = (1 << 31) // n + 3000
@@ -52,7 +52,7 @@ def test_expert_products_beyond_32_bits_of_outputs(uw, kernel, bn, rows):
     ids = torch.randint(0, e, (t, 1), device="cuda", generator=g).int()
     r = uw.group_rows(ids, e)
     routing = uw.Routing(ids, torch.full((t, 1), 0.5, device="cuda"), r.offsets, r.order, r.slot)
-    y = uw.expert_matmul(x, w, routing, gather=True, plan=uw.make_expert_plan(kernel, bn, rows))
+    y = uw.expert_matmul(x, w, routing, gather=True, plan=uw.make_expert_plan(kernel, bn, rows, sort=int(rows == 256)))
     out = uw.expert_combine(y, routing)
     for i in list(range(0, 40)) + list(range(t - 40, t)):
         want = w[int(ids[i, 0])].double() @ x[i].double()

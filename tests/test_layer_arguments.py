@@ -126,7 +126,7 @@ def test_expert_calls(uw):
     assert run(y=None) == uw.ERR_INVALID_ARG and run(y=FAKE + 8) == uw.ERR_INVALID_ARG
     assert run(ys=60) == uw.ERR_INVALID_ARG and run(ys=66) == uw.ERR_INVALID_ARG
     for plan in (P(uw.KERNEL_MMA, 0), P(uw.KERNEL_MMA, 9), P(uw.KERNEL_MMA, 4, 32), P(uw.KERNEL_MMA, 4, width=3),
-                 P(uw.KERNEL_MMA, 4, sort=1), P(uw.KERNEL_TC, 64), P(uw.KERNEL_TC, 256, 0), P(uw.KERNEL_TC, 256, 256),
+                 P(uw.KERNEL_MMA, 4, sort=1), P(uw.KERNEL_TC, 64), P(uw.KERNEL_TC, 256, 0), P(uw.KERNEL_TC, 256, 256), P(uw.KERNEL_TC, 128, 256), P(uw.KERNEL_TC, 128, 256, sort=1),
                  P(uw.KERNEL_TC, 256, width=1), P(uw.KERNEL_TC_SK, 16), P(uw.KERNEL_MMA, 4, timeout_ns=-1)):
         assert run(plan=plan) == uw.ERR_INVALID_ARG
     assert run(w=wset(k=192, stride=64 * 192), r=rows(xs=192), plan=P(uw.KERNEL_MMA, 4, width=2)) == uw.ERR_INVALID_ARG
