@@ -478,7 +478,7 @@ __device__ __forceinline__ void add4(float4 &s, const float4 &o) {
     s.w += o.w;
 }
 
-// 4096 rows, 8 slots of rank 32, 14336 columns: 85 us of the call's 109, 5.5 TB/s of y and
+// 4096 rows, 8 slots of rank 32, 14336 columns: 84 us of the call's 107, 5.6 TB/s of y and
 // sum.  More CTAs per SM with fewer registers (5 or 6 instead of 4): 114 and 125.
 template <int C, int MT>
 __global__ void __launch_bounds__(kExpandWarps * 32, C == 4 ? 3 : 4) k_lora_expand(const LoraArgs a) {
@@ -760,7 +760,7 @@ cudaError_t launch_lora(const LoraLaunch &p, cudaStream_t stream) {
     // enough steps per warp that the fragments of V are worth their set-up,
     // few enough that all SMs have work and no wave of CTAs is nearly empty
     const int64_t total = geo.expand_tiles * (p.n / 32);
-    a.steps = int(std::max<int64_t>(1, std::min<int64_t>(geo.token_tiles == 4 ? 4 : 16, total / (148 * 12))));
+    a.steps = int(std::max<int64_t>(1, std::min<int64_t>(geo.token_tiles == 4 ? 3 : 16, total / (148 * 12))));
     const int64_t per_cta = int64_t(kExpandWarps) * a.steps * 32;
     const dim3 grid2(unsigned(geo.expand_tiles), unsigned((p.n + per_cta - 1) / per_cta));
     const size_t smem = kExpandSmem + size_t(geo.token_tiles) * rt * 3 * 32 * 16;
