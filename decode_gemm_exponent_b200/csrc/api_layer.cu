@@ -141,7 +141,8 @@ ExpertLaunch expert_launch(const uw_expert_rows *r, const uw_expert_set *a, cons
     if (sorted) l.sorted = static_cast<uint16_t *>(ws);
     if (p->kernel == UW_KERNEL_TC && !a->w_dev)
         l.rebuilt = reinterpret_cast<uint16_t *>(static_cast<uint8_t *>(ws) + sorted);
-    l.timeout_ns = p->timeout_ns > 0 ? uint64_t(p->timeout_ns) : 2000000000ull;
+    // no shorter than what copies on their way need to land when a kernel gives up
+    l.timeout_ns = p->timeout_ns > 0 ? uint64_t(std::max<int64_t>(p->timeout_ns, 1000000)) : 2000000000ull;
     l.status = status;
     return l;
 }

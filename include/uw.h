@@ -573,7 +573,7 @@ typedef struct uw_expert_plan {
     int32_t sort;        /* TC: non-zero = copy the rows of x into expert order first (into
                             the workspace; no effect without order_dev); uw_expert_matmul
                             with 256 places per tile needs that; MMA: must be 0         */
-    int64_t timeout_ns;  /* TC: spin-wait limit (0 = 2 s)                               */
+    int64_t timeout_ns;  /* TC: spin-wait limit (0 = 2 s; at least 1 ms)                */
 } uw_expert_plan;
 
 /* A plan by the rows per expert, places / experts (places: routed slots, t * top_k):

@@ -188,6 +188,17 @@ def test_strides_and_guard_rows(uw, which):
     assert bool(y.isinf().all())
 
 
+@pytest.mark.parametrize("rows", [64, 256])
+def test_a_short_limit_is_long_enough_for_copies_to_land(uw, rows):
+    r = routed(uw, 300, 4, 2, 3)
+    x, w = normal(1, 300, 512), normal(2, 4, 256, 512)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    want = uw.expert_gate_up(x, w[:, :128], w[:, 128:], r, plan=uw.make_expert_plan(uw.KERNEL_TC, 256, rows))
+    got = uw.expert_gate_up(x, w[:, :128], w[:, 128:], r, plan=uw.make_expert_plan(uw.KERNEL_TC, 256, rows, timeout_ns=1),
+                            status=status)
+    assert torch.equal(got.view(torch.int16), want.view(torch.int16)) and int(status) == 0
+
+
 def test_nan_rows_stay_with_their_tokens(uw):
     r = routed(uw, 60, 2, 1, 9)
     w = normal(4, 2, 128, 128)
